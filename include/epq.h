@@ -89,7 +89,8 @@ const char *epq_status_string(epq_status s);
 int epq_last_cuda_error(void);
 
 /* Reads and clears the device-side error record of the current device:
- * 0 = none; otherwise a code naming the pipeline wait that timed out.
+ * 0 = none; 5 = a position of a paged cache had no page (see epq_pages);
+ * otherwise a code naming the pipeline wait that timed out.
  * Synchronizes the device. */
 int epq_device_error(void);
 
@@ -409,6 +410,171 @@ int64_t epq_kv_row_bytes(int head_dim);
 epq_status epq_attention_decode(const float *q, const float *k_new, const float *v_new, void *k_cache,
                                 void *v_cache, int n_heads, int n_kv_heads, int head_dim, int pos, int max_pos,
                                 float scale, float skip_log, float *out, float *scores_out, epq_stream_t stream);
+
+/* ---------------------------------------------------------------- paged cache
+ * A Q8_0 key/value cache in pages that sequences share: the store behind a
+ * speculative step (the verify vectors of [H] "速度上限：带宽 ÷ 权重字节数"
+ * with a cache; rows as in epq_attention_decode).  Position p of sequence s
+ * is row p % page_size of page table[s][p / page_size].
+ *   pool    uint8 [n_layers][n_pages][n_kv_heads][2][page_size][row], row =
+ *           epq_kv_row_bytes(head_dim); of the two planes the first holds keys
+ *   table   int32 [n_seq][max_pages]: page ids, -1 = none; a sequence's pages
+ *           are a prefix of its row
+ *   length  int32 [n_seq]: committed positions
+ *   refs    int32 [n_pages]: how many sequences hold a page (0 = free)
+ *   work    device scratch of epq_pages_work_bytes() bytes, zero-filled before
+ *           its first use; calls that share it must be ordered on one stream
+ * An empty cache has table -1, length 0 and refs 0.  All state lives on the
+ * device, so a whole step can be queued (or captured in a graph) without a
+ * host synchronisation; its calls must be ordered on one stream.
+ * Requirements: n_seq 1..256, page_size 16, 32, 64 or 128, head_dim 128 or
+ * 256, n_kv_heads 1..256, max_pages * page_size <= 2^30 (EPQ_ERR_SHAPE),
+ * 16-byte aligned pointers (EPQ_ERR_ALIGN).  Page ids, lengths and indices
+ * are checked on the device: an entry outside its range counts as missing
+ * and is never followed; a position that has to be read or written but has
+ * no page is left out and recorded (epq_device_error code 5). */
+typedef struct {
+  void *pool;
+  int32_t *table;
+  int32_t *length;
+  int32_t *refs;
+  void *work;
+  int n_layers, n_pages, n_kv_heads, head_dim, page_size, n_seq, max_pages;
+} epq_pages;
+
+/* Bytes of `work` (0 on bad sizes).  Host-only. */
+size_t epq_pages_work_bytes(const epq_pages *pages);
+
+/* epq_pages_truncate: new_length int32 [n_seq]; a negative entry leaves its
+ * sequence alone.  Otherwise length = min(length, new_length) and every page
+ * at or past ceil(length / page_size) is given back (0 frees the sequence).
+ * A page that no sequence holds any more is free; its bytes stay. */
+epq_status epq_pages_truncate(const epq_pages *pages, const int32_t *new_length, epq_stream_t stream);
+
+/* epq_pages_fork: for i < n (1..256) sequence dst[i] becomes a copy of
+ * src[i]: the same committed length and the same pages, shared (nothing is
+ * copied; pages past the committed length are not shared).  status (NULL or
+ * int32 [n]): 0 = done, 1 = refused, nothing changed: an index out of range,
+ * dst[i] not empty, dst[i] named by an earlier entry, or src[i] named as a
+ * destination in the same call. */
+epq_status epq_pages_fork(const epq_pages *pages, const int32_t *src, const int32_t *dst, int n, int32_t *status,
+                          epq_stream_t stream);
+
+/* epq_pages_reserve: makes positions length .. length + extra[s] - 1 of every
+ * sequence writable (extra int32 [n_seq]; <= 0: leave the sequence alone).
+ * Missing pages are taken in the order of (sequence, position), the lowest
+ * free page id first.  A partly filled last page that other sequences hold
+ * too is replaced by a copy of its committed rows in every layer (copy on
+ * write; of the holders in one call the last one left keeps the page).
+ * status (int32 [n_seq]): 0 = done; 1 = not enough free pages (from the first
+ * sequence that does not fit on, every later one with extra > 0 too), 2 =
+ * longer than max_pages; such a sequence is unchanged. */
+epq_status epq_pages_reserve(const epq_pages *pages, const int32_t *extra, int32_t *status, epq_stream_t stream);
+
+/* epq_pages_compact: commits drafted rows.  For i < n_keep[s] the row at
+ * position length + path[s][i] moves to length + i in every layer, then
+ * length += n_keep[s].  path int32 [n_seq][ntok] with rising entries below
+ * ntok (an accepted path of epq_verify_tree; ntok 1..64), n_keep int32
+ * [n_seq] (0..ntok; values outside are clamped).  An entry of path outside
+ * [i, ntok) moves nothing.  The positions must have been reserved. */
+epq_status epq_pages_compact(const epq_pages *pages, const int32_t *path, const int32_t *n_keep, int ntok,
+                             epq_stream_t stream);
+
+/* ---------------------------------------------------------------- tree step
+ * A tree of ntok (1..64) drafted tokens per sequence: token 0 is the last
+ * committed token (the root), parent[i] < i names the token before token i.
+ *
+ * epq_tree_mask: parent int32 [n_seq][ntok] -> mask uint64 [n_seq][ntok]: bit
+ * j of entry i is set when token j is i or an ancestor of i.  A parent
+ * outside [0, i) makes i a root. */
+epq_status epq_tree_mask(const int32_t *parent, int n_seq, int ntok, uint64_t *mask, epq_stream_t stream);
+
+/* Options of epq_attention_tree (all-zero: contiguous tensors, a chain of
+ * ntok tokens in every sequence).
+ *   mask    NULL or uint64 [n_seq][ntok]: token i attends to drafted token j
+ *           when bit j of entry i is set (NULL: j <= i)
+ *   n_tok   NULL or int32 [n_seq]: tokens of each sequence (0..ntok; the
+ *           others are not stored and not attended, their output is 0)
+ *   q_ld, q_seq_ld, kv_ld, kv_seq_ld  floats between tokens / sequences of q
+ *           and of k_new, v_new (0 = contiguous); multiples of 4 */
+typedef struct {
+  const uint64_t *mask;
+  const int32_t *n_tok;
+  int64_t q_ld, q_seq_ld, kv_ld, kv_seq_ld;
+} epq_attention_tree_opts;
+
+/* Workspace bytes of epq_attention_tree (0 on bad sizes).  Host-only. */
+size_t epq_attention_tree_workspace_bytes(const epq_pages *pages, int n_heads, int ntok);
+
+/* epq_attention_tree: attention of drafted tokens over a paged Q8_0 cache.
+ *   q             float32 [n_seq][ntok][n_heads][head_dim]
+ *   k_new, v_new  float32 [n_seq][ntok][n_kv_heads][head_dim]: quantized to
+ *                 Q8_0 (the packer's arithmetic) and stored at positions
+ *                 length + i of their sequence; length itself stays.
+ *   s_ij = scale * q_i . k_j over the cached positions j < length and the
+ *   drafted tokens that the mask names, keys as the cache holds them (the new
+ *   ones after quantization); out_i = sum_j softmax(s_i)_j v_j, 0 for a token
+ *   that sees no position.  Query head h reads key/value head h / (n_heads /
+ *   n_kv_heads).
+ *   out           float32 [n_seq][ntok][n_heads][head_dim]
+ *   ws, ws_bytes  device scratch of epq_attention_tree_workspace_bytes(),
+ *                 16-byte aligned, zero-filled before its first use; calls
+ *                 that share it must be ordered on one stream.
+ * Requirements: ntok 1..64, n_heads a multiple of n_kv_heads, at most 16
+ * heads per key/value head, scale > 0 and finite, finite q.  A drafted key or value
+ * that is not finite reaches only the tokens that attend to it. */
+epq_status epq_attention_tree(const epq_pages *pages, int layer, const float *q, const float *k_new,
+                              const float *v_new, int n_heads, int ntok, float scale,
+                              const epq_attention_tree_opts *opts, float *out, void *ws, size_t ws_bytes,
+                              epq_stream_t stream);
+
+/* Options of epq_verify_tree.
+ *   draft        NULL or float32 [n_seq][ntok][vocab]: row c holds the
+ *                probabilities from which the children of token c were drawn
+ *                (independently of one another).  NULL: the children are given
+ *                (a greedy or top-k draft).
+ *   n_tok        as in epq_attention_tree
+ *   temperature  of the target, > 0; 0 = greedy (the largest logit, ties to
+ *                the lowest index; u and draft are not read)
+ *   ld, draft_ld floats between rows of logits / draft (0 = vocab) */
+typedef struct {
+  const float *draft;
+  const int32_t *n_tok;
+  float temperature;
+  int64_t ld, draft_ld;
+} epq_verify_opts;
+
+/* Workspace bytes of epq_verify_tree (0 on bad sizes).  Host-only. */
+size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab);
+
+/* epq_verify_tree: acceptance of drafted tokens so that the tokens kept are
+ * distributed as the target's.  With w(v) = exp((l_v - max l) / temperature)
+ * over the logits of the current token c (first the root), Z = sum w:
+ *   draft given: r = w, R = Z, S = 0; a child x of c (in index order) is
+ *     accepted when u[x's index] * q(x) * R < r(x), q the draft row of c;
+ *     after a rejection S += R, r(v) = max(w(v) - S q(v), 0), R = sum r (where
+ *     that leaves nothing, S and R stay);
+ *   no draft: accepted when u * R < r(x); a rejected x leaves r (r(x) = 0).
+ * An accepted child becomes c.  When no child is accepted the next token is
+ * the least v with r(0) + ... + r(v) > u[0] * R (where nothing is left, the
+ * largest logit).
+ *   logits      float32 [n_seq][ntok][vocab]; -inf excludes a token, at least
+ *               one per row is finite
+ *   tokens      int32 [n_seq][ntok] (token 0 is not read; an id outside the
+ *               vocabulary is rejected)
+ *   parent, u   int32, float32 [n_seq][ntok]; u in [0, 1)
+ *   path        int32 [n_seq][ntok]: accepted token indices, 0 first, then -1
+ *   n_accept    int32 [n_seq]: entries of path (0 and next_token -1 for a
+ *               sequence of no tokens)
+ *   next_token  int32 [n_seq]
+ *   lse         NULL or float32 [n_seq][ntok]: log sum_v exp(l_v / temperature)
+ *               (greedy: temperature 1), 0 for unused rows
+ * Weights are held to 2^-44 of the largest and summed as integers, so the
+ * result does not depend on the order of summation.  vocab 1..262144. */
+epq_status epq_verify_tree(const float *logits, int64_t vocab, const int32_t *tokens, const int32_t *parent,
+                           const float *u, int n_seq, int ntok, const epq_verify_opts *opts, int32_t *path,
+                           int32_t *n_accept, int32_t *next_token, float *lse, void *ws, size_t ws_bytes,
+                           epq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -65,6 +65,23 @@ class MoeOpts(ctypes.Structure):
                 ("h_out", ctypes.c_void_p), ("stages", ctypes.c_int)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("table", ctypes.c_void_p), ("length", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p), ("work", ctypes.c_void_p), ("n_layers", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_seq", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class AttentionTreeOpts(ctypes.Structure):
+    _fields_ = [("mask", ctypes.c_void_p), ("n_tok", ctypes.c_void_p), ("q_ld", ctypes.c_int64),
+                ("q_seq_ld", ctypes.c_int64), ("kv_ld", ctypes.c_int64), ("kv_seq_ld", ctypes.c_int64)]
+
+
+class VerifyOpts(ctypes.Structure):
+    _fields_ = [("draft", ctypes.c_void_p), ("n_tok", ctypes.c_void_p), ("temperature", ctypes.c_float),
+                ("ld", ctypes.c_int64), ("draft_ld", ctypes.c_int64)]
+
+
 EPQ_MOE_ROUTE, EPQ_MOE_GATE_UP, EPQ_MOE_DOWN = 1, 2, 4
 
 
@@ -107,6 +124,18 @@ def load(path: str | None = None):
                                           ctypes.POINTER(MoeOpts), vp, vp, vp, vp]),
         "epq_kv_row_bytes": (i64, [i32]),
         "epq_attention_decode": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, f32, vp, vp, vp]),
+        "epq_pages_work_bytes": (ctypes.c_size_t, [ctypes.POINTER(Pages)]),
+        "epq_pages_truncate": (i32, [ctypes.POINTER(Pages), vp, vp]),
+        "epq_pages_fork": (i32, [ctypes.POINTER(Pages), vp, vp, i32, vp, vp]),
+        "epq_pages_reserve": (i32, [ctypes.POINTER(Pages), vp, vp, vp]),
+        "epq_pages_compact": (i32, [ctypes.POINTER(Pages), vp, vp, i32, vp]),
+        "epq_tree_mask": (i32, [vp, i32, i32, vp, vp]),
+        "epq_attention_tree_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Pages), i32, i32]),
+        "epq_attention_tree": (i32, [ctypes.POINTER(Pages), i32, vp, vp, vp, i32, i32, f32,
+                                     ctypes.POINTER(AttentionTreeOpts), vp, vp, ctypes.c_size_t, vp]),
+        "epq_verify_tree_workspace_bytes": (ctypes.c_size_t, [i32, i32, i64]),
+        "epq_verify_tree": (i32, [vp, i64, vp, vp, vp, i32, i32, ctypes.POINTER(VerifyOpts), vp, vp, vp, vp, vp,
+                                  ctypes.c_size_t, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -351,3 +380,193 @@ def epq_attention_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(cache.k), _ptr(cache.v), n_heads, cache.n_kv_heads, cache.head_dim,
         int(pos), cache.max_pos, float(scale), float(skip_log), _ptr(out), _ptr(scores_out), _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ paged cache
+def _need(t, name, dtype, shape):
+    """t is a contiguous tensor of this type and shape (None in shape: any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+class PagedKVCache:
+    """Q8_0 key/value cache in pages shared by sequences (epq_pages): pool
+    uint8 [n_layers, n_pages, n_kv_heads, 2, page_size, epq_kv_row_bytes(head_dim)],
+    table int32 [n_seq, max_pages], length int32 [n_seq], refs int32 [n_pages],
+    all on the device.  The positions of a sequence are appended by
+    epq_attention_tree and committed by epq_pages_compact."""
+
+    def __init__(self, n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, n_seq: int, max_pages: int,
+                 page_size: int = 64, device="cuda"):
+        rb = epq_kv_row_bytes(head_dim)
+        if rb < 0:
+            raise ValueError(f"head_dim {head_dim} not supported")
+        i32 = dict(dtype=torch.int32, device=device)
+        self._bind(torch.zeros((n_layers, n_pages, n_kv_heads, 2, page_size, rb), dtype=torch.uint8, device=device),
+                   torch.full((n_seq, max_pages), -1, **i32), torch.zeros(n_seq, **i32), torch.zeros(n_pages, **i32))
+
+    @classmethod
+    def over(cls, pool: torch.Tensor, table: torch.Tensor, length: torch.Tensor, refs: torch.Tensor) -> "PagedKVCache":
+        """A cache over tensors that the caller holds (layouts as above)."""
+        self = cls.__new__(cls)
+        self._bind(pool, table, length, refs)
+        return self
+
+    def _bind(self, pool, table, length, refs):
+        _need(pool, "pool", torch.uint8, (None, None, None, 2, None, None))
+        _need(table, "table", torch.int32, (None, None))
+        _need(length, "length", torch.int32, (table.shape[0],))
+        _need(refs, "refs", torch.int32, (pool.shape[1],))
+        self.n_layers, self.n_pages, self.n_kv_heads, _, self.page_size, rb = pool.shape
+        self.head_dim = rb * 16 // 17
+        if epq_kv_row_bytes(self.head_dim) != rb:
+            raise ValueError(f"rows of {rb} bytes are no cache rows")
+        self.n_seq, self.max_pages = table.shape
+        self.pool, self.table, self.length, self.refs = pool, table, length, refs
+        self._p = Pages(_addr(pool), _addr(table), _addr(length), _addr(refs), None, self.n_layers, self.n_pages,
+                        self.n_kv_heads, self.head_dim, self.page_size, self.n_seq, self.max_pages)
+        n = int(load().epq_pages_work_bytes(ctypes.byref(self._p)))
+        if n == 0:
+            raise ValueError("sizes of the paged cache not supported")
+        self.work = torch.zeros(n, dtype=torch.uint8, device=pool.device)
+        self._p.work = self.work.data_ptr()
+
+    def _ints(self, t, name, n=None):
+        return _need(t, name, torch.int32, (self.n_seq if n is None else n,))
+
+
+def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=None) -> None:
+    """new_length int32 [n_seq] (negative: leave): shorten sequences and give their pages back (0 frees one)."""
+    cache._ints(new_length, "new_length")
+    _check("epq_pages_truncate", load().epq_pages_truncate(ctypes.byref(cache._p), _ptr(new_length), _stream(stream)))
+
+
+def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, status: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """Sequences dst (int32 [n], empty) become copies of src, sharing their pages; no entries: nothing happens."""
+    n = dst.shape[0]
+    cache._ints(src, "src", n), cache._ints(dst, "dst", n)
+    if status is not None:
+        cache._ints(status, "status", n)
+    if n:
+        _check("epq_pages_fork", load().epq_pages_fork(ctypes.byref(cache._p), _ptr(src), _ptr(dst), n, _ptr(status),
+                                                       _stream(stream)))
+
+
+def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Make extra (int32 [n_seq]) more positions of every sequence writable -> status int32 [n_seq]."""
+    cache._ints(extra, "extra")
+    if status is None:
+        status = torch.empty_like(extra)
+    cache._ints(status, "status")
+    _check("epq_pages_reserve", load().epq_pages_reserve(ctypes.byref(cache._p), _ptr(extra), _ptr(status),
+                                                         _stream(stream)))
+    return status
+
+
+def epq_pages_compact(cache: PagedKVCache, path: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
+    """Commit the drafted rows path (int32 [n_seq, ntok], n_keep int32 [n_seq] of them) in every layer."""
+    _need(path, "path", torch.int32, (cache.n_seq, None))
+    cache._ints(n_keep, "n_keep")
+    _check("epq_pages_compact", load().epq_pages_compact(ctypes.byref(cache._p), _ptr(path), _ptr(n_keep),
+                                                         path.shape[1], _stream(stream)))
+
+
+# ------------------------------------------------------------------ tree step
+def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """parent int32 [n_seq, ntok] -> mask int64 [n_seq, ntok] (bit j: token j is i or an ancestor of i)."""
+    _need(parent, "parent", torch.int32, (None, None))
+    if mask is None:
+        mask = torch.empty(parent.shape, dtype=torch.int64, device=parent.device)
+    _need(mask, "mask", torch.int64, parent.shape)
+    _check("epq_tree_mask", load().epq_tree_mask(_ptr(parent), parent.shape[0], parent.shape[1], _ptr(mask),
+                                                 _stream(stream)))
+    return mask
+
+
+def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int) -> torch.Tensor:
+    """A zeroed workspace for epq_attention_tree, to be kept between calls."""
+    n = int(load().epq_attention_tree_workspace_bytes(ctypes.byref(cache._p), n_heads, ntok))
+    if n == 0:
+        raise ValueError("sizes of the tree attention not supported")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.pool.device)
+
+
+def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedKVCache, layer: int,
+                       n_heads: int, scale: float, mask: torch.Tensor | None = None,
+                       n_tok: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [n_seq, ntok, n_heads*D], k_new/v_new [n_seq, ntok, n_kv*D] (float32; views of one wider buffer are
+    read in place) -> out [n_seq, ntok, n_heads*D]; the new rows are stored behind the committed positions."""
+    lib = load()
+    D = cache.head_dim
+    for t, name, n in ((q, "q", n_heads * D), (k_new, "k_new", cache.n_kv_heads * D),
+                       (v_new, "v_new", cache.n_kv_heads * D)):
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != cache.n_seq or t.shape[2] != n or \
+                t.shape[1] != q.shape[1] or t.stride(2) != 1:
+            raise ValueError(f"{name}: expected float32 [{cache.n_seq}, {q.shape[1]}, {n}] with contiguous rows")
+    ntok = q.shape[1]
+    # the stride of a dimension of one entry says nothing
+    ld = lambda t, d: t.stride(d) if t.shape[d] > 1 else 0  # noqa: E731
+    if any(t.shape[d] > 1 and t.stride(d) == 0 for t in (q, k_new, v_new) for d in (0, 1)):
+        raise ValueError("q, k_new and v_new must not be broadcast")
+    if ld(k_new, 0) != ld(v_new, 0) or ld(k_new, 1) != ld(v_new, 1):
+        raise ValueError("k_new and v_new must have the same strides")
+    if mask is not None:
+        _need(mask, "mask", torch.int64, (cache.n_seq, ntok))
+    if n_tok is not None:
+        cache._ints(n_tok, "n_tok")
+    if out is None:
+        out = torch.empty((cache.n_seq, ntok, n_heads * D), dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.float32, (cache.n_seq, ntok, n_heads * D))
+    if workspace is None:
+        workspace = epq_attention_tree_workspace(cache, n_heads, ntok)
+    o = AttentionTreeOpts(_addr(mask), _addr(n_tok), ld(q, 1), ld(q, 0), ld(k_new, 1), ld(k_new, 0))
+    _check("epq_attention_tree", lib.epq_attention_tree(
+        ctypes.byref(cache._p), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new), n_heads, ntok, float(scale),
+        ctypes.byref(o), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out
+
+
+def epq_verify_tree_workspace(logits: torch.Tensor) -> torch.Tensor:
+    """A workspace for epq_verify_tree on logits of this shape."""
+    n = int(load().epq_verify_tree_workspace_bytes(logits.shape[0], logits.shape[1], logits.shape[2]))
+    if n == 0:
+        raise ValueError("sizes of the verification not supported")
+    return torch.zeros(n, dtype=torch.uint8, device=logits.device)
+
+
+def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, u: torch.Tensor | None = None,
+                    draft: torch.Tensor | None = None, n_tok: torch.Tensor | None = None, temperature: float = 1.0,
+                    path: torch.Tensor | None = None, n_accept: torch.Tensor | None = None,
+                    next_token: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """logits float32 [n_seq, ntok, vocab], tokens/parent int32 and u float32 [n_seq, ntok], draft None or float32
+    like logits -> (path int32 [n_seq, ntok], n_accept int32 [n_seq], next_token int32 [n_seq], lse float32
+    [n_seq, ntok])."""
+    lib = load()
+    _need(logits, "logits", torch.float32, (None, None, None))
+    nseq, ntok, vocab = logits.shape
+    _need(tokens, "tokens", torch.int32, (nseq, ntok)), _need(parent, "parent", torch.int32, (nseq, ntok))
+    if u is not None:
+        _need(u, "u", torch.float32, (nseq, ntok))
+    if draft is not None:
+        _need(draft, "draft", torch.float32, logits.shape)
+    if n_tok is not None:
+        _need(n_tok, "n_tok", torch.int32, (nseq,))
+    new = lambda t, name, dt, shape: (torch.empty(shape, dtype=dt, device=logits.device) if t is None  # noqa: E731
+                                      else _need(t, name, dt, shape))
+    path = new(path, "path", torch.int32, (nseq, ntok))
+    n_accept, next_token = new(n_accept, "n_accept", torch.int32, (nseq,)), new(next_token, "next_token", torch.int32, (nseq,))
+    lse = new(lse, "lse", torch.float32, (nseq, ntok))
+    if workspace is None:
+        workspace = epq_verify_tree_workspace(logits)
+    o = VerifyOpts(_addr(draft), _addr(n_tok), float(temperature), 0, 0)
+    _check("epq_verify_tree", lib.epq_verify_tree(
+        _ptr(logits), vocab, _ptr(tokens), _ptr(parent), _ptr(u), nseq, ntok, ctypes.byref(o), _ptr(path),
+        _ptr(n_accept), _ptr(next_token), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return path, n_accept, next_token, lse

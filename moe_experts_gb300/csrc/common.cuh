@@ -26,6 +26,7 @@ enum DeviceError : unsigned {
   DEVERR_EMPTY_WAIT = 2,   // producer waited too long for a free stage
   DEVERR_DRAIN_WAIT = 3,   // copies still in flight at exit
   DEVERR_RED_WAIT = 4,     // waited too long for the cross-warp reduction
+  DEVERR_NO_PAGE = 5,      // a position of a paged cache that has to be read or written has no page
 };
 
 // ------------------------------------------------------------------ PTX wrappers

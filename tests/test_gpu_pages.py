@@ -1,0 +1,180 @@
+"""GPU parity of epq_pages_* against the page-by-page oracle: tables, lengths,
+reference counts and status exactly, and the bytes of every committed row."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree as T
+
+pytestmark = pytest.mark.gpu
+
+
+class Both:
+    """The library's cache and the oracle's, driven together.  Oracle rows are
+    tags; the library's rows are those tags as bytes in every layer, head and
+    plane."""
+
+    def __init__(self, epq, dev, layers=2, n_pages=24, kv=2, D=128, n_seq=4, max_pages=8, P=16):
+        self.epq, self.dev = epq, dev
+        self.c = epq.PagedKVCache(layers, n_pages, kv, D, n_seq, max_pages, P, dev)
+        self.o = T.Pages(n_pages, n_seq, max_pages, P)
+        self.n_seq, self.P, self.tag = n_seq, P, 0
+
+    def i32(self, x):
+        return torch.tensor(x, dtype=torch.int32, device=self.dev)
+
+    def row(self, tag, page_unit):
+        """The bytes of a tagged row in one (layer, head, plane)."""
+        rng = np.random.default_rng(tag * 1000 + page_unit)
+        return rng.integers(0, 256, self.c.pool.shape[-1], dtype=np.uint8)
+
+    def write(self, s, pos):
+        """A new tagged row at a reserved position."""
+        self.tag += 1
+        page, slot = self.o.table[s][pos // self.P], pos % self.P
+        self.o.rows[page, slot] = self.tag
+        L, _, H, _, _, R = self.c.pool.shape
+        b = np.stack([self.row(self.tag, u) for u in range(L * H * 2)]).reshape(L, H, 2, R)
+        self.c.pool[:, page, :, :, slot] = torch.from_numpy(b).to(self.dev)
+
+    def truncate(self, n):
+        self.o.truncate(n)
+        self.epq.epq_pages_truncate(self.c, self.i32(n))
+
+    def fork(self, a, b):
+        st = torch.full((len(a),), -7, dtype=torch.int32, device=self.dev)
+        want = self.o.fork(a, b)
+        self.epq.epq_pages_fork(self.c, self.i32(a), self.i32(b), st)
+        assert st.tolist() == want
+        return want
+
+    def reserve(self, n):
+        want = self.o.reserve(n)
+        assert self.epq.epq_pages_reserve(self.c, self.i32(n)).tolist() == want
+        return want
+
+    def compact(self, path, keep):
+        self.o.compact(path, keep)
+        self.epq.epq_pages_compact(self.c, self.i32(path), self.i32(keep))
+
+    def same(self):
+        torch.cuda.synchronize()
+        table = self.c.table.tolist()
+        assert [[p for p in r if p >= 0] for r in table] == self.o.table
+        assert all(r[len(t):] == [-1] * (len(r) - len(t)) for r, t in zip(table, self.o.table))
+        assert self.c.length.tolist() == self.o.length and self.c.refs.tolist() == self.o.refs
+        pool = self.c.pool.cpu().numpy()
+        L, _, H, _, _, R = pool.shape
+        for s in range(self.n_seq):
+            for pos in range(self.o.length[s]):
+                page, slot = self.o.table[s][pos // self.P], pos % self.P
+                tag = self.o.rows[page, slot]
+                got = pool[:, page, :, :, slot].reshape(L * H * 2, R)
+                for u in (0, L * H * 2 - 1, tag % (L * H * 2)):
+                    assert np.array_equal(got[u], self.row(tag, u)), (s, pos)
+        assert self.epq.epq_device_error() == 0
+
+
+@pytest.mark.parametrize("P, D", [(16, 128), (32, 256), (64, 128), (128, 128)])
+def test_random_calls(epq_lib, cuda_dev, P, D):
+    """Forks, truncations, reservations that fit or do not, and commits."""
+    rnd = random.Random(P + D)
+    n = 13
+    b = Both(epq_lib, cuda_dev, D=D, P=P, n_pages=14, n_seq=4, max_pages=max(3, 96 // P))
+    for step in range(60):
+        op = rnd.randrange(5)
+        if op == 0:
+            k = rnd.randint(1, 3)
+            b.fork([rnd.randint(-1, 4) for _ in range(k)], [rnd.randint(0, 4) for _ in range(k)])
+        elif op == 1:
+            b.truncate([rnd.choice([-1, -1, -1, rnd.randrange(90), 0]) for _ in range(4)])
+        else:
+            extra = [rnd.choice([n, n, 0, -1]) for _ in range(4)]
+            ok = b.reserve(extra)
+            path, keep = [[-1] * n for _ in range(4)], [0] * 4
+            for s in range(4):
+                if extra[s] <= 0 or ok[s] != 0:
+                    continue
+                for i in range(n):
+                    b.write(s, b.o.length[s] + i)
+                p = sorted(rnd.sample(range(n), rnd.randint(0, n)))
+                path[s], keep[s] = p + [-1] * (n - len(p)), len(p)
+            b.compact(path, keep)
+        if step % 6 == 5:
+            b.same()
+    b.same()
+
+
+def test_copy_on_write_rows_and_keeper(epq_lib, cuda_dev):
+    """Three branches of one prompt: the first two copy the partly filled
+    page, the last one keeps it; a full last page is shared for good."""
+    b = Both(epq_lib, cuda_dev)
+    assert b.reserve([21, 0, 0, 0]) == [0, 0, 0, 0]
+    for i in range(21):
+        b.write(0, i)
+    b.compact([list(range(21)), [-1] * 21, [-1] * 21, [-1] * 21], [21, 0, 0, 0])
+    assert b.fork([0, 0], [1, 2]) == [0, 0]
+    b.same()
+    assert b.reserve([3, 3, 3, 0]) == [0, 0, 0, 0]
+    assert b.o.refs[1] == 1 and b.o.table[2][1] == 1 and b.o.refs[0] == 3
+    b.same()
+    b.truncate([16, 0, 0, -1])
+    assert b.fork([0], [3]) == [0]
+    assert b.reserve([1, 0, 0, 1]) == [0, 0, 0, 0]  # 16 positions fill their page: nothing is copied
+    b.same()
+
+
+def test_fork_refusals(epq_lib, cuda_dev):
+    b = Both(epq_lib, cuda_dev)
+    b.reserve([5, 0, 0, 0])
+    for i in range(5):
+        b.write(0, i)
+    b.compact([list(range(5))] + [[-1] * 5] * 3, [5, 0, 0, 0])
+    # the first entry names sequence 0 as a destination, so no entry may read it
+    assert b.fork([0, 0, -1, 0, 0, 1], [0, 4, 2, 1, 1, 3]) == [1, 1, 1, 1, 1, 1]
+    # out of range, done, twice the same, a source that is a destination
+    assert b.fork([0, -1, 0, 0, 1], [4, 2, 1, 1, 3]) == [1, 1, 0, 1, 1]
+    assert b.fork([0, 1], [1, 2]) == [1, 1]
+    b.same()
+
+
+def test_reserve_without_room(epq_lib, cuda_dev):
+    """Pages run out: the first sequence that does not fit and all later ones
+    stay as they are; one longer than its table is refused by itself."""
+    b = Both(epq_lib, cuda_dev, n_pages=5, max_pages=4)
+    assert b.reserve([20, 65, 40, 16]) == [0, 2, 0, 1]
+    b.same()
+    assert b.reserve([0, 1, 0, 0]) == [0, 1, 0, 0]
+    b.truncate([0, -1, -1, -1])
+    assert b.reserve([0, 32, 8, 1]) == [0, 0, 0, 1]
+    b.same()
+
+
+def test_reserve_many_pages(epq_lib, cuda_dev):
+    """Free ids past one scan of the reference counts, and a long reservation."""
+    b = Both(epq_lib, cuda_dev, layers=1, kv=1, n_pages=5000, n_seq=3, max_pages=3000, P=16)
+    assert b.reserve([16 * 2049, 0, 5]) == [0, 0, 0]
+    b.truncate([16 * 7, -1, -1])
+    assert b.reserve([0, 16 * 2900, 16 * 30]) == [0, 0, 0]
+    b.same()
+
+
+def test_bad_state_is_not_followed(epq_lib, cuda_dev):
+    """Page ids, lengths and path entries out of range: nothing is read or
+    written through them, and a drafted row without a page is recorded."""
+    c = epq_lib.PagedKVCache(1, 4, 1, 128, 2, 3, 16, cuda_dev)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    c.table.copy_(i32([[9, -5, 1 << 30], [0, 1, -1]]))
+    c.length.copy_(i32([40, 1 << 30]))
+    c.refs.copy_(i32([1, 1, 0, 0]))
+    before = c.pool.clone()
+    epq_lib.epq_pages_compact(c, i32([[0, 3, 2, 99], [1, 2, 3, -4]]), i32([4, 77]))
+    torch.cuda.synchronize()
+    assert torch.equal(before, c.pool) and c.length.tolist() == [44, 48]
+    assert epq_lib.epq_device_error() == 5
+    assert epq_lib.epq_pages_reserve(c, i32([2, 1])).tolist() == [0, 2]
+    assert c.table.tolist() == [[9, -5, 2], [0, 1, -1]] and c.refs.tolist() == [1, 1, 1, 0]
+    epq_lib.epq_pages_truncate(c, i32([0, 0]))
+    assert c.refs.tolist() == [0, 0, 0, 0] and epq_lib.epq_device_error() == 0

@@ -1,0 +1,148 @@
+"""GPU parity of epq_verify_tree and epq_tree_mask against the float64 oracle:
+paths, counts and next tokens exactly (a wrong side of a comparison needs u
+within about 1e-7 of a threshold), the log sums within their rounding."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree as T
+
+pytestmark = pytest.mark.gpu
+
+
+def _tree(rng, n):
+    return [-1] + [int(rng.integers(max(0, i - 4), i)) for i in range(1, n)]
+
+
+def _case(seed, nseq, ntok, vocab, temperature, draft, noise=0.5, spread=3.0):
+    rng = np.random.default_rng(seed)
+    logits = (spread * rng.standard_normal((nseq, ntok, vocab))).astype(np.float32)
+    parent = np.array([_tree(rng, ntok) for _ in range(nseq)], np.int32)
+    z = logits + noise * rng.standard_normal(logits.shape)
+    q = np.exp((z - z.max(-1, keepdims=True)) / (temperature or 1.0))
+    q = (q / q.sum(-1, keepdims=True)).astype(np.float32)
+    tokens = np.zeros((nseq, ntok), np.int32)
+    for s in range(nseq):
+        for i in range(1, ntok):
+            p = q[s, parent[s, i]].astype(np.float64)
+            tokens[s, i] = rng.choice(vocab, p=p / p.sum())
+    u = rng.random((nseq, ntok)).astype(np.float32)
+    return logits, tokens, parent, np.minimum(u, np.float32(1 - 2.0 ** -24)), q if draft else None
+
+
+def _check(epq, dev, case, temperature, n_tok=None):
+    logits, tokens, parent, u, q = case
+    t = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to(dev)  # noqa: E731
+    nt = None if n_tok is None else torch.tensor(n_tok, dtype=torch.int32, device=dev)
+    ws = epq.epq_verify_tree_workspace(t(logits))
+    got = [x.cpu().numpy() for x in epq.epq_verify_tree(t(logits), t(tokens), t(parent), t(u), draft=t(q), n_tok=nt,
+                                                        temperature=temperature, workspace=ws)]
+    again = [x.cpu().numpy() for x in epq.epq_verify_tree(t(logits), t(tokens), t(parent), t(u), draft=t(q), n_tok=nt,
+                                                          temperature=temperature, workspace=ws)]
+    assert all(np.array_equal(a, b) for a, b in zip(got, again))
+    path, count, nxt, lse = got
+    nseq, ntok, vocab = logits.shape
+    for s in range(nseq):
+        n = ntok if n_tok is None else n_tok[s]
+        if n == 0:
+            assert count[s] == 0 and nxt[s] == -1 and (path[s] == -1).all() and (lse[s] == 0).all()
+            continue
+        wp, wn, wl = T.verify_tree(logits[s, :n], tokens[s, :n], parent[s, :n], u[s, :n], None if q is None else q[s, :n],
+                                   temperature)
+        assert path[s].tolist() == wp + [-1] * (ntok - len(wp)), s
+        assert count[s] == len(wp) and nxt[s] == wn, s
+        # log of a float32 sum of up to vocab terms, each through at most vocab/256 + 32 additions; the argument
+        # (l - max) / T is off by three roundings of its size
+        tol = (vocab / 256 + 64) * 2.0 ** -24 + 4 * 2.0 ** -24 * (np.abs(wl).max() + np.ptp(logits[s]) / (temperature or 1.0))
+        assert np.abs(lse[s, :n] - wl).max() <= tol and (lse[s, n:] == 0).all()
+    return path, count, nxt
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 31, 1000, 4097, 50001, 128256])
+@pytest.mark.parametrize("draft", [False, True])
+def test_sizes(epq_lib, cuda_dev, vocab, draft):
+    nseq, ntok = (3, 9) if vocab <= 5000 else (2, 5)
+    for k, temperature in enumerate((1.0, 0.0, 0.7)):
+        _check(epq_lib, cuda_dev, _case(vocab + k, nseq, ntok, vocab, temperature, draft), temperature)
+
+
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("seed", range(6))
+def test_many_walks(epq_lib, cuda_dev, draft, seed):
+    """Wide trees, both far and near drafts: rejections among siblings, long paths, ends at every depth."""
+    _, count, _ = _check(epq_lib, cuda_dev, _case(seed, 24, 64, 97, 1.3, draft, noise=(0.1, 3.0)[seed % 2]), 1.3)
+    if draft and seed % 2 == 0:  # near drafts: paths of several lengths
+        assert count.max() > 2 and len(set(count.tolist())) > 2
+
+
+@pytest.mark.parametrize("ntok", [1, 2, 64])
+def test_ragged_trees(epq_lib, cuda_dev, ntok):
+    n_tok = [0, 1, ntok, max(1, ntok // 2)]
+    for temperature in (0.0, 1.0):
+        _check(epq_lib, cuda_dev, _case(ntok, 4, ntok, 3001, temperature, True), temperature, n_tok)
+
+
+def test_excluded_tokens_and_ids_out_of_range(epq_lib, cuda_dev):
+    logits, tokens, parent, u, q = _case(11, 4, 8, 600, 1.0, False)
+    logits[:, :, 100:] = -np.inf
+    logits[1, :, :] = -np.inf
+    logits[1, :, 599] = -3.0  # one token left
+    tokens[0, 1:4] = [-1, 600, 2 ** 31 - 1]
+    tokens[2, 1:3] = [250, 599]  # excluded by the target
+    u[3, :] = 0.0
+    _check(epq_lib, cuda_dev, (logits, tokens, parent, u, None), 1.0)
+    _check(epq_lib, cuda_dev, (logits, tokens, parent, u, None), 0.0)
+    u[:] = np.float32(1 - 2.0 ** -24)
+    _check(epq_lib, cuda_dev, (logits, tokens, parent, u, None), 1.0)
+
+
+def test_draft_equal_to_the_target_is_accepted(epq_lib, cuda_dev):
+    """q = p: every first child is accepted; rejected siblings cannot occur on the way."""
+    case = _case(21, 8, 12, 500, 1.0, True, noise=0.0)
+    case[2][:] = np.arange(-1, 11)  # chains
+    case[3][:] = np.minimum(case[3], 0.999)
+    path, count, _ = _check(epq_lib, cuda_dev, case, 1.0)
+    assert (count == 12).all()
+
+
+def test_siblings_drawn_twice(epq_lib, cuda_dev):
+    logits, tokens, parent, u, q = _case(31, 6, 10, 50, 1.0, True, noise=2.0)
+    parent[:, 1:] = 0
+    tokens[:, 5:] = tokens[:, 1:6]
+    _check(epq_lib, cuda_dev, (logits, tokens, parent, u, q), 1.0)
+    _check(epq_lib, cuda_dev, (logits, tokens, parent, u, None), 1.0)
+
+
+def test_row_strides(epq_lib, cuda_dev):
+    """Rows further apart than the vocabulary, through the C entry."""
+    import ctypes
+
+    logits, tokens, parent, u, q = _case(41, 2, 5, 777, 1.0, True)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(cuda_dev)  # noqa: E731
+    wide = torch.full((2, 5, 1001), float("nan"), device=cuda_dev)
+    wide[..., :777] = t(logits)
+    qw = torch.full((2, 5, 801), float("nan"), device=cuda_dev)
+    qw[..., :777] = t(q)
+    ws = torch.zeros(4096, dtype=torch.uint8, device=cuda_dev)
+    path, na, nx = (torch.empty(n, dtype=torch.int32, device=cuda_dev) for n in ((2, 5), (2,), (2,)))
+    tt, tp, tu = t(tokens), t(parent), t(u)
+    lib = epq_lib.load()
+    from moe_experts_gb300 import _lib as L
+    o = L.VerifyOpts(qw.data_ptr(), None, 1.0, 1001, 801)
+    p = lambda x: ctypes.c_void_p(x.data_ptr())  # noqa: E731
+    assert ws.numel() >= lib.epq_verify_tree_workspace_bytes(2, 5, 777)
+    assert lib.epq_verify_tree(p(wide), 777, p(tt), p(tp), p(tu), 2, 5, ctypes.byref(o), p(path), p(na), p(nx), None, p(ws),
+                               ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    for s in range(2):
+        wp, wn, _ = T.verify_tree(logits[s], tokens[s], parent[s], u[s], q[s], 1.0)
+        assert path[s, :len(wp)].tolist() == wp and na[s].item() == len(wp) and nx[s].item() == wn
+
+
+def test_tree_mask(epq_lib, cuda_dev):
+    rng = np.random.default_rng(2)
+    for n in (1, 2, 33, 64):
+        parent = np.array([_tree(rng, n) for _ in range(5)], np.int32)
+        parent[1] = np.arange(-1, n - 1)
+        parent[2, rng.integers(0, n)] = 77
+        got = epq_lib.epq_tree_mask(torch.from_numpy(parent).to(cuda_dev)).cpu().numpy().view(np.uint64)
+        assert [[int(m) for m in r] for r in got] == [T.ancestors(p) for p in parent.tolist()]
