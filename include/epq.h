@@ -518,8 +518,8 @@ size_t epq_attention_tree_workspace_bytes(const epq_pages *pages, int n_heads, i
  *   n_kv_heads).
  *   out           float32 [n_seq][ntok][n_heads][head_dim]
  *   ws, ws_bytes  device scratch of epq_attention_tree_workspace_bytes(),
- *                 16-byte aligned, zero-filled before its first use; calls
- *                 that share it must be ordered on one stream.
+ *                 16-byte aligned, needs no initialisation; calls that share
+ *                 it must be ordered on one stream.
  * Requirements: ntok 1..64, n_heads a multiple of n_kv_heads, at most 16
  * heads per key/value head, scale > 0 and finite, finite q.  A drafted key or value
  * that is not finite reaches only the tokens that attend to it. */

@@ -489,11 +489,11 @@ def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream
 
 
 def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int) -> torch.Tensor:
-    """A zeroed workspace for epq_attention_tree, to be kept between calls."""
+    """A workspace for epq_attention_tree, to be kept between calls."""
     n = int(load().epq_attention_tree_workspace_bytes(ctypes.byref(cache._p), n_heads, ntok))
     if n == 0:
         raise ValueError("sizes of the tree attention not supported")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.pool.device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.pool.device)
 
 
 def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedKVCache, layer: int,
@@ -537,7 +537,7 @@ def epq_verify_tree_workspace(logits: torch.Tensor) -> torch.Tensor:
     n = int(load().epq_verify_tree_workspace_bytes(logits.shape[0], logits.shape[1], logits.shape[2]))
     if n == 0:
         raise ValueError("sizes of the verification not supported")
-    return torch.zeros(n, dtype=torch.uint8, device=logits.device)
+    return torch.empty(n, dtype=torch.uint8, device=logits.device)
 
 
 def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, u: torch.Tensor | None = None,

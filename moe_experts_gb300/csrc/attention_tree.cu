@@ -22,9 +22,8 @@
 //            of the largest, which shows where the larger ones meet a code 0).
 // Work: the tiles of all (sequence, head, row tile) items in a row, cut into
 // equal shares, one per CTA.  A CTA's part of an item that it does not hold
-// whole goes to the workspace (maximum, sum, unnormalised output), and the
-// last CTA of the item to arrive joins the parts in the order of their
-// positions, so the result does not depend on which one that is.
+// whole goes to the workspace (maximum, sum, unnormalised output), and a
+// second launch joins the parts in the order of their positions.
 // A producer warp streams the rows of a tile (contiguous within a page) with
 // bulk copies into a ring of shared-memory stages; the D/32 consumer warps
 // compute the scores of 64 / (D/32) positions each, exchange the weights
@@ -45,6 +44,7 @@ constexpr int kMaxGroupTree = 16;
 constexpr int kTile = 64;        // positions of a tile
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 512;
+constexpr int kJoinThreads = 128;
 
 struct TreeParams {
   PagesView v;
@@ -55,13 +55,17 @@ struct TreeParams {
   int layer, n_heads, group, ntok;
   float scale;
   float *out;
-  unsigned *count;  // workspace: arrivals per item
   float *parts;     // workspace: [2 per CTA][rows][D + 2]
   unsigned *err;
 };
 
 __device__ __forceinline__ int tree_size(const TreeParams &p, int s) {
   return p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
+}
+
+// Tiles of one row tile of a sequence with n tokens.
+__device__ __forceinline__ int sequence_tiles(const TreeParams &p, int s, int n) {
+  return n ? (seq_length(p.v, s) + n + kTile - 1) / kTile : 0;
 }
 
 __device__ __forceinline__ uint64_t token_mask(const TreeParams &p, int s, int i, int n) {
@@ -137,7 +141,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
 
 // What a work item is: rows [16 MT rt, ...) of head h of sequence s.
 struct Item {
-  int s, h, rt, tiles, len, n, index;
+  int s, h, rt, tiles, len, n;
 };
 
 template <int NB, int MT>
@@ -161,12 +165,11 @@ struct Plan {
   static constexpr uint32_t oTiles = oScale + 4u * kRows;              // [n_seq + 1] tiles before a sequence
   static constexpr uint32_t oBar = oTiles + 8u * (kMaxSeq + 8);        // full, empty
   static constexpr uint32_t oMiss = oBar + 16u * kStages;              // [stages] missing pieces
-  static constexpr uint32_t oFlag = oMiss + 4u * kStages + 4u;
-  static constexpr uint32_t kSmem = oFlag + 16u;
+  static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
 
 template <int NB, int MT>
-__global__ void __launch_bounds__(Plan<NB, MT>::kThreads) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3 : 2) : 1) tree_kernel(const __grid_constant__ TreeParams p) {
   using L = Plan<NB, MT>;
   constexpr int kRows = L::kRows, kD = L::kD, kRow = L::kRow, kNT = L::kNT;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -176,7 +179,6 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads) tree_kernel(const __gr
   uint64_t *empty = full + kStages;
   long long *before = reinterpret_cast<long long *>(smem + L::oTiles);
   unsigned *miss = reinterpret_cast<unsigned *>(smem + L::oMiss);
-  int *flag = reinterpret_cast<int *>(smem + L::oFlag);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads) tree_kernel(const __gr
   auto rows_tiles = [&](int s, int *nrt) {
     const int n = tree_size(p, s);
     *nrt = (n * p.group + kRows - 1) / kRows;
-    return n ? (seq_length(p.v, s) + n + kTile - 1) / kTile : 0;
+    return sequence_tiles(p, s, n);
   };
   for (int s = tid; s < p.v.n_seq; s += L::kThreads) {
     int nrt;
@@ -241,8 +243,6 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads) tree_kernel(const __gr
     const int k = static_cast<int>(rel / it.tiles);
     it.h = k / nrt;
     it.rt = k % nrt;
-    const int max_rt = (p.ntok * p.group + kRows - 1) / kRows;
-    it.index = (lo * p.v.n_kv + it.h) * max_rt + it.rt;
     return static_cast<int>(rel % it.tiles);
   };
   const int piece_rows = min(p.v.P, kTile);
@@ -625,52 +625,81 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads) tree_kernel(const __gr
           dst[32 * warp + 8 * t + 4 + j] = whole ? (l != 0.0f ? y1 * f : 0.0f) : y1;
         }
       }
-    if (whole) continue;
-    // -------------------------------------------------------------- join
-    const long long i0 = x0 - first, i1 = i0 + it.tiles - 1;  // the item's tiles
-    const int c0 = static_cast<int>(((i0 + 1) * ctas - 1) / total), c1 = static_cast<int>(((i1 + 1) * ctas - 1) / total);
-    __threadfence();
-    sync();
-    if (tid == 0) *flag = atomicAdd(&p.count[it.index], 1u) == static_cast<unsigned>(c1 - c0);
-    sync();
-    if (!*flag) continue;
-    __threadfence();
-    if (tid == 0) p.count[it.index] = 0;  // ready for the next call
-    // only the first of the item's CTAs can have begun before it
-    const float *head = p.parts + (2ll * c0 + (c0 * total / ctas >= i0 ? 0 : 1)) * kRows * (kD + 2);
-    auto slot = [&](int c) { return c == c0 ? head : p.parts + 2ll * c * kRows * (kD + 2); };
-    for (int idx = tid; idx < n_rows * (kD / 2); idx += L::kConsumers) {
-      const int r = idx / (kD / 2), e = 2 * (idx % (kD / 2));
-      float top = -INFINITY;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot(c) + r * (kD + 2) + kD));
-      const float ref = top == -INFINITY ? 0.0f : top;
-      float n0 = 0.0f, n1 = 0.0f, den = 0.0f;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const float *q = slot(c) + r * (kD + 2);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(q + kD));
-        const float2 y = __ldcg(reinterpret_cast<const float2 *>(q + e));
-        const float f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
-        n0 = fmaf(f, y.x, n0);
-        n1 = fmaf(f, y.y, n1);
-        den = fmaf(f, ml.y, den);
-      }
-      const int row = it.rt * kRows + r;
-      *reinterpret_cast<float2 *>(p.out + (static_cast<int64_t>(it.s) * p.ntok + row / p.group) * p.n_heads * kD +
-                                  (it.h * p.group + row % p.group) * kD + e) =
-          den != 0.0f ? make_float2(n0 / den, n1 / den) : make_float2(0.0f, 0.0f);
+  }
+}
+
+// Joins the parts of the items that more than one CTA holds: one warp per
+// (item, row), the parts in the order of their positions.
+template <int NB, int MT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p, int grid) {
+  constexpr int kRows = 16 * MT, kD = 32 * NB, kPart = kRows * (kD + 2);
+  __shared__ long long before_s;
+  __shared__ long long total_s;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = tree_size(p, s);
+  const int nrt = (n * p.group + kRows - 1) / kRows;
+  const int tiles = sequence_tiles(p, s, n);
+  // tiles of the sequences before this one, and of all
+  if (warp == 0) {
+    long long below = 0, all = 0;
+    for (int k = lane; k < p.v.n_seq; k += 32) {
+      const int m = tree_size(p, k);
+      const long long x = static_cast<long long>(sequence_tiles(p, k, m)) * ((m * p.group + kRows - 1) / kRows) * p.v.n_kv;
+      all += x;
+      if (k < s) below += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      below += __shfl_xor_sync(0xffffffffu, below, o);
+      all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    if (lane == 0) before_s = below, total_s = all;
+  }
+  __syncthreads();
+  const int x = blockIdx.x * (kJoinThreads / 32) + warp;  // (head, row of the head)
+  const int h = x / (p.ntok * p.group), row = x % (p.ntok * p.group);
+  if (h >= p.v.n_kv || row >= n * p.group) return;
+  const long long total = total_s, ctas = grid < total ? grid : total;
+  const long long i0 = before_s + static_cast<long long>(h * nrt + row / kRows) * tiles, i1 = i0 + tiles - 1;
+  const int c0 = static_cast<int>(((i0 + 1) * ctas - 1) / total), c1 = static_cast<int>(((i1 + 1) * ctas - 1) / total);
+  if (c0 == c1) return;  // one CTA held it whole and wrote it
+  // only the first of the item's CTAs can have begun before it
+  const float *rest = p.parts + (row % kRows) * (kD + 2);
+  const float *head = rest + (c0 * total / ctas >= i0 ? 0 : kPart);
+  float top = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, (c == c0 ? head : rest)[2ll * c * kPart + kD]);
+  top = warp_max_all(top);
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float4 y[NB / 4] = {};
+  float den = 0.0f;
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const float *q = (c == c0 ? head : rest) + 2ll * c * kPart;
+    const float2 ml = *reinterpret_cast<const float2 *>(q + kD);
+    const float f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
+    den = fmaf(f, ml.y, den);
+#pragma unroll
+    for (int e = 0; e < NB / 4; ++e) {
+      const float2 a = *reinterpret_cast<const float2 *>(q + 128 * e + 4 * lane);
+      const float2 b = *reinterpret_cast<const float2 *>(q + 128 * e + 4 * lane + 2);
+      y[e].x = fmaf(f, a.x, y[e].x);
+      y[e].y = fmaf(f, a.y, y[e].y);
+      y[e].z = fmaf(f, b.x, y[e].z);
+      y[e].w = fmaf(f, b.y, y[e].w);
     }
   }
+  float *out = p.out + (static_cast<int64_t>(s) * p.ntok + row / p.group) * p.n_heads * kD +
+               (h * p.group + row % p.group) * kD;
+#pragma unroll
+  for (int e = 0; e < NB / 4; ++e)
+    *reinterpret_cast<float4 *>(out + 128 * e + 4 * lane) =
+        den != 0.0f ? make_float4(y[e].x / den, y[e].y / den, y[e].z / den, y[e].w / den) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // rows of a row tile for ntok tokens of `group` heads
 inline int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
-
-inline size_t count_bytes(const epq_pages *pages, int group, int ntok) {
-  const int rt = (ntok * group + 15) / 16;
-  return (4 * static_cast<size_t>(pages->n_seq) * pages->n_kv_heads * rt + 127) & ~size_t(127);
-}
 
 template <int NB, int MT>
 cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t s) {
@@ -682,7 +711,11 @@ cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, L::kThreads, L::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(kMaxCtas, dev.sm_count * std::max(per_sm, 1));
-  return launch_pdl(k, dim3(grid), dim3(L::kThreads), L::kSmem, s, p);
+  e = launch_pdl(k, dim3(grid), dim3(L::kThreads), L::kSmem, s, p);
+  if (e != cudaSuccess) return e;
+  const int rows = p.v.n_kv * p.ntok * p.group;
+  return launch_pdl(join_kernel<NB, MT>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.v.n_seq),
+                    dim3(kJoinThreads), 0, s, p, grid);
 }
 
 }  // namespace
@@ -695,8 +728,7 @@ extern "C" size_t epq_attention_tree_workspace_bytes(const epq_pages *pages, int
       n_heads / pages->n_kv_heads > kMaxGroupTree || ntok < 1 || ntok > kMaxTree)
     return 0;
   const int group = n_heads / pages->n_kv_heads;
-  return count_bytes(pages, group, ntok) +
-         2 * sizeof(float) * kMaxCtas * static_cast<size_t>(tile_rows(ntok * group)) * (pages->head_dim + 2);
+  return 2 * sizeof(float) * kMaxCtas * static_cast<size_t>(tile_rows(ntok * group)) * (pages->head_dim + 2);
 }
 
 extern "C" epq_status epq_attention_tree(const epq_pages *pages, int layer, const float *q, const float *k_new,
@@ -736,8 +768,7 @@ extern "C" epq_status epq_attention_tree(const epq_pages *pages, int layer, cons
   p.ntok = ntok;
   p.scale = scale;
   p.out = out;
-  p.count = static_cast<unsigned *>(ws);
-  p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + count_bytes(pages, p.group, ntok));
+  p.parts = static_cast<float *>(ws);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool small = tile_rows(ntok * p.group) == 16;
   cudaError_t e = D == 128 ? (small ? launch_tree<4, 1>(p, dev, s) : launch_tree<4, 2>(p, dev, s))
