@@ -1,15 +1,26 @@
 // Acceptance of drafted tokens against the target's probabilities
 // (epq_verify_tree).
 //
-// Two launches: row_stats_kernel reads every logits row once (maximum with
-// its lowest index, sum of exponentials), walk_kernel goes down the tree of
-// one sequence, one CTA per sequence.
+// Two launches.  row_stats_kernel reads every logits row once, in chunks of
+// CTAs: maximum with its lowest index and the sum of exponentials (float32,
+// relative to the chunk's maximum).  walk_kernel joins them and goes down the
+// tree, one thread-block cluster per sequence; every thread takes the same
+// decisions from the same numbers.  An acceptance needs only w(x) of the
+// drafted token, which the CTA gathers for all tokens at the start; the row
+// itself is read again only where a draft row has to be subtracted after a
+// rejection, and once to draw the next token.
 //
-// The weights w(v) = exp((l_v - max) / T) of a row in which the walk rejects
-// or ends are formed in double precision and summed as 64-bit integers in
-// units of 2^-44: the sums do not depend on their order, and the drawn token
-// (a comparison of a partial sum with u times the total) is settled to about
-// 2^-45 of the largest weight.  vocab <= 2^18 keeps every sum below 2^62.
+// Drawing compares a partial sum of up to 2^18 weights with u times their
+// total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
+// about 2^-31 of themselves and summed as 64-bit integers in units of 2^-44:
+// the sums do not depend on their order, and a wrong neighbour needs u within
+// about 1e-10 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
+// (n, j integers, |g| <= 1/64, everything that float32 loses of l - max and
+// of the product kept in a second float)
+//   w = 2^n 2^(j/32) (1 + (z + z^2/2 + z^3/6 + ...)),  z = g ln 2,
+// a table entry of 62 bits plus a small float, shifted right by 18 - n.  (GB300
+// has two double-precision lanes per SM and clock; the same pass in double
+// precision took 0.8 ms for 128256 tokens.)
 #include <cmath>
 
 #include "pages.cuh"
@@ -18,21 +29,27 @@ namespace epq {
 namespace {
 
 constexpr int kStatThreads = 256;
-constexpr int kWalkThreads = 1024;
+constexpr int kWalkThreads = 512;
+constexpr int kWalkWarps = kWalkThreads / 32;
+constexpr int kWalkCluster = 8;
 constexpr int64_t kMaxVocab = 262144;
 constexpr double kUnit = 17592186044416.0;  // 2^44
+// CTAs from which row_stats_kernel takes long chunks (two per SM of a GB300)
+constexpr int64_t kManyChunks = 304;
 
 struct VerifyParams {
   const float *logits, *draft, *u;
   const int32_t *tokens, *parent, *n_tok;
   int64_t ld, draft_ld;
-  int vocab, n_seq, ntok, greedy;
-  float temperature;
+  int vocab, n_seq, ntok, greedy, splits;
+  float c_hi, c_lo;  // log2(e) / temperature in two parts
+  float inv_t;
   int32_t *path, *n_accept, *next_token;
   float *lse;
-  float *row_max;  // workspace: [n_seq * ntok]
-  float *row_sum;
-  int32_t *row_arg;
+  float *part_max;  // workspace: [rows][splits]
+  float *part_sum;
+  int32_t *part_arg;
+  unsigned long long table[32];  // 2^(j/32) in units of 2^-62
 };
 
 __device__ __forceinline__ int tree_size(const int32_t *n_tok, int s, int ntok) {
@@ -44,166 +61,298 @@ __device__ __forceinline__ void take_max(float &m, int &at, float m2, int at2) {
   if (m2 > m || (m2 == m && at2 < at)) m = m2, at = at2;
 }
 
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Sum over maxima: z relative to m joined with z2 relative to m2.
+__device__ __forceinline__ float join_sum(float m, float z, float top, float c) {
+  return m == -INFINITY ? 0.0f : z * exp2_fast((m - top) * c);
+}
+
+// Grid (splits, rows).  A CTA reads 1024 VEC consecutive floats of a row,
+// 16 bytes at a time from 16-byte boundaries (a row may begin between two).
+template <int VEC>
 __global__ void __launch_bounds__(kStatThreads) row_stats_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ float sm[8];
+  __shared__ float sm[8], ss[8];
   __shared__ int si[8];
-  __shared__ float ss[8];
   pdl_launch_dependents();
   pdl_wait();
-  const int s = blockIdx.x / p.ntok, i = blockIdx.x % p.ntok;
-  if (i >= tree_size(p.n_tok, s, p.ntok)) {
-    if (threadIdx.x == 0 && p.lse) p.lse[blockIdx.x] = 0.0f;
-    return;
-  }
-  const float *row = p.logits + blockIdx.x * p.ld;
+  const int r = blockIdx.y;
+  if (r % p.ntok >= tree_size(p.n_tok, r / p.ntok, p.ntok)) return;
+  const float *row = p.logits + static_cast<int64_t>(r) * p.ld;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) / 4 & 3);  // floats past a boundary
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float4 x[VEC];
+  const int v0 = blockIdx.x * (1024 * VEC) - shift + 4 * static_cast<int>(threadIdx.x);
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    const int v = v0 + 1024 * k;
+    if (v >= 0 && v + 3 < p.vocab) {
+      x[k] = __ldg(reinterpret_cast<const float4 *>(row + v));
+    } else {
+      x[k].x = v >= 0 && v < p.vocab ? row[v] : -INFINITY;
+      x[k].y = v + 1 >= 0 && v + 1 < p.vocab ? row[v + 1] : -INFINITY;
+      x[k].z = v + 2 >= 0 && v + 2 < p.vocab ? row[v + 2] : -INFINITY;
+      x[k].w = v + 3 >= 0 && v + 3 < p.vocab ? row[v + 3] : -INFINITY;
+    }
+  }
   float m = -INFINITY;
-  int at = 0;
-  for (int v = threadIdx.x; v < p.vocab; v += kStatThreads) take_max(m, at, row[v], v);
+  int at = 0x7fffffff;
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {  // rising indices: a later one replaces only a smaller value
+    const int v = v0 + 1024 * k;
+    if (x[k].x > m) m = x[k].x, at = v;
+    if (x[k].y > m) m = x[k].y, at = v + 1;
+    if (x[k].z > m) m = x[k].z, at = v + 2;
+    if (x[k].w > m) m = x[k].w, at = v + 3;
+  }
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     take_max(m, at, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, at, o));
   if (lane == 0) sm[warp] = m, si[warp] = at;
   __syncthreads();
   m = sm[0], at = si[0];
+#pragma unroll
   for (int w = 1; w < 8; ++w) take_max(m, at, sm[w], si[w]);
-  const float inv_t = p.greedy ? 1.0f : 1.0f / p.temperature;
+  const float ref = m == -INFINITY ? 0.0f : m;
   float z = 0.0f;
-  for (int v = threadIdx.x; v < p.vocab; v += kStatThreads) z += expf((row[v] - m) * inv_t);
+#pragma unroll
+  for (int k = 0; k < VEC; ++k)
+    z += (exp2_fast((x[k].x - ref) * p.c_hi) + exp2_fast((x[k].y - ref) * p.c_hi)) +
+         (exp2_fast((x[k].z - ref) * p.c_hi) + exp2_fast((x[k].w - ref) * p.c_hi));
   z = warp_sum_xor<32>(z);
   if (lane == 0) ss[warp] = z;
   __syncthreads();
   if (threadIdx.x == 0) {
     z = 0.0f;
     for (int w = 0; w < 8; ++w) z += ss[w];
-    p.row_max[blockIdx.x] = m;
-    p.row_sum[blockIdx.x] = z;
-    p.row_arg[blockIdx.x] = at;
-    if (p.lse) p.lse[blockIdx.x] = m * inv_t + logf(z);
+    const int64_t i = static_cast<int64_t>(r) * p.splits + blockIdx.x;
+    p.part_max[i] = m;
+    p.part_sum[i] = z;
+    p.part_arg[i] = at;
   }
 }
 
-__device__ __forceinline__ long long block_sum(long long x, long long *sums) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-  for (int w = 0; w < kWalkThreads / 32; ++w) x += sums[w];
-  return x;
+struct Table {
+  unsigned long long t[32];
+  float f[32];  // 2^(j/32) in units of 2^-36
+};
+
+// exp((l - m) / T) in units of 2^-44, l <= m (see the head of the file).
+__device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, float c_lo, const Table &tab) {
+  const float d = l - m;
+  float t = d * c_hi;
+  if (t < -64.0f) return 0;
+  const float b = d - l;
+  const float e = (l - (d - b)) + (-m - b);  // l - m = d + e
+  const float te = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);
+  const float k = rintf(t * 32.0f);
+  const float g = fmaf(k, -0.03125f, t);
+  const float z = fmaf(g, 0.693147182464599609375f, fmaf(te, 0.693147182464599609375f, g * -1.904654323148236e-09f));
+  const float x = fmaf(z * z, fmaf(z, fmaf(z, 0.041666667f, 0.16666667f), 0.5f), z);
+  const int ki = static_cast<int>(k), j = ki & 31;
+  const long long f = static_cast<long long>(tab.t[j]) + (static_cast<long long>(__float2int_rn(x * tab.f[j])) << 26);
+  const int s = min(18 - (ki >> 5), 63);
+  return static_cast<long long>((static_cast<unsigned long long>(f) + (1ull << (s - 1))) >> s);
 }
 
+// max(w - S q, 0) in the same units, S = s_hi + s_lo.
+__device__ __forceinline__ long long subtract_fixed(long long w, float s_hi, float s_lo, float q) {
+  const float a = s_hi * q;
+  if (!(a < 2.0f)) return 0;  // w <= 1
+  const float ae = fmaf(s_hi, q, -a) + s_lo * q;
+  const int i = __float2int_rn(a * 268435456.0f);  // 2^28
+  const float rest = fmaf(static_cast<float>(i >> 8), -9.5367431640625e-7f, a) -
+                     static_cast<float>(i & 255) * 3.7252902984619140625e-9f + ae;
+  const long long v = w - (static_cast<long long>(i) << 16) - __float2int_rn(rest * 17592186044416.0f);
+  return v > 0 ? v : 0;
+}
+
+// One cluster per sequence.
 __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ long long sums[kWalkThreads / 32];
-  __shared__ int gone[kMaxTree];  // rejected tokens of the current node (no draft)
-  __shared__ int drawn;
+  __shared__ Table tab;
+  __shared__ float top[kMaxTree], sum[kMaxTree], lx[kMaxTree], qx[kMaxTree], us[kMaxTree];
+  __shared__ int arg[kMaxTree], tok[kMaxTree], up[kMaxTree], gone[kMaxTree];
+  __shared__ long long warp_sum[kWalkWarps];
+  __shared__ long long cta_sum[2][kWalkCluster];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int s = blockIdx.x / kWalkCluster;
+  if (tid < 32) {
+    tab.t[tid] = p.table[tid];
+    tab.f[tid] = static_cast<float>(static_cast<double>(p.table[tid]) * 1.4901161193847656e-08);  // 2^-26
+  }
   pdl_launch_dependents();
   pdl_wait();
-  const int s = blockIdx.x, tid = threadIdx.x;
   const int n = tree_size(p.n_tok, s, p.ntok);
   const int base = s * p.ntok;
   int32_t *path = p.path + base;
-  for (int i = tid; i < p.ntok; i += kWalkThreads)
-    if (i >= 1 || n == 0) path[i] = -1;
-  if (n == 0) {
-    if (tid == 0) p.n_accept[s] = 0, p.next_token[s] = -1;
-    return;
+  const bool writer = rank == 0;
+  if (writer) {
+    for (int i = tid; i < p.ntok; i += kWalkThreads) {
+      if (i >= n && p.lse) p.lse[base + i] = 0.0f;
+      if (i >= 1 || n == 0) path[i] = -1;
+    }
+    if (n == 0 && tid == 0) p.n_accept[s] = 0, p.next_token[s] = -1;
   }
+  if (n == 0) return;  // the whole cluster
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const bool use_draft = p.draft != nullptr && !p.greedy;
-  const double inv_t = p.greedy ? 1.0 : 1.0 / static_cast<double>(p.temperature);
-  int cur = 0, count = 1, n_gone = 0;
+  // the drafted tokens' logits and draft probabilities in their parents' rows
+  if (tid < n) {
+    const int x = p.tokens[base + tid], a = p.parent[base + tid];
+    tok[tid] = x;
+    up[tid] = a;
+    us[tid] = p.greedy ? 0.0f : p.u[base + tid];
+    const bool known = tid > 0 && a >= 0 && a < tid && x >= 0 && x < p.vocab;
+    lx[tid] = known ? p.logits[static_cast<int64_t>(base + a) * p.ld + x] : -INFINITY;
+    qx[tid] = known && use_draft ? p.draft[static_cast<int64_t>(base + a) * p.draft_ld + x] : 1.0f;
+  }
+  for (int r = warp; r < n; r += kWalkWarps) {
+    const int64_t i = static_cast<int64_t>(base + r) * p.splits;
+    float m = -INFINITY, z = 0.0f;
+    int at = 0x7fffffff;
+    for (int k = lane; k < p.splits; k += 32) take_max(m, at, p.part_max[i + k], p.part_arg[i + k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      take_max(m, at, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, at, o));
+    for (int k = lane; k < p.splits; k += 32) z += join_sum(p.part_max[i + k], p.part_sum[i + k], m, p.c_hi);
+    z = warp_sum_xor<32>(z);
+    if (lane == 0) {
+      top[r] = m;
+      sum[r] = z;
+      arg[r] = at < p.vocab ? at : 0;  // a row without a finite logit
+      if (writer && p.lse) p.lse[base + r] = m * p.inv_t + logf(z);
+    }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA has started: its shared memory may be written
+
+  int cur = 0, count = 1, n_gone = 0, phase = 0;
+  double R = sum[0], S = 0.0;  // in units of the largest weight
+  // slice of a row: a warp has `per` consecutive entries (a multiple of 128)
+  const int per = ((p.vocab + kWalkCluster * kWalkWarps - 1) / (kWalkCluster * kWalkWarps) + 127) & ~127;
+  const int w0 = min((static_cast<int>(rank) * kWalkWarps + warp) * per, p.vocab), w1 = min(w0 + per, p.vocab);
   const float *row = p.logits + static_cast<int64_t>(base) * p.ld;
   const float *q = use_draft ? p.draft + static_cast<int64_t>(base) * p.draft_ld : nullptr;
-  float m = p.row_max[base];
-  double R = p.row_sum[base];  // in units of the largest weight
-  double S = 0.0;
-  auto weight = [&](int v) { return exp((static_cast<double>(row[v]) - static_cast<double>(m)) * inv_t); };
-  auto left = [&](int v) {  // r(v) in units of 2^-44
-    double w = weight(v);
-    if (use_draft) w = fmax(w - S * static_cast<double>(q[v]), 0.0);
-    for (int k = 0; k < n_gone; ++k)
-      if (gone[k] == v) w = 0.0;
-    return __double2ll_rn(w * kUnit);
+  auto left = [&](int v, float s_hi, float s_lo) {
+    long long w = weight_fixed(row[v], top[cur], p.c_hi, p.c_lo, tab);
+    if (s_hi > 0.0f) w = subtract_fixed(w, s_hi, s_lo, q[v]);
+    return w;
   };
+  // r(v) summed over the row, in units of 2^-44; warp_sum and cta_sum[phase]
+  // keep the parts
   auto total = [&]() {
+    const float s_hi = static_cast<float>(S), s_lo = static_cast<float>(S - static_cast<double>(s_hi));
     long long t = 0;
-    for (int v = tid; v < p.vocab; v += kWalkThreads) t += left(v);
-    return block_sum(t, sums);
+#pragma unroll 4
+    for (int v = w0 + lane; v < w1; v += 32) t += left(v, s_hi, s_lo);
+    for (int k = lane; k < n_gone; k += 32)
+      if (gone[k] >= w0 && gone[k] < w1) t -= left(gone[k], s_hi, s_lo);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    phase ^= 1;
+    if (lane == 0) warp_sum[warp] = t;
+    __syncthreads();
+    if (tid < kWalkCluster) {
+      t = 0;
+      for (int w = 0; w < kWalkWarps; ++w) t += warp_sum[w];
+      uint32_t remote;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                   : "=r"(remote)
+                   : "r"(smem_addr(&cta_sum[phase][rank])), "r"(static_cast<uint32_t>(tid)));
+      asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(remote), "l"(t) : "memory");
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    t = 0;
+    for (int c = 0; c < kWalkCluster; ++c) t += cta_sum[phase][c];
+    return t;
   };
-  if (tid == 0) path[0] = 0;
-  __syncthreads();
-  for (int i = 1; i < n; ++i) {  // every thread takes the same decisions
-    if (p.parent[base + i] != cur) continue;
-    const int x = p.tokens[base + i];
+  long long all = -1;  // the last total, while it is that of the current state
+  if (writer && tid == 0) path[0] = 0;
+  for (int i = 1; i < n; ++i) {
+    if (up[i] != cur) continue;
+    const int x = tok[i];
     const bool known = x >= 0 && x < p.vocab;
     bool yes = false;
+    double here = 0.0;
     if (p.greedy) {
-      yes = x == p.row_arg[base + cur];
+      yes = x == arg[cur];
     } else if (known) {
-      const double here = static_cast<double>(left(x)) / kUnit;
-      const double qx = use_draft ? static_cast<double>(q[x]) : 1.0;
-      yes = static_cast<double>(p.u[base + i]) * qx * R < here;
+      const double w = static_cast<double>(weight_fixed(lx[i], top[cur], p.c_hi, p.c_lo, tab)) / kUnit;
+      here = fmax(w - S * static_cast<double>(qx[i]), 0.0);
+      for (int k = 0; k < n_gone; ++k)
+        if (gone[k] == x) here = 0.0;
+      yes = static_cast<double>(us[i]) * static_cast<double>(qx[i]) * R < here;
     }
     if (yes) {
       __syncthreads();  // `gone` is no longer read
       cur = i;
       n_gone = 0;
       S = 0.0;
+      R = sum[i];
+      all = -1;
       row = p.logits + static_cast<int64_t>(base + i) * p.ld;
       if (use_draft) q = p.draft + static_cast<int64_t>(base + i) * p.draft_ld;
-      m = p.row_max[base + i];
-      R = p.row_sum[base + i];
-      if (tid == 0) path[count] = i;
+      if (writer && tid == 0) path[count] = i;
       ++count;
     } else if (!p.greedy && use_draft) {
-      if (S == 0.0) R = static_cast<double>(total()) / kUnit;  // the exact sum of the row's weights
+      if (S == 0.0) R = static_cast<double>(total()) / kUnit;  // the row's weights, to the unit
       const double kept = S;
       S += R;
-      const double less = static_cast<double>(total()) / kUnit;
-      if (less > 0.0) R = less;
-      else S = kept;
-    } else if (!p.greedy && known) {
-      R -= static_cast<double>(left(x)) / kUnit;
+      all = total();
+      if (all > 0) {
+        R = static_cast<double>(all) / kUnit;
+      } else {
+        S = kept;
+        all = -1;
+      }
+    } else if (!p.greedy && known && here > 0.0) {
+      R -= here;
+      all = -1;
       __syncthreads();
       if (tid == 0) gone[n_gone] = x;
       ++n_gone;
       __syncthreads();
     }
   }
-  // the next token
-  int next = p.row_arg[base + cur];
-  if (!p.greedy) {
-    const int per = (p.vocab + kWalkThreads - 1) / kWalkThreads;  // consecutive entries of a thread
-    const int v0 = min(tid * per, p.vocab), v1 = min(v0 + per, p.vocab);
-    long long mine = 0;
-    for (int v = v0; v < v1; ++v) mine += left(v);
-    const long long all = block_sum(mine, sums);
-    // exclusive prefix of the thread's entries
-    long long before = mine;
-    const int lane = tid & 31, warp = tid >> 5;
+  if (writer && tid == 0) p.n_accept[s] = count;
+  if (!p.greedy && all < 0) all = total();
+  if (p.greedy || all <= 0) {
+    if (writer && tid == 0) p.next_token[s] = arg[cur];
+  } else {
+    // the entry where the running sum passes t: its CTA, its warp, its place
+    const long long t = static_cast<long long>(floor(static_cast<double>(us[0]) * static_cast<double>(all)));
+    long long at = 0;
+    for (uint32_t c = 0; c < rank; ++c) at += cta_sum[phase][c];
+    for (int w = 0; w < warp; ++w) at += warp_sum[w];
+    if (at <= t && t < at + warp_sum[warp]) {
+      const float s_hi = static_cast<float>(S), s_lo = static_cast<float>(S - static_cast<double>(s_hi));
+      for (int v0 = w0; v0 < w1; v0 += 32) {
+        const int v = v0 + lane;
+        long long x = v < w1 ? left(v, s_hi, s_lo) : 0;
+        for (int k = 0; k < n_gone; ++k)
+          if (gone[k] == v) x = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += y;
-    }
-    before -= mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
-    if (tid == 0) drawn = next;
-    __syncthreads();
-    const double t = static_cast<double>(p.u[base]) * static_cast<double>(all);
-    if (static_cast<double>(before) <= t && static_cast<double>(before + mine) > t) {
-      for (int v = v0; v < v1; ++v) {
-        before += left(v);
-        if (static_cast<double>(before) > t) {
-          drawn = v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, at + x > t);
+        if (past) {
+          if (lane == __ffs(past) - 1) p.next_token[s] = v;
           break;
         }
+        at += __shfl_sync(0xffffffffu, x, 31);
       }
     }
-    __syncthreads();
-    next = drawn;
   }
-  if (tid == 0) p.n_accept[s] = count, p.next_token[s] = next;
+  // no CTA leaves while another may still write into its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(64) tree_mask_kernel(const int32_t *__restrict__ parent, int n_seq, int ntok,
@@ -242,9 +391,20 @@ extern "C" epq_status epq_tree_mask(const int32_t *parent, int n_seq, int ntok, 
   return e == cudaSuccess ? EPQ_OK : cuda_fail(e);
 }
 
+// Chunks of a row: long ones where there are rows enough to fill the GPU.
+static int64_t stats_chunk(int64_t rows, int64_t vocab) {
+  return rows * ((vocab + 8191) / 8192) >= kManyChunks ? 8192 : 2048;
+}
+
+static int64_t stats_splits(int64_t rows, int64_t vocab) {
+  const int64_t c = stats_chunk(rows, vocab);
+  return (vocab + 3 + c - 1) / c;  // up to 3 floats of a chunk lie before the row
+}
+
 extern "C" size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab) {
   if (n_seq < 1 || n_seq > kMaxSeq || ntok < 1 || ntok > kMaxTree || vocab < 1 || vocab > kMaxVocab) return 0;
-  return 3 * sizeof(float) * static_cast<size_t>(n_seq) * ntok;
+  const int64_t rows = static_cast<int64_t>(n_seq) * ntok;
+  return 3 * sizeof(float) * static_cast<size_t>(rows * stats_splits(rows, vocab));
 }
 
 extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const int32_t *tokens, const int32_t *parent,
@@ -255,9 +415,9 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   const size_t need = epq_verify_tree_workspace_bytes(n_seq, ntok, vocab);
   if (!need) return EPQ_ERR_SHAPE;
   VerifyParams p = {};
-  p.temperature = opts ? opts->temperature : 1.0f;
-  if (!(p.temperature >= 0.0f) || std::isinf(p.temperature)) return EPQ_ERR_ARG;
-  p.greedy = p.temperature == 0.0f;
+  const float temperature = opts ? opts->temperature : 1.0f;
+  if (!(temperature >= 0.0f) || std::isinf(temperature)) return EPQ_ERR_ARG;
+  p.greedy = temperature == 0.0f;
   if (!p.greedy && !u) return EPQ_ERR_ARG;
   p.ld = opts && opts->ld ? opts->ld : vocab;
   p.draft_ld = opts && opts->draft_ld ? opts->draft_ld : vocab;
@@ -265,6 +425,7 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   if (!ws || ws_bytes < need) return EPQ_ERR_WORKSPACE;
   if (!aligned16(logits) || !aligned16(ws) || (opts && opts->draft && !aligned16(opts->draft))) return EPQ_ERR_ALIGN;
   if (!device_ok()) return EPQ_ERR_DEVICE;
+  const int64_t rows = static_cast<int64_t>(n_seq) * ntok;
   p.logits = logits;
   p.draft = opts ? opts->draft : nullptr;
   p.u = u;
@@ -274,15 +435,37 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   p.vocab = static_cast<int>(vocab);
   p.n_seq = n_seq;
   p.ntok = ntok;
+  p.splits = static_cast<int>(stats_splits(rows, vocab));
+  const double c = 1.4426950408889634 / (p.greedy ? 1.0 : static_cast<double>(temperature));
+  p.c_hi = static_cast<float>(c);
+  p.c_lo = static_cast<float>(c - static_cast<double>(p.c_hi));
+  p.inv_t = p.greedy ? 1.0f : static_cast<float>(1.0 / static_cast<double>(temperature));
   p.path = path;
   p.n_accept = n_accept;
   p.next_token = next_token;
   p.lse = lse;
-  p.row_max = static_cast<float *>(ws);
-  p.row_sum = p.row_max + static_cast<size_t>(n_seq) * ntok;
-  p.row_arg = reinterpret_cast<int32_t *>(p.row_sum + static_cast<size_t>(n_seq) * ntok);
+  p.part_max = static_cast<float *>(ws);
+  p.part_sum = p.part_max + rows * p.splits;
+  p.part_arg = reinterpret_cast<int32_t *>(p.part_sum + rows * p.splits);
+  for (int j = 0; j < 32; ++j) p.table[j] = static_cast<unsigned long long>(std::exp2(j / 32.0) * 4611686018427387904.0);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(row_stats_kernel, dim3(n_seq * ntok), dim3(kStatThreads), 0, s, p);
-  if (e == cudaSuccess) e = launch_pdl(walk_kernel, dim3(n_seq), dim3(kWalkThreads), 0, s, p);
+  const dim3 grid(p.splits, static_cast<unsigned>(rows));
+  cudaError_t e = stats_chunk(rows, vocab) == 8192 ? launch_pdl(row_stats_kernel<8>, grid, dim3(kStatThreads), 0, s, p)
+                                                   : launch_pdl(row_stats_kernel<2>, grid, dim3(kStatThreads), 0, s, p);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_seq) * kWalkCluster);
+  cfg.blockDim = dim3(kWalkThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kWalkCluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, walk_kernel, p);
   return e == cudaSuccess ? EPQ_OK : cuda_fail(e);
 }
