@@ -4,11 +4,12 @@
 // Two launches.  row_stats_kernel reads every logits row once, in chunks of
 // CTAs: maximum with its lowest index and the sum of exponentials (float32,
 // relative to the chunk's maximum).  walk_kernel joins them and goes down the
-// tree, one thread-block cluster per sequence; every thread takes the same
-// decisions from the same numbers.  An acceptance needs only w(x) of the
+// tree, one thread-block cluster per sequence; warp 0 of every CTA takes the
+// same decisions from the same numbers.  An acceptance needs only w(x) of the
 // drafted token, which the CTA gathers for all tokens at the start; the row
 // itself is read again only where a draft row has to be subtracted after a
-// rejection, and once to draw the next token.
+// rejection, and once to draw the next token (its weights then stay in shared
+// memory).
 //
 // Drawing compares a partial sum of up to 2^18 weights with u times their
 // total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
@@ -31,7 +32,8 @@ namespace {
 constexpr int kStatThreads = 256;
 constexpr int kWalkThreads = 512;
 constexpr int kWalkWarps = kWalkThreads / 32;
-constexpr int kWalkCluster = 8;
+constexpr int kWalkCluster = 16;  // CTAs of one sequence; more than 8 need the kernel's opt-in
+constexpr int kGroup = 256;       // entries that a warp reads at a time
 constexpr int64_t kMaxVocab = 262144;
 constexpr double kUnit = 17592186044416.0;  // 2^44
 // CTAs from which row_stats_kernel takes long chunks (two per SM of a GB300)
@@ -171,13 +173,25 @@ __device__ __forceinline__ long long subtract_fixed(long long w, float s_hi, flo
   return v > 0 ? v : 0;
 }
 
+// Consecutive entries of a row that one warp of a cluster holds.
+__host__ __device__ inline int walk_entries(int vocab) {
+  const int warps = kWalkCluster * kWalkWarps;
+  return ((vocab + warps - 1) / warps + kGroup - 1) / kGroup * kGroup;
+}
+
 // One cluster per sequence.
 __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constant__ VerifyParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];  // weights, draft row
   __shared__ Table tab;
   __shared__ float top[kMaxTree], sum[kMaxTree], lx[kMaxTree], qx[kMaxTree], us[kMaxTree];
   __shared__ int arg[kMaxTree], tok[kMaxTree], up[kMaxTree], gone[kMaxTree];
   __shared__ long long warp_sum[kWalkWarps];
   __shared__ long long cta_sum[2][kWalkCluster];
+  __shared__ struct {
+    int state, cur, n_gone, filled, next, draw;
+    float s_hi, s_lo;
+    long long u_all;
+  } ask;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t rank;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -232,27 +246,48 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA has started: its shared memory may be written
 
-  int cur = 0, count = 1, n_gone = 0, phase = 0;
-  double R = sum[0], S = 0.0;  // in units of the largest weight
-  // slice of a row: a warp has `per` consecutive entries (a multiple of 128)
-  const int per = ((p.vocab + kWalkCluster * kWalkWarps - 1) / (kWalkCluster * kWalkWarps) + 127) & ~127;
+  // A warp has `per` consecutive entries of a row (whole groups).  The weights
+  // of the current row, once they are needed, and its draft row stay in shared
+  // memory.
+  const int per = walk_entries(p.vocab);
   const int w0 = min((static_cast<int>(rank) * kWalkWarps + warp) * per, p.vocab), w1 = min(w0 + per, p.vocab);
-  const float *row = p.logits + static_cast<int64_t>(base) * p.ld;
-  const float *q = use_draft ? p.draft + static_cast<int64_t>(base) * p.draft_ld : nullptr;
-  auto left = [&](int v, float s_hi, float s_lo) {
-    long long w = weight_fixed(row[v], top[cur], p.c_hi, p.c_lo, tab);
-    if (s_hi > 0.0f) w = subtract_fixed(w, s_hi, s_lo, q[v]);
-    return w;
-  };
-  // r(v) summed over the row, in units of 2^-44; warp_sum and cta_sum[phase]
+  long long *w_row = reinterpret_cast<long long *>(smem) + warp * per;
+  float *q_row = reinterpret_cast<float *>(smem + 8 * kWalkWarps * per) + warp * per;
+  int phase = 0;
+  // sum of r(v) over the row, in units of 2^-44; warp_sum and cta_sum[phase]
   // keep the parts
-  auto total = [&]() {
-    const float s_hi = static_cast<float>(S), s_lo = static_cast<float>(S - static_cast<double>(s_hi));
+  auto total = [&](int cur, bool filled, float s_hi, float s_lo, int n_gone) {
+    const float m = top[cur];
+    const float *row = p.logits + static_cast<int64_t>(base + cur) * p.ld;
+    const float *q = use_draft ? p.draft + static_cast<int64_t>(base + cur) * p.draft_ld : nullptr;
     long long t = 0;
+    if (filled) {
 #pragma unroll 4
-    for (int v = w0 + lane; v < w1; v += 32) t += left(v, s_hi, s_lo);
-    for (int k = lane; k < n_gone; k += 32)
-      if (gone[k] >= w0 && gone[k] < w1) t -= left(gone[k], s_hi, s_lo);
+      for (int i = lane; i < w1 - w0; i += 32) t += subtract_fixed(w_row[i], s_hi, s_lo, q_row[i]);
+    } else {  // S is 0
+      for (int g = lane; g < w1 - w0; g += kGroup) {
+        float l[kGroup / 32], d[kGroup / 32];
+#pragma unroll
+        for (int j = 0; j < kGroup / 32; ++j) {
+          const bool in = g + 32 * j < w1 - w0;
+          l[j] = in ? __ldg(row + w0 + g + 32 * j) : -INFINITY;
+          d[j] = in && use_draft ? __ldg(q + w0 + g + 32 * j) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kGroup / 32; ++j) {  // the slice holds whole groups
+          const long long w = weight_fixed(l[j], m, p.c_hi, p.c_lo, tab);
+          w_row[g + 32 * j] = w;
+          if (use_draft) q_row[g + 32 * j] = d[j];
+          t += w;
+        }
+      }
+    }
+    __syncwarp();
+    for (int k = 0; k < n_gone; ++k) {
+      const int i = gone[k] - w0;
+      if (i < 0 || i >= w1 - w0) continue;
+      if (lane == 0) t -= w_row[i], w_row[i] = 0;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     phase ^= 1;
@@ -272,71 +307,97 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
     for (int c = 0; c < kWalkCluster; ++c) t += cta_sum[phase][c];
     return t;
   };
-  long long all = -1;  // the last total, while it is that of the current state
+  // The walk: warp 0 takes the decisions (they are scalar, some in double
+  // precision, of which an SM has two lanes) and asks all warps for a sum
+  // where it needs one.
+  int cur = 0, count = 1, n_gone = 0, i = 1, state = 0;  // state 1: sum of the whole row wanted, 2: of what is left
+  double R = sum[0], S = 0.0, kept = 0.0;                // in units of the largest weight
+  long long all = -1;                                    // the last sum, while it is that of the current state
+  bool filled = false;
   if (writer && tid == 0) path[0] = 0;
-  for (int i = 1; i < n; ++i) {
-    if (up[i] != cur) continue;
-    const int x = tok[i];
-    const bool known = x >= 0 && x < p.vocab;
-    bool yes = false;
-    double here = 0.0;
-    if (p.greedy) {
-      yes = x == arg[cur];
-    } else if (known) {
-      const double w = static_cast<double>(weight_fixed(lx[i], top[cur], p.c_hi, p.c_lo, tab)) / kUnit;
-      here = fmax(w - S * static_cast<double>(qx[i]), 0.0);
-      for (int k = 0; k < n_gone; ++k)
-        if (gone[k] == x) here = 0.0;
-      yes = static_cast<double>(us[i]) * static_cast<double>(qx[i]) * R < here;
-    }
-    if (yes) {
-      __syncthreads();  // `gone` is no longer read
-      cur = i;
-      n_gone = 0;
-      S = 0.0;
-      R = sum[i];
-      all = -1;
-      row = p.logits + static_cast<int64_t>(base + i) * p.ld;
-      if (use_draft) q = p.draft + static_cast<int64_t>(base + i) * p.draft_ld;
-      if (writer && tid == 0) path[count] = i;
-      ++count;
-    } else if (!p.greedy && use_draft) {
-      if (S == 0.0) R = static_cast<double>(total()) / kUnit;  // the row's weights, to the unit
-      const double kept = S;
-      S += R;
-      all = total();
-      if (all > 0) {
-        R = static_cast<double>(all) / kUnit;
+  constexpr double kInv = 1.0 / kUnit;
+  for (;;) {
+    if (warp == 0) {
+      if (state == 1) {  // a first rejection: from here on R is exact to the unit
+        R = static_cast<double>(all) * kInv;
+        kept = S;
+        S += R;
+        state = 2;
       } else {
-        S = kept;
-        all = -1;
+        if (state == 2) {
+          if (all > 0) R = static_cast<double>(all) * kInv;
+          else S = kept, all = -1;
+        }
+        const bool done = state == 3;
+        state = 0;
+        for (; i < n && state == 0; ++i) {
+          if (up[i] != cur) continue;
+          const int x = tok[i];
+          const bool known = x >= 0 && x < p.vocab;
+          bool yes = false;
+          double here = 0.0;
+          if (p.greedy) {
+            yes = x == arg[cur];
+          } else if (known) {
+            const double w = static_cast<double>(weight_fixed(lx[i], top[cur], p.c_hi, p.c_lo, tab)) * kInv;
+            here = fmax(w - S * static_cast<double>(qx[i]), 0.0);
+            for (int k = 0; k < n_gone; ++k)
+              if (gone[k] == x) here = 0.0;
+            yes = static_cast<double>(us[i]) * static_cast<double>(qx[i]) * R < here;
+          }
+          if (yes) {
+            cur = i;
+            n_gone = 0;
+            S = 0.0;
+            R = sum[i];
+            all = -1;
+            filled = false;
+            if (writer && lane == 0) path[count] = i;
+            ++count;
+          } else if (!p.greedy && use_draft) {
+            state = S == 0.0 ? 1 : 2;
+            if (state == 2) kept = S, S += R;
+          } else if (!p.greedy && known && here > 0.0) {
+            R -= here;
+            __syncwarp();
+            if (lane == 0) gone[n_gone] = x;
+            ++n_gone;
+            __syncwarp();
+          }
+        }
+        if (state == 0 && !done && !p.greedy && all < 0) state = 3;  // the sum to draw from
       }
-    } else if (!p.greedy && known && here > 0.0) {
-      R -= here;
-      all = -1;
-      __syncthreads();
-      if (tid == 0) gone[n_gone] = x;
-      ++n_gone;
-      __syncthreads();
+      if (lane == 0) {
+        const float s_hi = static_cast<float>(S);
+        ask.state = state;
+        ask.cur = cur;
+        ask.n_gone = n_gone;
+        ask.filled = filled;
+        ask.s_hi = state == 1 ? 0.0f : s_hi;
+        ask.s_lo = state == 1 ? 0.0f : static_cast<float>(S - static_cast<double>(s_hi));
+        ask.u_all = static_cast<long long>(floor(static_cast<double>(us[0]) * static_cast<double>(all)));
+        ask.next = arg[cur];
+        ask.draw = !p.greedy && all > 0;
+        if (state == 0 && writer) p.n_accept[s] = count;
+      }
     }
+    __syncthreads();
+    if (ask.state == 0) break;
+    all = total(ask.cur, ask.filled, ask.s_hi, ask.s_lo, ask.n_gone);
+    filled = true;
   }
-  if (writer && tid == 0) p.n_accept[s] = count;
-  if (!p.greedy && all < 0) all = total();
-  if (p.greedy || all <= 0) {
-    if (writer && tid == 0) p.next_token[s] = arg[cur];
+  if (!ask.draw) {
+    if (writer && tid == 0) p.next_token[s] = ask.next;
   } else {
     // the entry where the running sum passes t: its CTA, its warp, its place
-    const long long t = static_cast<long long>(floor(static_cast<double>(us[0]) * static_cast<double>(all)));
+    const long long t = ask.u_all;
     long long at = 0;
     for (uint32_t c = 0; c < rank; ++c) at += cta_sum[phase][c];
     for (int w = 0; w < warp; ++w) at += warp_sum[w];
     if (at <= t && t < at + warp_sum[warp]) {
-      const float s_hi = static_cast<float>(S), s_lo = static_cast<float>(S - static_cast<double>(s_hi));
-      for (int v0 = w0; v0 < w1; v0 += 32) {
-        const int v = v0 + lane;
-        long long x = v < w1 ? left(v, s_hi, s_lo) : 0;
-        for (int k = 0; k < n_gone; ++k)
-          if (gone[k] == v) x = 0;
+      for (int v = lane; v - lane < w1 - w0; v += 32) {
+        long long x = 0;
+        if (v < w1 - w0) x = ask.s_hi > 0.0f ? subtract_fixed(w_row[v], ask.s_hi, ask.s_lo, q_row[v]) : w_row[v];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -344,7 +405,7 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
         }
         const unsigned past = __ballot_sync(0xffffffffu, at + x > t);
         if (past) {
-          if (lane == __ffs(past) - 1) p.next_token[s] = v;
+          if (lane == __ffs(past) - 1) p.next_token[s] = w0 + v;
           break;
         }
         at += __shfl_sync(0xffffffffu, x, 31);
@@ -453,7 +514,12 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   cudaError_t e = stats_chunk(rows, vocab) == 8192 ? launch_pdl(row_stats_kernel<8>, grid, dim3(kStatThreads), 0, s, p)
                                                    : launch_pdl(row_stats_kernel<2>, grid, dim3(kStatThreads), 0, s, p);
   if (e != cudaSuccess) return cuda_fail(e);
+  const size_t smem = 12 * static_cast<size_t>(kWalkWarps) * walk_entries(p.vocab);
+  e = cudaFuncSetAttribute(walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(walk_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3(static_cast<unsigned>(n_seq) * kWalkCluster);
   cfg.blockDim = dim3(kWalkThreads);
   cfg.stream = s;
