@@ -145,8 +145,14 @@ def load(path: str | None = None):
     return lib
 
 
+# the current stream's handle without a Stream object, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -383,13 +389,19 @@ def epq_attention_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
 
 
 # ------------------------------------------------------------------ paged cache
-def _need(t, name, dtype, shape):
-    """t is a contiguous tensor of this type and shape (None in shape: any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+# The calls of a speculative step are short next to what Python costs, so the
+# functions below compare shapes as tuples and pass addresses as integers.
+def _wrong(t, name, dtype, shape):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def _need(t, name, dtype, shape):
+    """t is a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _wrong(t, name, dtype, shape)
+    return t.data_ptr()
 
 
 class PagedKVCache:
@@ -416,8 +428,10 @@ class PagedKVCache:
         return self
 
     def _bind(self, pool, table, length, refs):
-        _need(pool, "pool", torch.uint8, (None, None, None, 2, None, None))
-        _need(table, "table", torch.int32, (None, None))
+        if pool.dim() != 6 or pool.shape[3] != 2 or table.dim() != 2:
+            raise ValueError("pool must be [layers, pages, heads, 2, page_size, row] and table [n_seq, max_pages]")
+        _need(pool, "pool", torch.uint8, pool.shape)
+        _need(table, "table", torch.int32, table.shape)
         _need(length, "length", torch.int32, (table.shape[0],))
         _need(refs, "refs", torch.int32, (pool.shape[1],))
         self.n_layers, self.n_pages, self.n_kv_heads, _, self.page_size, rb = pool.shape
@@ -433,67 +447,81 @@ class PagedKVCache:
             raise ValueError("sizes of the paged cache not supported")
         self.work = torch.zeros(n, dtype=torch.uint8, device=pool.device)
         self._p.work = self.work.data_ptr()
-
-    def _ints(self, t, name, n=None):
-        return _need(t, name, torch.int32, (self.n_seq if n is None else n,))
+        self._ref = ctypes.byref(self._p)
+        self._per_seq = (self.n_seq,)
 
 
 def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=None) -> None:
     """new_length int32 [n_seq] (negative: leave): shorten sequences and give their pages back (0 frees one)."""
-    cache._ints(new_length, "new_length")
-    _check("epq_pages_truncate", load().epq_pages_truncate(ctypes.byref(cache._p), _ptr(new_length), _stream(stream)))
+    n = _need(new_length, "new_length", torch.int32, cache._per_seq)
+    st = _lib.epq_pages_truncate(cache._ref, n, _stream(stream))
+    if st:
+        raise EpqError("epq_pages_truncate", st)
 
 
 def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, status: torch.Tensor | None = None,
                    stream=None) -> None:
     """Sequences dst (int32 [n], empty) become copies of src, sharing their pages; no entries: nothing happens."""
     n = dst.shape[0]
-    cache._ints(src, "src", n), cache._ints(dst, "dst", n)
-    if status is not None:
-        cache._ints(status, "status", n)
+    a, b = _need(src, "src", torch.int32, (n,)), _need(dst, "dst", torch.int32, (n,))
+    c = None if status is None else _need(status, "status", torch.int32, (n,))
     if n:
-        _check("epq_pages_fork", load().epq_pages_fork(ctypes.byref(cache._p), _ptr(src), _ptr(dst), n, _ptr(status),
-                                                       _stream(stream)))
+        st = _lib.epq_pages_fork(cache._ref, a, b, n, c, _stream(stream))
+        if st:
+            raise EpqError("epq_pages_fork", st)
 
 
 def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """Make extra (int32 [n_seq]) more positions of every sequence writable -> status int32 [n_seq]."""
-    cache._ints(extra, "extra")
+    e = _need(extra, "extra", torch.int32, cache._per_seq)
     if status is None:
         status = torch.empty_like(extra)
-    cache._ints(status, "status")
-    _check("epq_pages_reserve", load().epq_pages_reserve(ctypes.byref(cache._p), _ptr(extra), _ptr(status),
-                                                         _stream(stream)))
+    st = _lib.epq_pages_reserve(cache._ref, e, _need(status, "status", torch.int32, cache._per_seq), _stream(stream))
+    if st:
+        raise EpqError("epq_pages_reserve", st)
     return status
 
 
 def epq_pages_compact(cache: PagedKVCache, path: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
     """Commit the drafted rows path (int32 [n_seq, ntok], n_keep int32 [n_seq] of them) in every layer."""
-    _need(path, "path", torch.int32, (cache.n_seq, None))
-    cache._ints(n_keep, "n_keep")
-    _check("epq_pages_compact", load().epq_pages_compact(ctypes.byref(cache._p), _ptr(path), _ptr(n_keep),
-                                                         path.shape[1], _stream(stream)))
+    ntok = path.shape[-1]
+    a = _need(path, "path", torch.int32, (cache.n_seq, ntok))
+    st = _lib.epq_pages_compact(cache._ref, a, _need(n_keep, "n_keep", torch.int32, cache._per_seq), ntok,
+                                _stream(stream))
+    if st:
+        raise EpqError("epq_pages_compact", st)
 
 
 # ------------------------------------------------------------------ tree step
 def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """parent int32 [n_seq, ntok] -> mask int64 [n_seq, ntok] (bit j: token j is i or an ancestor of i)."""
-    _need(parent, "parent", torch.int32, (None, None))
+    if parent.dim() != 2:
+        raise ValueError("parent must be [n_seq, ntok]")
+    a = _need(parent, "parent", torch.int32, parent.shape)
     if mask is None:
         mask = torch.empty(parent.shape, dtype=torch.int64, device=parent.device)
-    _need(mask, "mask", torch.int64, parent.shape)
-    _check("epq_tree_mask", load().epq_tree_mask(_ptr(parent), parent.shape[0], parent.shape[1], _ptr(mask),
-                                                 _stream(stream)))
+    b = _need(mask, "mask", torch.int64, parent.shape)
+    _check("epq_tree_mask", load().epq_tree_mask(a, parent.shape[0], parent.shape[1], b, _stream(stream)))
     return mask
 
 
 def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int) -> torch.Tensor:
     """A workspace for epq_attention_tree, to be kept between calls."""
-    n = int(load().epq_attention_tree_workspace_bytes(ctypes.byref(cache._p), n_heads, ntok))
+    n = int(load().epq_attention_tree_workspace_bytes(cache._ref, n_heads, ntok))
     if n == 0:
         raise ValueError("sizes of the tree attention not supported")
     return torch.empty(n, dtype=torch.uint8, device=cache.pool.device)
+
+
+def _token_strides(t, name, shape):
+    """Floats between sequences and tokens of t [n_seq, ntok, n] (0: a dimension of one entry says nothing)."""
+    if t.dtype is not torch.float32 or t.shape != shape:
+        raise ValueError(f"{name}: expected float32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    a, b, c = t.stride()
+    if c != 1 or (a == 0 and shape[0] > 1) or (b == 0 and shape[1] > 1):
+        raise ValueError(f"{name}: rows must be contiguous and not broadcast")
+    return a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
 
 def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, cache: PagedKVCache, layer: int,
@@ -502,33 +530,25 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [n_seq, ntok, n_heads*D], k_new/v_new [n_seq, ntok, n_kv*D] (float32; views of one wider buffer are
     read in place) -> out [n_seq, ntok, n_heads*D]; the new rows are stored behind the committed positions."""
-    lib = load()
-    D = cache.head_dim
-    for t, name, n in ((q, "q", n_heads * D), (k_new, "k_new", cache.n_kv_heads * D),
-                       (v_new, "v_new", cache.n_kv_heads * D)):
-        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] != cache.n_seq or t.shape[2] != n or \
-                t.shape[1] != q.shape[1] or t.stride(2) != 1:
-            raise ValueError(f"{name}: expected float32 [{cache.n_seq}, {q.shape[1]}, {n}] with contiguous rows")
-    ntok = q.shape[1]
-    # the stride of a dimension of one entry says nothing
-    ld = lambda t, d: t.stride(d) if t.shape[d] > 1 else 0  # noqa: E731
-    if any(t.shape[d] > 1 and t.stride(d) == 0 for t in (q, k_new, v_new) for d in (0, 1)):
-        raise ValueError("q, k_new and v_new must not be broadcast")
-    if ld(k_new, 0) != ld(v_new, 0) or ld(k_new, 1) != ld(v_new, 1):
+    ntok, nseq, D = q.shape[1], cache.n_seq, cache.head_dim
+    shape = (nseq, ntok, n_heads * D)
+    q_seq, q_tok = _token_strides(q, "q", shape)
+    kv = (nseq, ntok, cache.n_kv_heads * D)
+    kv_seq, kv_tok = _token_strides(k_new, "k_new", kv)
+    if _token_strides(v_new, "v_new", kv) != (kv_seq, kv_tok):
         raise ValueError("k_new and v_new must have the same strides")
-    if mask is not None:
-        _need(mask, "mask", torch.int64, (cache.n_seq, ntok))
-    if n_tok is not None:
-        cache._ints(n_tok, "n_tok")
     if out is None:
-        out = torch.empty((cache.n_seq, ntok, n_heads * D), dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.float32, (cache.n_seq, ntok, n_heads * D))
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = epq_attention_tree_workspace(cache, n_heads, ntok)
-    o = AttentionTreeOpts(_addr(mask), _addr(n_tok), ld(q, 1), ld(q, 0), ld(k_new, 1), ld(k_new, 0))
-    _check("epq_attention_tree", lib.epq_attention_tree(
-        ctypes.byref(cache._p), int(layer), _ptr(q), _ptr(k_new), _ptr(v_new), n_heads, ntok, float(scale),
-        ctypes.byref(o), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok)),
+                          None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq),
+                          q_tok, q_seq, kv_tok, kv_seq)
+    st = _lib.epq_attention_tree(cache._ref, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), n_heads, ntok,
+                                 scale, ctypes.byref(o), _need(out, "out", torch.float32, shape),
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if st:
+        raise EpqError("epq_attention_tree", st)
     return out
 
 
@@ -549,24 +569,25 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     like logits -> (path int32 [n_seq, ntok], n_accept int32 [n_seq], next_token int32 [n_seq], lse float32
     [n_seq, ntok])."""
     lib = load()
-    _need(logits, "logits", torch.float32, (None, None, None))
-    nseq, ntok, vocab = logits.shape
-    _need(tokens, "tokens", torch.int32, (nseq, ntok)), _need(parent, "parent", torch.int32, (nseq, ntok))
-    if u is not None:
-        _need(u, "u", torch.float32, (nseq, ntok))
-    if draft is not None:
-        _need(draft, "draft", torch.float32, logits.shape)
-    if n_tok is not None:
-        _need(n_tok, "n_tok", torch.int32, (nseq,))
-    new = lambda t, name, dt, shape: (torch.empty(shape, dtype=dt, device=logits.device) if t is None  # noqa: E731
-                                      else _need(t, name, dt, shape))
-    path = new(path, "path", torch.int32, (nseq, ntok))
-    n_accept, next_token = new(n_accept, "n_accept", torch.int32, (nseq,)), new(next_token, "next_token", torch.int32, (nseq,))
-    lse = new(lse, "lse", torch.float32, (nseq, ntok))
+    i32, f32, dev = torch.int32, torch.float32, logits.device
+    if logits.dim() != 3:
+        raise ValueError("logits must be [n_seq, ntok, vocab]")
+    full = logits.shape
+    nseq, ntok, vocab = full
+    tree, each = (nseq, ntok), (nseq,)
+    path = torch.empty(tree, dtype=i32, device=dev) if path is None else path
+    n_accept = torch.empty(each, dtype=i32, device=dev) if n_accept is None else n_accept
+    next_token = torch.empty(each, dtype=i32, device=dev) if next_token is None else next_token
+    lse = torch.empty(tree, dtype=f32, device=dev) if lse is None else lse
     if workspace is None:
         workspace = epq_verify_tree_workspace(logits)
-    o = VerifyOpts(_addr(draft), _addr(n_tok), float(temperature), 0, 0)
-    _check("epq_verify_tree", lib.epq_verify_tree(
-        _ptr(logits), vocab, _ptr(tokens), _ptr(parent), _ptr(u), nseq, ntok, ctypes.byref(o), _ptr(path),
-        _ptr(n_accept), _ptr(next_token), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(stream)))
+    o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full),
+                   None if n_tok is None else _need(n_tok, "n_tok", i32, each), temperature, 0, 0)
+    st = lib.epq_verify_tree(
+        _need(logits, "logits", f32, full), vocab, _need(tokens, "tokens", i32, tree), _need(parent, "parent", i32, tree),
+        None if u is None else _need(u, "u", f32, tree), nseq, ntok, ctypes.byref(o), _need(path, "path", i32, tree),
+        _need(n_accept, "n_accept", i32, each), _need(next_token, "next_token", i32, each), _need(lse, "lse", f32, tree),
+        workspace.data_ptr(), workspace.numel(), _stream(stream))
+    if st:
+        raise EpqError("epq_verify_tree", st)
     return path, n_accept, next_token, lse

@@ -705,12 +705,11 @@ template <int NB, int MT>
 cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t s) {
   using L = Plan<NB, MT>;
   auto k = tree_kernel<NB, MT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::kSmem));
-  if (e != cudaSuccess) return e;
+  static LaunchOnce once;
   int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, L::kThreads, L::kSmem);
+  cudaError_t e = once.prepare(dev.device, k, L::kThreads, L::kSmem, false, &per_sm);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(kMaxCtas, dev.sm_count * std::max(per_sm, 1));
+  const int grid = std::min(kMaxCtas, dev.sm_count * per_sm);
   e = launch_pdl(k, dim3(grid), dim3(L::kThreads), L::kSmem, s, p);
   if (e != cudaSuccess) return e;
   const int rows = p.v.n_kv * p.ntok * p.group;

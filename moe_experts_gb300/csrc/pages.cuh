@@ -2,6 +2,8 @@
 // addressing.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace epq {
@@ -55,6 +57,32 @@ inline epq_status pages_view(const epq_pages *p, PagesView *v) {
   v->layer_bytes = v->page_bytes * p->n_pages;
   return EPQ_OK;
 }
+
+// What a kernel's launch needs to know or set once per device: its dynamic
+// shared-memory limit (and the opt-in to clusters of more than 8 CTAs), and
+// how many of its CTAs fit an SM.  A value is looked up once and kept.
+class LaunchOnce {
+ public:
+  template <typename K>
+  cudaError_t prepare(int device, K kernel, int threads, size_t smem, bool large_cluster, int *per_sm) {
+    std::atomic<int> &slot = known_[device];
+    int n = slot.load(std::memory_order_acquire);
+    if (n == 0) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e == cudaSuccess && large_cluster)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+      if (e != cudaSuccess) return e;
+      n = n > 0 ? n : 1;
+      slot.store(n, std::memory_order_release);
+    }
+    if (per_sm) *per_sm = n;
+    return cudaSuccess;
+  }
+
+ private:
+  std::atomic<int> known_[64] = {};  // current_device admits no more devices
+};
 
 #ifdef __CUDACC__
 // Committed length of sequence s, held to what its table can address.

@@ -485,7 +485,8 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   if (p.ld < vocab || p.draft_ld < vocab) return EPQ_ERR_SHAPE;
   if (!ws || ws_bytes < need) return EPQ_ERR_WORKSPACE;
   if (!aligned16(logits) || !aligned16(ws) || (opts && opts->draft && !aligned16(opts->draft))) return EPQ_ERR_ALIGN;
-  if (!device_ok()) return EPQ_ERR_DEVICE;
+  DeviceInfo dev;
+  if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int64_t rows = static_cast<int64_t>(n_seq) * ntok;
   p.logits = logits;
   p.draft = opts ? opts->draft : nullptr;
@@ -515,8 +516,9 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
                                                    : launch_pdl(row_stats_kernel<2>, grid, dim3(kStatThreads), 0, s, p);
   if (e != cudaSuccess) return cuda_fail(e);
   const size_t smem = 12 * static_cast<size_t>(kWalkWarps) * walk_entries(p.vocab);
-  e = cudaFuncSetAttribute(walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(walk_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  static LaunchOnce once;
+  e = once.prepare(dev.device, walk_kernel, kWalkThreads, 12 * static_cast<size_t>(kWalkWarps) * walk_entries(kMaxVocab),
+                   true, nullptr);
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchConfig_t cfg = {};
   cfg.dynamicSmemBytes = smem;
