@@ -5,10 +5,10 @@
 // over the committed positions and the drafted tokens that token i's mask
 // names.  The rows of one (sequence, key/value head) are its tokens times its
 // `group` query heads (row r: token r / group, head r % group); a row tile is
-// 16 MT of them.
+// 16 WM of them.
 //
 // One pass over the positions in tiles of 64, a running maximum per row, and
-// both products on the tensor cores (mma.sync m16n8k16, fp16 operands, float32
+// both products on the tensor cores (mma.sync m16n8k16, 16-bit operands, float32
 // sums) without giving up float32 accuracy:
 //   scores   the int8 codes of a key are exact in fp16; a query row is scaled
 //            by a power of two and split into two fp16 parts (2^-22 of the
@@ -16,17 +16,22 @@
 //            block is multiplied by that key's block factor in float32.
 //   values   the codes are again the operand; the factor of (position, block)
 //            goes to the other side: warp b owns the 32 columns of block b and
-//            multiplies the weights by that block's factors before it splits
-//            the product's 24 bits into three bf16 parts (exact, and with
-//            float32's range: two fp16 parts would lose a weight below 2^-39
-//            of the largest, which shows where the larger ones meet a code 0).
+//            multiplies the weights by that block's factors.  A weight is kept
+//            as two fp16 parts, so a product is three half2 operations: its
+//            rounded value, what the rounding lost (exact), plus the second
+//            part's product: 2^-22 of it, or 2^-39 of the largest one.  That
+//            floor would show where every larger weight meets a code 0, so it
+//            is only used where a row has at least 12 weights within 2^-16 of
+//            its largest; the others (and tiles with drafted tokens, whose
+//            factors may not be finite) take 16 positions at a time with
+//            float32 products in three bf16 parts, which lose nothing.
 // Work: the tiles of all (sequence, head, row tile) items in a row, cut into
 // equal shares, one per CTA.  A CTA's part of an item that it does not hold
 // whole goes to the workspace (maximum, sum, unnormalised output), and a
 // second launch joins the parts in the order of their positions.
-// A producer warp streams the rows of a tile (contiguous within a page) with
-// bulk copies into a ring of shared-memory stages; the D/32 consumer warps
-// compute the scores of 64 / (D/32) positions each, exchange the weights
+// Warp 0 streams the rows of a tile (contiguous within a page) with bulk
+// copies into a ring of three stages, two tiles ahead; the warps of a row
+// group compute the scores of 64 / (D/32) positions each, exchange the weights
 // through shared memory (one barrier per tile) and accumulate 32 columns each.
 // The new rows are quantized into their tile by the CTAs that read it (the
 // one of row tile 0 also stores them in the cache).
@@ -41,10 +46,13 @@ namespace epq {
 namespace {
 
 constexpr int kMaxGroupTree = 16;
-constexpr int kTile = 64;        // positions of a tile
+constexpr int kTile = 64;  // positions of a tile
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 512;
 constexpr int kJoinThreads = 128;
+constexpr float kUp = 14.0f;         // log2 of the largest weight of a row as it is held
+constexpr float kWeighty = 0.25f;    // a weight that counts: 2^-16 of the largest
+constexpr float kWeightyMin = 3.0f;  // of them, in each of a row's four lanes
 
 struct TreeParams {
   PagesView v;
@@ -55,7 +63,8 @@ struct TreeParams {
   int layer, n_heads, group, ntok;
   float scale;
   float *out;
-  float *parts;     // workspace: [2 per CTA][rows][D + 2]
+  long long *before;  // workspace: tiles of the sequences before each, then their total
+  float *parts;       // workspace: [2 per CTA][rows][D + 4]
   unsigned *err;
 };
 
@@ -73,6 +82,17 @@ __device__ __forceinline__ uint64_t token_mask(const TreeParams &p, int s, int i
   return n >= 64 ? m : m & ((1ull << n) - 1);
 }
 
+// Shares of `total` tiles: CTA c holds [c share + min(c, rest), ...).
+struct Shares {
+  long long share, rest;
+  __device__ Shares(long long total, int ctas) : share(total / ctas), rest(total % ctas) {}
+  __device__ long long begin(long long c) const { return c * share + (c < rest ? c : rest); }
+  __device__ int holder(long long x) const {
+    const long long cut = rest * (share + 1);
+    return static_cast<int>(x < cut ? x / (share + 1) : rest + (x - cut) / share);
+  }
+};
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -80,18 +100,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t 
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// Codes: a byte u = code + 128 under the exponent byte 0x64 is the half 1024 + u.
-__device__ __forceinline__ uint32_t codes_to_half2(uint32_t x, uint32_t sel) {
-  const uint32_t h = __byte_perm(x, 0x64646464u, sel);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), __half2half2(__ushort_as_half(0x6480)));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
+// Two codes as fp16: a byte u = code + 128 under the byte 0x64 is the half
+// 1024 + u.
+__device__ __forceinline__ uint32_t codes_to_half2(uint32_t x, uint32_t sel) {
+  return as_bits(__hsub2(as_half2(__byte_perm(x, 0x64646464u, sel)), __half2half2(__ushort_as_half(0x6480))));
 }
 
 // Two codes (bytes c of x picked by sel) as bf16: under the byte 0x43 the low
@@ -116,10 +138,6 @@ __device__ __forceinline__ void split_bf162(float x, float y, uint32_t &p1, uint
   p3 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
 }
 
-__device__ __forceinline__ float f16_at(const uint8_t *p) {
-  return __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short *>(p)));
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -129,8 +147,12 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 // x, y -> fp16 parts: first = rounded, second = the rest rounded.
 __device__ __forceinline__ void split_half2(float x, float y, uint32_t &first, uint32_t &rest) {
   first = pack_half2(x, y);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&first));
+  const float2 f = __half22float2(as_half2(first));
   rest = pack_half2(x - f.x, y - f.y);
+}
+
+__device__ __forceinline__ float f16_at(const uint8_t *p) {
+  return __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short *>(p)));
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -139,51 +161,71 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// What a work item is: rows [16 MT rt, ...) of head h of sequence s.
+// What a work item is: rows [16 WM rt, ...) of head h of sequence s.
 struct Item {
   int s, h, rt, tiles, len, n;
 };
 
-template <int NB, int MT>
+template <int NB, int WM>
 struct Plan {
   static constexpr int kD = 32 * NB;
   static constexpr int kRow = kD + kD / 16;
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kConsumers = 32 * NB;
-  static constexpr int kThreads = kConsumers + 32;
+  static constexpr int kRows = 16 * WM;
+  static constexpr int kWarps = NB * WM;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kKeys = kTile / NB;  // positions whose scores a warp computes
   static constexpr int kNT = kKeys / 8;
   static constexpr uint32_t kStageBytes = 2u * kTile * kRow;
+  static constexpr int kPart = kRows * (kD + 4);  // floats of a part
   // shared memory (bytes)
   static constexpr uint32_t oStage = 0;
-  static constexpr uint32_t oQ = oStage + kStages * kStageBytes;       // query fragments, two parts
-  static constexpr uint32_t oW = oQ + 2u * 2u * kRows * kD;            // [2][rows][64] weights
-  static constexpr uint32_t oMax = oW + 2u * 4u * kRows * kTile;       // [2][NB][rows] tile maxima
-  static constexpr uint32_t oSum = oMax + 2u * 4u * NB * kRows;        // [NB][rows]
-  static constexpr uint32_t oMask = oSum + 4u * NB * kRows;            // [rows] mask words
-  static constexpr uint32_t oScale = oMask + 8u * kRows;               // [rows] score factors (log2 units)
-  static constexpr uint32_t oTiles = oScale + 4u * kRows;              // [n_seq + 1] tiles before a sequence
-  static constexpr uint32_t oBar = oTiles + 8u * (kMaxSeq + 8);        // full, empty
-  static constexpr uint32_t oMiss = oBar + 16u * kStages;              // [stages] missing pieces
+  static constexpr uint32_t oQ = oStage + kStages * kStageBytes;    // query fragments, two parts
+  static constexpr uint32_t oW = oQ + 2u * 2u * kRows * kD;         // [2][rows][64] weights
+  static constexpr uint32_t oMax = oW + 2u * 4u * kRows * kTile;    // [2][NB][rows] tile maxima
+  static constexpr uint32_t oSum = oMax + 2u * 4u * NB * kRows;     // [NB][rows]
+  static constexpr uint32_t oMask = oSum + 4u * NB * kRows;         // [rows] mask words
+  static constexpr uint32_t oScale = oMask + 8u * kRows;            // [rows] score factors (log2 units)
+  static constexpr uint32_t oTiles = oScale + 4u * kRows;           // [n_seq + 1] tiles before a sequence, begin, end
+  static constexpr uint32_t oBar = oTiles + 8u * (kMaxSeq + 8);     // full
+  static constexpr uint32_t oFactor = oBar + 8u * (kStages + 1);    // [2][NB] largest value factor
+  static constexpr uint32_t oWide = oFactor + 2u * 4u * NB;         // [2][warps] three parts wanted
+  static constexpr uint32_t oMiss = oWide + 2u * 4u * kWarps;       // [stages] missing pieces
   static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
 
-template <int NB, int MT>
-__global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3 : 2) : 1) tree_kernel(const __grid_constant__ TreeParams p) {
-  using L = Plan<NB, MT>;
-  constexpr int kRows = L::kRows, kD = L::kD, kRow = L::kRow, kNT = L::kNT;
+// Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127), codes rint(x /
+// factor) in +-127, 0 for a zero factor) of 4 elements a lane, 8 lanes a block.
+__device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
+  const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
+  float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
+#pragma unroll
+  for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
+  const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
+  const float d = __half2float(dh);
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
+    word |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xffu) << (8 * j);
+  }
+  *factor = dh;
+  return word;
+}
+
+template <int NB, int WM>
+__global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3 : 2) : 1)
+    tree_kernel(const __grid_constant__ TreeParams p) {
+  using L = Plan<NB, WM>;
+  constexpr int kRows = L::kRows, kD = L::kD, kRow = L::kRow, kNT = L::kNT, kOwn = 2 * kNT;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int wm = warp / NB, wb = warp % NB;  // rows 16 wm ..., positions wb kKeys ..., columns 32 wb ...
   const int g = lane >> 2, t = lane & 3;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::oBar);
-  uint64_t *empty = full + kStages;
   long long *before = reinterpret_cast<long long *>(smem + L::oTiles);
   unsigned *miss = reinterpret_cast<unsigned *>(smem + L::oMiss);
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], NB);
-    }
+    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   pdl_launch_dependents();
@@ -195,17 +237,15 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3
     *nrt = (n * p.group + kRows - 1) / kRows;
     return sequence_tiles(p, s, n);
   };
-  for (int s = tid; s < p.v.n_seq; s += L::kThreads) {
-    int nrt;
-    const int tiles = rows_tiles(s, &nrt);
-    before[s + 1] = static_cast<long long>(tiles) * nrt * p.v.n_kv;
-  }
-  if (tid == 0) before[0] = 0;
-  __syncthreads();
   if (warp == 0) {
     long long run = 0;
     for (int s0 = 0; s0 < p.v.n_seq; s0 += 32) {
-      long long x = s0 + lane < p.v.n_seq ? before[s0 + lane + 1] : 0;
+      long long x = 0;
+      if (s0 + lane < p.v.n_seq) {
+        int nrt;
+        const int tiles = rows_tiles(s0 + lane, &nrt);
+        x = static_cast<long long>(tiles) * nrt * p.v.n_kv;
+      }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -214,18 +254,31 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3
       if (s0 + lane < p.v.n_seq) before[s0 + lane + 1] = run + x;
       run += __shfl_sync(0xffffffffu, x, 31);
     }
+    if (lane == 0) {
+      before[0] = 0;
+      const int ctas = static_cast<int>(run < gridDim.x ? run : gridDim.x);
+      long long b = 0, e = 0;
+      if (blockIdx.x < ctas) {
+        const Shares sh(run, ctas);
+        b = sh.begin(blockIdx.x);
+        e = sh.begin(blockIdx.x + 1);
+      }
+      before[p.v.n_seq + 1] = b;
+      before[p.v.n_seq + 2] = e;
+    }
   }
   __syncthreads();
-  const long long total = before[p.v.n_seq];
-  const long long ctas = gridDim.x < total ? gridDim.x : total;
+  if (blockIdx.x == 0)  // for the join
+    for (int s = tid; s <= p.v.n_seq; s += L::kThreads) p.before[s] = before[s];
   // tokens beyond a sequence's tree: 0
-  for (int r = blockIdx.x; r < p.v.n_seq * p.ntok; r += gridDim.x) {
-    if (r % p.ntok < tree_size(p, r / p.ntok)) continue;
-    float4 *o = reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(r) * p.n_heads * kD);
-    for (int i = tid; i < p.n_heads * kD / 4; i += L::kThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  if (blockIdx.x >= ctas) return;
-  const long long begin = blockIdx.x * total / ctas, end = (blockIdx.x + 1) * total / ctas;
+  if (p.n_tok)
+    for (int r = blockIdx.x; r < p.v.n_seq * p.ntok; r += gridDim.x) {
+      if (r % p.ntok < tree_size(p, r / p.ntok)) continue;
+      float4 *o = reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(r) * p.n_heads * kD);
+      for (int i = tid; i < p.n_heads * kD / 4; i += L::kThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  const long long begin = before[p.v.n_seq + 1], end = before[p.v.n_seq + 2];
+  if (begin == end) return;
   // the item that holds tile x, and the tile's place in it
   auto find = [&](long long x, Item &it) {
     int lo = 0, hi = p.v.n_seq - 1;
@@ -240,54 +293,65 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3
     it.len = seq_length(p.v, lo);
     it.n = tree_size(p, lo);
     const long long rel = x - before[lo];
-    const int k = static_cast<int>(rel / it.tiles);
+    int k, tile;
+    if (rel >> 31) {
+      k = static_cast<int>(rel / it.tiles);
+      tile = static_cast<int>(rel % it.tiles);
+    } else {
+      k = static_cast<int>(rel) / it.tiles;
+      tile = static_cast<int>(rel) - k * it.tiles;
+    }
     it.h = k / nrt;
-    it.rt = k % nrt;
-    return static_cast<int>(rel % it.tiles);
+    it.rt = k - it.h * nrt;
+    return tile;
   };
   const int piece_rows = min(p.v.P, kTile);
 
-  // ================================================================ producer
-  if (warp == NB) {
-    bool ok = true;
-    uint32_t k = 0;
-    for (long long x = begin; x < end;) {
-      Item it;
-      const int first = find(x, it);
-      const int last = static_cast<int>(min(static_cast<long long>(it.tiles), first + (end - x)));
-      x += last - first;
-      for (int tile = first; tile < last; ++tile, ++k) {
-        const int st = k % kStages;
-        if (k >= kStages && ok)
-          ok = warp_wait(&empty[st], (k / kStages - 1) & 1, p.err, DEVERR_EMPTY_WAIT, k);
-        // lane = 2 * piece + plane
-        const int piece = lane >> 1, c = lane & 1;
-        const int pos = tile * kTile + piece * piece_rows;
-        const int rows = piece < kTile / piece_rows ? min(max(it.len - pos, 0), piece_rows) : 0;
-        const int page = rows > 0 ? seq_page(p.v, it.s, pos / p.v.P) : 0;
-        const uint32_t bytes = rows > 0 && page >= 0 ? (static_cast<uint32_t>(rows) * kRow) & ~15u : 0u;
-        const unsigned lost = __ballot_sync(0xffffffffu, page < 0);
-        if (lost && lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(it.s));
-        const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
-        if (lane == 0) {
-          miss[st] = lost;
-          if (all) mbar_arrive_expect_tx(&full[st], all);
-          else mbar_arrive(&full[st]);
-        }
-        __syncwarp();
-        if (bytes)
-          bulk_g2s(smem + L::oStage + st * L::kStageBytes + (c * kTile + piece * piece_rows) * kRow,
-                   page_row(p.v, p.layer, page, it.h, c, pos % p.v.P), bytes, &full[st]);
-      }
+  // ---------------------------------------------------------------- loads
+  // Warp 0 copies a tile's committed rows: lane 2 piece + plane takes the rows
+  // of one page (at most four of them in a tile).  The page ids are read a
+  // tile earlier than they are needed.
+  Item load_it = {};
+  int load_tile = 0, load_rows = 0, load_page = 0;
+  long long load_x = begin;
+  uint32_t load_k = 0;
+  auto look_ahead = [&]() {
+    if (load_x >= end) return;
+    if (load_x == begin || load_tile == load_it.tiles) load_tile = find(load_x, load_it);
+    const int pos = load_tile * kTile + (lane >> 1) * piece_rows;
+    load_rows = (lane >> 1) < kTile / piece_rows ? min(max(load_it.len - pos, 0), piece_rows) : 0;
+    load_page = load_rows > 0 ? p.v.table[static_cast<int64_t>(load_it.s) * p.v.max_pages + pos / p.v.P] : 0;
+  };
+  auto load = [&]() {
+    if (load_x >= end) return;
+    const int st = load_k % kStages, piece = lane >> 1, c = lane & 1;
+    const bool page_ok = load_page >= 0 && load_page < p.v.n_pages;
+    const uint32_t bytes = load_rows > 0 && page_ok ? (static_cast<uint32_t>(load_rows) * kRow) & ~15u : 0u;
+    const unsigned lost = __ballot_sync(0xffffffffu, !page_ok);
+    if (lost && lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(load_it.s));
+    const uint32_t all = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) {
+      miss[st] = lost;
+      if (all) mbar_arrive_expect_tx(&full[st], all);
+      else mbar_arrive(&full[st]);
     }
-    // every copy has landed before the CTA ends
-    for (uint32_t i = k > kStages ? k - kStages : 0; i < k; ++i)
-      warp_wait(&full[i % kStages], (i / kStages) & 1, p.err, DEVERR_DRAIN_WAIT, i);
-    return;
+    __syncwarp();
+    if (bytes)
+      bulk_g2s(smem + L::oStage + st * L::kStageBytes + (c * kTile + piece * piece_rows) * kRow,
+               page_row(p.v, p.layer, load_page, load_it.h, c, (load_tile * kTile + piece * piece_rows) % p.v.P), bytes,
+               &full[st]);
+    ++load_tile;
+    ++load_x;
+    ++load_k;
+  };
+  if (warp == 0) {
+    look_ahead();
+    load();
+    look_ahead();
+    load();
+    look_ahead();
   }
 
-  // ================================================================ consumers
-  auto sync = [&]() { named_sync(1, L::kConsumers); };
   uint64_t *row_mask = reinterpret_cast<uint64_t *>(smem + L::oMask);
   float *row_scale = reinterpret_cast<float *>(smem + L::oScale);
   float *sums = reinterpret_cast<float *>(smem + L::oSum);
@@ -302,124 +366,109 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3
     const int n_rows = min(kRows, it.n * p.group - it.rt * kRows);
 
     // -------------------------------------------------------------- queries
-    // A warp takes a row: scaled by a power of two so that the largest entry
+    // A warp takes rows: scaled by a power of two so that the largest entry
     // is in [2^13, 2^14), split, stored as MMA A fragments (element 16 ks +
-    // 4 t + e of a block pair: lane t of the row, register e / 2).
-    for (int r = warp; r < kRows; r += NB) {
-      const int row = it.rt * kRows + r, i = row / p.group;
-      float4 q[NB / 4];
-      float a = 0.0f;
+    // 4 t + e: lane t of the row, register e / 2).
+    {
+      constexpr int kPer = 16 / NB;  // rows of a warp
+      float4 q[kPer][NB / 4];
 #pragma unroll
-      for (int c = 0; c < NB / 4; ++c) {
-        q[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n_rows)
-          q[c] = *reinterpret_cast<const float4 *>(p.q + it.s * p.q_seq_ld + i * p.q_ld +
-                                                   (it.h * p.group + row % p.group) * kD + 128 * c + 4 * lane);
-        a = fmaxf(fmaxf(a, fmaxf(fabsf(q[c].x), fabsf(q[c].y))), fmaxf(fabsf(q[c].z), fabsf(q[c].w)));
-      }
-      a = warp_absmax(a);
-      const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -100), 127);
-      const float up = exp2i(13 - e);
-      if (lane == 0) {
-        row_scale[r] = p.scale * 1.4426950408889634f * exp2i(e - 13);
-        row_mask[r] = r < n_rows ? token_mask(p, it.s, i, it.n) : 0;
+      for (int u = 0; u < kPer; ++u) {
+        const int r = warp + L::kWarps * u, row = it.rt * kRows + r, i = row / p.group;
+#pragma unroll
+        for (int c = 0; c < NB / 4; ++c)
+          q[u][c] = r < n_rows ? *reinterpret_cast<const float4 *>(p.q + it.s * p.q_seq_ld + i * p.q_ld +
+                                                                   (it.h * p.group + row % p.group) * kD + 128 * c +
+                                                                   4 * lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane == 0) row_mask[r] = r < n_rows ? token_mask(p, it.s, i, it.n) : 0;
       }
 #pragma unroll
-      for (int c = 0; c < NB / 4; ++c) {
-        uint32_t h0, h1, l0, l1;
-        split_half2(q[c].x * up, q[c].y * up, h0, l0);
-        split_half2(q[c].z * up, q[c].w * up, h1, l1);
-        // float4 index 32 c + lane = 4 (16-element step) + t
-        const int step = 8 * c + (lane >> 2);
-        uint32_t *f = reinterpret_cast<uint32_t *>(smem + L::oQ) +
-                      (((r >> 4) * (2 * NB) + step) * 2 * 32 + (r & 7) * 4 + t) * 4 + ((r >> 3) & 1);
-        f[0] = h0;
-        f[2] = h1;
-        f[128] = l0;
-        f[130] = l1;
+      for (int u = 0; u < kPer; ++u) {
+        const int r = warp + L::kWarps * u;
+        float a = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NB / 4; ++c)
+          a = fmaxf(fmaxf(a, fmaxf(fabsf(q[u][c].x), fabsf(q[u][c].y))), fmaxf(fabsf(q[u][c].z), fabsf(q[u][c].w)));
+        a = warp_absmax(a);
+        const int e = min(max(static_cast<int>(__float_as_uint(a) >> 23) - 127, -100), 127);
+        const float up = exp2i(13 - e);
+        if (lane == 0) row_scale[r] = p.scale * 1.4426950408889634f * exp2i(e - 13);
+#pragma unroll
+        for (int c = 0; c < NB / 4; ++c) {
+          uint32_t h0, h1, l0, l1;
+          split_half2(q[u][c].x * up, q[u][c].y * up, h0, l0);
+          split_half2(q[u][c].z * up, q[u][c].w * up, h1, l1);
+          // float4 index 32 c + lane = 4 (16-element step) + t
+          uint32_t *f = reinterpret_cast<uint32_t *>(smem + L::oQ) +
+                        (((r >> 4) * (2 * NB) + 8 * c + g) * 2 * 32 + (r & 7) * 4 + t) * 4 + ((r >> 3) & 1);
+          f[0] = h0;
+          f[2] = h1;
+          f[128] = l0;
+          f[130] = l1;
+        }
       }
     }
-    sync();
+    __syncthreads();
 
-    float o[MT][4][4] = {};
-    float m_run[MT][2], l_run[MT][2], c_row[MT][2];
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        m_run[a][b] = -INFINITY;
-        l_run[a][b] = 0.0f;
-        c_row[a][b] = row_scale[16 * a + 8 * b + g];
-      }
-    float s[MT][2][2 * kNT];  // scores of rows g, g + 8 at the lane's 2 kNT positions
+    float o[4][4] = {}, s[2][kOwn];  // s: scores of rows g, g + 8 at the lane's positions
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {}, weighty[2] = {};
+    const float c_row[2] = {row_scale[16 * wm + g], row_scale[16 * wm + 8 + g]};
+    float unit = 1.0f, d_min = 0.0f;  // power of two on the value factors; smallest factor of the warp's positions
 
     // Scores of tile `tile` (pipeline step kk) into s, its row maxima into oMax.
     auto scores = [&](int tile, uint32_t kk) {
       const int st = kk % kStages;
       uint8_t *kt = smem + L::oStage + st * L::kStageBytes, *vt = kt + kTile * kRow;
-      if (ok) ok = warp_wait(&full[st], (kk / kStages) & 1, p.err, DEVERR_FULL_WAIT, kk);
+      if (ok) ok = mbar_wait_poll(&full[st], (kk / kStages) & 1, p.err, DEVERR_FULL_WAIT, kk);
       const int t0 = tile * kTile;
       const unsigned lost = miss[st];
       const bool special = t0 + kTile > it.len || lost;
       if (special) {
-        // new rows, the end of an odd number of committed rows (a bulk copy
-        // moves 16 bytes), and rows that hold nothing (their factors are 0)
-        for (int rr = warp; rr < 2 * kTile; rr += NB) {
+        // rows that hold nothing: their factors are 0
+        for (int i = tid; i < 2 * kTile; i += L::kThreads) {
+          const int r = i >> 1, pos = t0 + r;
+          if (pos >= it.len + it.n || (pos < it.len && lost >> (2 * (r / piece_rows)) & 1)) {
+            uint2 *f = reinterpret_cast<uint2 *>((i & 1 ? vt : kt) + r * kRow);
+#pragma unroll
+            for (int b = 0; b < NB / 4; ++b) f[b] = make_uint2(0, 0);
+          } else if (pos == it.len - 1 && ((r % piece_rows + 1) * kRow & 8)) {
+            // the end of an odd number of rows (a bulk copy moves 16 bytes)
+            *reinterpret_cast<uint2 *>((i & 1 ? vt : kt) + r * kRow + kRow - 8) = *reinterpret_cast<const uint2 *>(
+                page_row(p.v, p.layer, seq_page(p.v, it.s, pos / p.v.P), it.h, i & 1, pos % p.v.P) + kRow - 8);
+          }
+        }
+        // the new rows
+        const int r0 = max(it.len - t0, 0), r1 = min(it.len + it.n - t0, kTile);
+#pragma unroll 2
+        for (int rr = 2 * r0 + warp; rr < 2 * r1; rr += L::kWarps) {
           const int r = rr >> 1, c = rr & 1, pos = t0 + r;
-          uint8_t *dst = (c ? vt : kt) + r * kRow;
-          const bool gone = lost >> (2 * (r / piece_rows)) & 1;
-          if (pos < it.len && !gone) {
-            if (pos == it.len - 1 && ((r % piece_rows + 1) * kRow & 8) && lane == 0)
-              *reinterpret_cast<uint2 *>(dst + kRow - 8) = *reinterpret_cast<const uint2 *>(
-                  page_row(p.v, p.layer, seq_page(p.v, it.s, pos / p.v.P), it.h, c, pos % p.v.P) + kRow - 8);
-          } else if (pos >= it.len && pos < it.len + it.n) {
-            const int i = pos - it.len;
-            uint8_t *row = nullptr;
-            if (it.rt == 0) {
-              const int page = seq_page(p.v, it.s, pos / p.v.P);
-              if (page >= 0) row = page_row(p.v, p.layer, page, it.h, c, pos % p.v.P);
-              else if (lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(it.s));
+          const float *src = (c ? p.v_new : p.k_new) + it.s * p.kv_seq_ld + (pos - it.len) * p.kv_ld + it.h * kD;
+          uint8_t *dst = (c ? vt : kt) + r * kRow, *row = nullptr;
+          if (it.rt == 0) {
+            const int page = seq_page(p.v, it.s, pos / p.v.P);
+            if (page >= 0) row = page_row(p.v, p.layer, page, it.h, c, pos % p.v.P);
+            else if (lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(it.s));
+          }
+#pragma unroll
+          for (int b = 0; b < NB / 4; ++b) {
+            __half d;
+            const uint32_t word = quantize4(*reinterpret_cast<const float4 *>(src + 128 * b + 4 * lane), &d);
+            const int at = kD / 16 + 128 * b + 4 * lane, fat = 2 * (4 * b + (lane >> 3));
+            *reinterpret_cast<uint32_t *>(dst + at) = word;
+            if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(dst + fat) = __half_as_ushort(d);
+            if (row) {
+              *reinterpret_cast<uint32_t *>(row + at) = word;
+              if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(row + fat) = __half_as_ushort(d);
             }
-            const float *src = (c ? p.v_new : p.k_new) + it.s * p.kv_seq_ld + i * p.kv_ld + it.h * kD;
-#pragma unroll
-            for (int q4 = 0; q4 < NB / 4; ++q4) {
-              // Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127),
-              // codes rint(x / factor) in +-127, 0 for a zero factor); 8 lanes
-              // hold a block
-              const float4 xv = *reinterpret_cast<const float4 *>(src + 128 * q4 + 4 * lane);
-              const float e[4] = {__fadd_rn(xv.x, 0.0f), __fadd_rn(xv.y, 0.0f), __fadd_rn(xv.z, 0.0f),
-                                  __fadd_rn(xv.w, 0.0f)};
-              float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
-#pragma unroll
-              for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-              const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
-              const float d = __half2float(dh);
-              uint32_t word = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
-                word |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xffu) << (8 * j);
-              }
-              const int at = kD / 16 + 128 * q4 + 4 * lane, fat = 2 * (4 * q4 + (lane >> 3));
-              *reinterpret_cast<uint32_t *>(dst + at) = word;
-              if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(dst + fat) = __half_as_ushort(dh);
-              if (row) {
-                *reinterpret_cast<uint32_t *>(row + at) = word;
-                if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(row + fat) = __half_as_ushort(dh);
-              }
-            }
-          } else if (lane < NB) {
-            reinterpret_cast<uint16_t *>(dst)[lane] = 0;
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        sync();
+        __syncthreads();
       }
-      const uint8_t *kw = kt + warp * L::kKeys * kRow;
+      const uint8_t *kw = kt + wb * L::kKeys * kRow;
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int j = 0; j < 2 * kNT; ++j) s[a][0][j] = s[a][1][j] = 0.0f;
+      for (int j = 0; j < kOwn; ++j) s[0][j] = s[1][j] = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t kb[kNT][4];
@@ -433,261 +482,330 @@ __global__ void __launch_bounds__(Plan<NB, MT>::kThreads, NB == 4 ? (MT == 1 ? 3
           kb[j][2] = codes_to_half2(w1, 0x4140);
           kb[j][3] = codes_to_half2(w1, 0x4342);
         }
-        float d[2 * kNT];  // factors of the lane's positions 2 kNT t ...
+        float acc[kNT][4] = {};
 #pragma unroll
-        for (int j = 0; j < 2 * kNT; ++j) d[j] = f16_at(kw + (2 * kNT * t + j) * kRow + 2 * b);
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          float acc[kNT][4] = {};
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            const uint4 *f = reinterpret_cast<const uint4 *>(smem + L::oQ) + (a * (2 * NB) + 2 * b + ks) * 64 + lane;
-            const uint4 hi = f[0], lo = f[32];
-#pragma unroll
-            for (int j = 0; j < kNT; ++j) {
-              mma_f16(acc[j], hi, kb[j][2 * ks], kb[j][2 * ks + 1]);
-              mma_f16(acc[j], lo, kb[j][2 * ks], kb[j][2 * ks + 1]);
-            }
-          }
+        for (int ks = 0; ks < 2; ++ks) {
+          const uint4 *f = reinterpret_cast<const uint4 *>(smem + L::oQ) + (wm * (2 * NB) + 2 * b + ks) * 64 + lane;
+          const uint4 hi = f[0], lo = f[32];
 #pragma unroll
           for (int j = 0; j < kNT; ++j) {
-            s[a][0][j] = fmaf(d[j], acc[j][0], s[a][0][j]);
-            s[a][0][kNT + j] = fmaf(d[kNT + j], acc[j][1], s[a][0][kNT + j]);
-            s[a][1][j] = fmaf(d[j], acc[j][2], s[a][1][j]);
-            s[a][1][kNT + j] = fmaf(d[kNT + j], acc[j][3], s[a][1][kNT + j]);
+            mma_f16(acc[j], hi, kb[j][2 * ks], kb[j][2 * ks + 1]);
+            mma_f16(acc[j], lo, kb[j][2 * ks], kb[j][2 * ks + 1]);
           }
+        }
+        float d[kOwn];  // factors of the lane's positions kOwn t ...
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) d[j] = f16_at(kw + (kOwn * t + j) * kRow + 2 * b);
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+          s[0][j] = fmaf(d[j], acc[j][0], s[0][j]);
+          s[0][kNT + j] = fmaf(d[kNT + j], acc[j][1], s[0][kNT + j]);
+          s[1][j] = fmaf(d[j], acc[j][2], s[1][j]);
+          s[1][kNT + j] = fmaf(d[kNT + j], acc[j][3], s[1][kNT + j]);
         }
       }
-      float *mx = reinterpret_cast<float *>(smem + L::oMax) + ((kk & 1) * NB + warp) * kRows;
+      // the largest value factor of each of the warp's positions: their range
+      {
+        const uint8_t *r = vt + (wb * L::kKeys + (lane & (L::kKeys - 1))) * kRow;
+        __half2 a = __half2half2(__ushort_as_half(0));
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float m = -INFINITY;
-          const uint64_t may = special ? row_mask[16 * a + 8 * b + g] : 0;
-#pragma unroll
-          for (int j = 0; j < 2 * kNT; ++j) {
-            s[a][b][j] *= c_row[a][b];
-            if (special) {
-              const int r = warp * L::kKeys + 2 * kNT * t + j, i = t0 + r - it.len;
-              const bool see = i < 0 ? !(lost >> (2 * (r / piece_rows)) & 1) : i < 64 && (may >> i & 1);
-              if (!see) s[a][b][j] = -INFINITY;
-            }
-            m = fmaxf(m, s[a][b][j]);
-          }
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if (t == 0) mx[16 * a + 8 * b + g] = m;
+        for (int b = 0; b < NB / 4; ++b) {
+          const uint2 f = *reinterpret_cast<const uint2 *>(r + 8 * b);
+          a = __hmax2(a, __hmax2(__habs2(as_half2(f.x)), __habs2(as_half2(f.y))));
         }
+        const uint32_t bits = __float_as_uint(fmaxf(__low2float(a), __high2float(a)));
+        d_min = __uint_as_float(__reduce_min_sync(0xffffffffu, bits));
+        const uint32_t top = __reduce_max_sync(0xffffffffu, bits);
+        if (wm == 0 && lane == 0) reinterpret_cast<uint32_t *>(smem + L::oFactor)[(kk & 1) * NB + wb] = top;
+      }
+      float *mx = reinterpret_cast<float *>(smem + L::oMax) + ((kk & 1) * NB + wb) * kRows + 16 * wm;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) s[b][j] *= c_row[b];
+        if (special) {
+          const uint64_t may = row_mask[16 * wm + 8 * b + g];
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            const int r = wb * L::kKeys + kOwn * t + j, i = t0 + r - it.len;
+            const bool see = i < 0 ? !(lost >> (2 * (r / piece_rows)) & 1) : i < 64 && (may >> i & 1);
+            if (!see) s[b][j] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) m = fmaxf(m, s[b][j]);
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (t == 0) mx[8 * b + g] = m;
+      }
     };
 
     scores(first, k);
-    sync();
+    __syncthreads();
     for (int tile = first; tile < last; ++tile, ++k) {
       const int st = k % kStages;
+      const bool special = tile * kTile + kTile > it.len;
       // ------------------------------------------------------------ weights
-      float keep[MT][2];
-      float *w = reinterpret_cast<float *>(smem + L::oW) + (k & 1) * kRows * kTile;
+      float keep[2];  // on the sums so far (keep) and on the output so far (keep * moved)
+      float *w = reinterpret_cast<float *>(smem + L::oW) + ((k & 1) * kRows + 16 * wm) * kTile;
+      int *wide = reinterpret_cast<int *>(smem + L::oWide) + (k & 1) * L::kWarps + wm * NB;
+      float moved;
       {
-        const float *mx = reinterpret_cast<const float *>(smem + L::oMax) + (k & 1) * NB * kRows;
+        uint32_t top = 0;
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+        for (int c = 0; c < NB; ++c)
+          top = max(top, reinterpret_cast<const uint32_t *>(smem + L::oFactor)[(k & 1) * NB + c]);
+        // the largest factor of the tile times new_unit is in [1, 2)
+        const float new_unit = exp2i(min(max(127 - static_cast<int>(top >> 23), -15), 15));
+        moved = new_unit * (1.0f / unit);
+        unit = new_unit;
+        const float *mx = reinterpret_cast<const float *>(smem + L::oMax) + (k & 1) * NB * kRows + 16 * wm;
+        float e[2][kOwn];
+        bool few = special || !(d_min * unit >= kWeighty);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const int r = 16 * a + 8 * b + g;
-            float m = m_run[a][b];
+        for (int b = 0; b < 2; ++b) {
+          float m = m_run[b];
 #pragma unroll
-            for (int c = 0; c < NB; ++c) m = fmaxf(m, mx[c * kRows + r]);
-            const float ref = m == -INFINITY ? 0.0f : m;
-            keep[a][b] = exp2_approx(m_run[a][b] - ref);
-            m_run[a][b] = m;
-            float sum = 0.0f, e[2 * kNT];
+          for (int c = 0; c < NB; ++c) m = fmaxf(m, mx[c * kRows + 8 * b + g]);
+          const float ref = m == -INFINITY ? 0.0f : m - kUp;
+          keep[b] = m_run[b] == m ? 1.0f : exp2_approx(m_run[b] - m);
+          m_run[b] = m;
+          float sum = 0.0f, many = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 2 * kNT; ++j) {
-              e[j] = exp2_approx(s[a][b][j] - ref);
-              sum += e[j];
-            }
-            l_run[a][b] = fmaf(l_run[a][b], keep[a][b], sum);
-            // the 16-byte chunks of odd rows are stored with bit 2 of their index flipped
-            const int col = warp * L::kKeys + 2 * kNT * t;
-            float *dst = w + r * kTile + (col ^ ((g & 1) << 4));
-            if constexpr (kNT == 2) *reinterpret_cast<float4 *>(dst) = make_float4(e[0], e[1], e[2], e[3]);
-            else *reinterpret_cast<float2 *>(dst) = make_float2(e[0], e[1]);
+          for (int j = 0; j < kOwn; ++j) {
+            e[b][j] = exp2_approx(s[b][j] - ref);
+            sum += e[b][j];
+            many += e[b][j] >= kWeighty ? 1.0f : 0.0f;
           }
+          l_run[b] = fmaf(l_run[b], keep[b], sum);
+          weighty[b] = fmaf(weighty[b], keep[b], many);
+          few = few || weighty[b] < kWeightyMin;
+        }
+        few = __any_sync(0xffffffffu, few);
+        if (lane == 0) wide[wb] = few;
+        // the 16-byte chunks of odd rows are stored with bit 2 of their index
+        // flipped; a chunk is 4 weights, or their first parts, then the second
+        const int col = (wb * L::kKeys + kOwn * t) ^ ((g & 1) << 4);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float *dst = w + (8 * b + g) * kTile + col;
+          if constexpr (kNT == 2) {
+            if (few) {
+              *reinterpret_cast<float4 *>(dst) = make_float4(e[b][0], e[b][1], e[b][2], e[b][3]);
+            } else {
+              uint4 h;
+              split_half2(e[b][0], e[b][1], h.x, h.z);
+              split_half2(e[b][2], e[b][3], h.y, h.w);
+              *reinterpret_cast<uint4 *>(dst) = h;
+            }
+          } else {
+            if (few) {
+              *reinterpret_cast<float2 *>(dst) = make_float2(e[b][0], e[b][1]);
+            } else {
+              uint32_t h0, h1;
+              split_half2(e[b][0], e[b][1], h0, h1);
+              uint32_t *u = reinterpret_cast<uint32_t *>(dst - 2 * (t & 1)) + (t & 1);
+              u[0] = h0;
+              u[2] = h1;
+            }
+          }
+        }
       }
       if (tile + 1 < last) scores(tile + 1, k + 1);
-      sync();
+      __syncthreads();
+      // every warp is past the values of the tile before: its stage is free
+      if (warp == 0) {
+        load();
+        look_ahead();
+      }
       // ------------------------------------------------------------ values
       // The tile's products go to accumulators of their own: the tensor cores
       // round every sum towards zero, which over a long context would add up.
-      float acc[MT][4][4] = {};
+      float acc[4][4] = {};
       const uint8_t *vt = smem + L::oStage + st * L::kStageBytes + kTile * kRow;
-      const bool special = tile * kTile + kTile > it.len;  // a new row's factor may not be finite
+      const __half2 unit2 = __float2half2_rn(unit);
 #pragma unroll
       for (int kg = 0; kg < kTile / 16; ++kg) {
         const uint8_t *r = vt + (16 * kg + 4 * t) * kRow;
-        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(r + kD / 16 + 32 * warp + 4 * g);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(r + kRow + kD / 16 + 32 * warp + 4 * g);
-        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(r + 2 * kRow + kD / 16 + 32 * warp + 4 * g);
-        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(r + 3 * kRow + kD / 16 + 32 * warp + 4 * g);
-        float d[4];
+        uint32_t cw[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = f16_at(r + j * kRow + 2 * warp);
+        for (int j = 0; j < 4; ++j)
+          cw[j] = *reinterpret_cast<const uint32_t *>(r + j * kRow + kD / 16 + 32 * wb + 4 * g);
+        const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
+        const uint4 x0 = *reinterpret_cast<const uint4 *>(w + g * kTile + col);
+        const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
+        const bool mine = kNT == 2 ? wide[kg] : wide[2 * kg + (t >> 1)];  // how the lane's weights are held
+        const bool slow = kNT == 2 ? wide[kg] : wide[2 * kg] || wide[2 * kg + 1];
         // column n of MMA tile j: element 4 n + j of the block
-        uint32_t vb[4][2];
-        {
-          const uint32_t a = __byte_perm(w0, w1, 0x5140), b = __byte_perm(w0, w1, 0x7362);
-          const uint32_t c = __byte_perm(w2, w3, 0x5140), e = __byte_perm(w2, w3, 0x7362);
-          vb[0][0] = codes_to_bf162(a, 0x4140);
-          vb[1][0] = codes_to_bf162(a, 0x4342);
-          vb[2][0] = codes_to_bf162(b, 0x4140);
-          vb[3][0] = codes_to_bf162(b, 0x4342);
-          vb[0][1] = codes_to_bf162(c, 0x4140);
-          vb[1][1] = codes_to_bf162(c, 0x4342);
-          vb[2][1] = codes_to_bf162(e, 0x4140);
-          vb[3][1] = codes_to_bf162(e, 0x4342);
-        }
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          uint4 p1, p2, p3;
-          const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
-          float4 x0 = *reinterpret_cast<const float4 *>(w + (16 * a + g) * kTile + col);
-          float4 x1 = *reinterpret_cast<const float4 *>(w + (16 * a + 8 + g) * kTile + col);
-          if (special) {
-            x0 = make_float4(x0.x != 0.0f ? x0.x * d[0] : 0.0f, x0.y != 0.0f ? x0.y * d[1] : 0.0f,
-                             x0.z != 0.0f ? x0.z * d[2] : 0.0f, x0.w != 0.0f ? x0.w * d[3] : 0.0f);
-            x1 = make_float4(x1.x != 0.0f ? x1.x * d[0] : 0.0f, x1.y != 0.0f ? x1.y * d[1] : 0.0f,
-                             x1.z != 0.0f ? x1.z * d[2] : 0.0f, x1.w != 0.0f ? x1.w * d[3] : 0.0f);
-          } else {
-            x0 = make_float4(x0.x * d[0], x0.y * d[1], x0.z * d[2], x0.w * d[3]);
-            x1 = make_float4(x1.x * d[0], x1.y * d[1], x1.z * d[2], x1.w * d[3]);
+        if (!slow) {
+          uint32_t f01, f23;  // factors of positions 4 t ...
+          {
+            const uint32_t a0 = *reinterpret_cast<const unsigned short *>(r + 2 * wb);
+            const uint32_t a1 = *reinterpret_cast<const unsigned short *>(r + kRow + 2 * wb);
+            const uint32_t a2 = *reinterpret_cast<const unsigned short *>(r + 2 * kRow + 2 * wb);
+            const uint32_t a3 = *reinterpret_cast<const unsigned short *>(r + 3 * kRow + 2 * wb);
+            f01 = __byte_perm(a0, a1, 0x5410);
+            f23 = __byte_perm(a2, a3, 0x5410);
           }
-          split_bf162(x0.x, x0.y, p1.x, p2.x, p3.x);
-          split_bf162(x1.x, x1.y, p1.y, p2.y, p3.y);
-          split_bf162(x0.z, x0.w, p1.z, p2.z, p3.z);
-          split_bf162(x1.z, x1.w, p1.w, p2.w, p3.w);
+          const __half2 d01 = __hmul2(as_half2(f01), unit2), d23 = __hmul2(as_half2(f23), unit2);
+          auto times = [](uint32_t h, uint32_t l, __half2 d, uint32_t &hi, uint32_t &lo) {
+            const __half2 y = __hmul2(as_half2(h), d);
+            hi = as_bits(y);
+            lo = as_bits(__hfma2(as_half2(l), d, __hfma2(as_half2(h), d, __hneg2(y))));
+          };
+          uint4 hi, lo;
+          times(x0.x, x0.z, d01, hi.x, lo.x);
+          times(x1.x, x1.z, d01, hi.y, lo.y);
+          times(x0.y, x0.w, d23, hi.z, lo.z);
+          times(x1.y, x1.w, d23, hi.w, lo.w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) cw[j] ^= 0x80808080u;
+          const uint32_t a = __byte_perm(cw[0], cw[1], 0x5140), b = __byte_perm(cw[0], cw[1], 0x7362);
+          const uint32_t c = __byte_perm(cw[2], cw[3], 0x5140), e = __byte_perm(cw[2], cw[3], 0x7362);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            mma_bf16(acc[a][j], p1, vb[j][0], vb[j][1]);
-            mma_bf16(acc[a][j], p2, vb[j][0], vb[j][1]);
-            mma_bf16(acc[a][j], p3, vb[j][0], vb[j][1]);
+            const uint32_t v0 = codes_to_half2(j < 2 ? a : b, j & 1 ? 0x4342 : 0x4140);
+            const uint32_t v1 = codes_to_half2(j < 2 ? c : e, j & 1 ? 0x4342 : 0x4140);
+            mma_f16(acc[j], hi, v0, v1);
+            mma_f16(acc[j], lo, v0, v1);
+          }
+        } else {
+          float y0[4] = {__uint_as_float(x0.x), __uint_as_float(x0.y), __uint_as_float(x0.z), __uint_as_float(x0.w)};
+          float y1[4] = {__uint_as_float(x1.x), __uint_as_float(x1.y), __uint_as_float(x1.z), __uint_as_float(x1.w)};
+          if (kNT == 1 && !mine) {
+            auto whole = [](uint32_t h, uint32_t l, float *y) {
+              const float2 a = __half22float2(as_half2(h)), b = __half22float2(as_half2(l));
+              y[0] = a.x + b.x;
+              y[1] = a.y + b.y;
+            };
+            whole(x0.x, x0.z, y0);
+            whole(x0.y, x0.w, y0 + 2);
+            whole(x1.x, x1.z, y1);
+            whole(x1.y, x1.w, y1 + 2);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float d = f16_at(r + j * kRow + 2 * wb) * unit;
+            // a weight of 0 (a masked position) stays 0 whatever the factor
+            y0[j] = y0[j] != 0.0f ? y0[j] * d : 0.0f;
+            y1[j] = y1[j] != 0.0f ? y1[j] * d : 0.0f;
+          }
+          uint4 p1, p2, p3;
+          split_bf162(y0[0], y0[1], p1.x, p2.x, p3.x);
+          split_bf162(y1[0], y1[1], p1.y, p2.y, p3.y);
+          split_bf162(y0[2], y0[3], p1.z, p2.z, p3.z);
+          split_bf162(y1[2], y1[3], p1.w, p2.w, p3.w);
+          const uint32_t a = __byte_perm(cw[0], cw[1], 0x5140), b = __byte_perm(cw[0], cw[1], 0x7362);
+          const uint32_t c = __byte_perm(cw[2], cw[3], 0x5140), e = __byte_perm(cw[2], cw[3], 0x7362);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v0 = codes_to_bf162(j < 2 ? a : b, j & 1 ? 0x4342 : 0x4140);
+            const uint32_t v1 = codes_to_bf162(j < 2 ? c : e, j & 1 ? 0x4342 : 0x4140);
+            mma_bf16(acc[j], p1, v0, v1);
+            mma_bf16(acc[j], p2, v0, v1);
+            mma_bf16(acc[j], p3, v0, v1);
           }
         }
       }
+      const float k0 = keep[0] * moved, k1 = keep[1] * moved;
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[a][j][c] = fmaf(o[a][j][c], keep[a][c >> 1], acc[a][j][c]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      for (int j = 0; j < 4; ++j) {
+        o[j][0] = fmaf(o[j][0], k0, acc[j][0]);
+        o[j][1] = fmaf(o[j][1], k0, acc[j][1]);
+        o[j][2] = fmaf(o[j][2], k1, acc[j][2]);
+        o[j][3] = fmaf(o[j][3], k1, acc[j][3]);
+      }
     }
 
     // -------------------------------------------------------------- the item's rows
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float l = l_run[a][b];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t == 0) sums[warp * kRows + 16 * a + 8 * b + g] = l;
-      }
-    sync();
+    for (int b = 0; b < 2; ++b) {
+      float l = l_run[b];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (t == 0) sums[wb * kRows + 16 * wm + 8 * b + g] = l;
+    }
+    __syncthreads();
     const bool whole = first == 0 && last == it.tiles;
-    float *part = p.parts + (2ll * blockIdx.x + (x0 == begin ? 0 : 1)) * kRows * (kD + 2);
+    float *part = p.parts + (2ll * blockIdx.x + (x0 == begin ? 0 : 1)) * L::kPart;
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int b = 0; b < 2; ++b) {
+      const int r = 16 * wm + 8 * b + g;
+      if (r >= n_rows) continue;
+      float l = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int r = 16 * a + 8 * b + g;
-        if (r >= n_rows) continue;
-        float l = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NB; ++c) l += sums[c * kRows + r];
-        const int row = it.rt * kRows + r;
-        float f = 1.0f;
-        float *dst = part + r * (kD + 2);
-        if (whole) {
-          f = l != 0.0f ? 1.0f / l : 0.0f;
-          dst = p.out + (static_cast<int64_t>(it.s) * p.ntok + row / p.group) * p.n_heads * kD +
-                (it.h * p.group + row % p.group) * kD;
-        } else if (warp == 0 && t == 0) {
-          dst[kD] = m_run[a][b];
-          dst[kD + 1] = l;
-        }
-        // the lane's 8 columns 8 t ... of the warp's block
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float y0 = o[a][j][2 * b], y1 = o[a][j][2 * b + 1];
-          dst[32 * warp + 8 * t + j] = whole ? (l != 0.0f ? y0 * f : 0.0f) : y0;
-          dst[32 * warp + 8 * t + 4 + j] = whole ? (l != 0.0f ? y1 * f : 0.0f) : y1;
-        }
+      for (int c = 0; c < NB; ++c) l += sums[c * kRows + r];
+      const int row = it.rt * kRows + r;
+      float f = 1.0f / unit;  // a power of two
+      float *dst = part + r * (kD + 4);
+      if (whole) {
+        f = l != 0.0f ? f / l : 0.0f;
+        dst = p.out + (static_cast<int64_t>(it.s) * p.ntok + row / p.group) * p.n_heads * kD +
+              (it.h * p.group + row % p.group) * kD;
+      } else if (wb == 0 && t == 0) {
+        *reinterpret_cast<float2 *>(dst + kD) = make_float2(m_run[b], l);
       }
+      // the lane's 8 columns 8 t ... of the warp's block
+      float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * wb + 8 * t);
+      d4[0] = make_float4(o[0][2 * b] * f, o[1][2 * b] * f, o[2][2 * b] * f, o[3][2 * b] * f);
+      d4[1] = make_float4(o[0][2 * b + 1] * f, o[1][2 * b + 1] * f, o[2][2 * b + 1] * f, o[3][2 * b + 1] * f);
+    }
   }
+  // after a wait that gave up: the copies in flight land before the CTA ends
+  if (!ok && tid == 0)
+    for (uint32_t i = load_k > kStages ? load_k - kStages : 0; i < load_k; ++i)
+      mbar_wait(&full[i % kStages], (i / kStages) & 1, p.err, DEVERR_DRAIN_WAIT, i);
 }
 
 // Joins the parts of the items that more than one CTA holds: one warp per
 // (item, row), the parts in the order of their positions.
-template <int NB, int MT>
+template <int NB, int WM>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p, int grid) {
-  constexpr int kRows = 16 * MT, kD = 32 * NB, kPart = kRows * (kD + 2);
-  __shared__ long long before_s;
-  __shared__ long long total_s;
+  constexpr int kRows = 16 * WM, kD = 32 * NB;
+  constexpr long long kPart = Plan<NB, WM>::kPart;
   pdl_launch_dependents();
   pdl_wait();
-  const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const int x = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // (head, row of the head)
+  const int rows = p.ntok * p.group, h = x / rows, row = x - h * rows;
+  const long long first = p.before[s], total = p.before[p.v.n_seq];
   const int n = tree_size(p, s);
-  const int nrt = (n * p.group + kRows - 1) / kRows;
   const int tiles = sequence_tiles(p, s, n);
-  // tiles of the sequences before this one, and of all
-  if (warp == 0) {
-    long long below = 0, all = 0;
-    for (int k = lane; k < p.v.n_seq; k += 32) {
-      const int m = tree_size(p, k);
-      const long long x = static_cast<long long>(sequence_tiles(p, k, m)) * ((m * p.group + kRows - 1) / kRows) * p.v.n_kv;
-      all += x;
-      if (k < s) below += x;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      below += __shfl_xor_sync(0xffffffffu, below, o);
-      all += __shfl_xor_sync(0xffffffffu, all, o);
-    }
-    if (lane == 0) before_s = below, total_s = all;
-  }
-  __syncthreads();
-  const int x = blockIdx.x * (kJoinThreads / 32) + warp;  // (head, row of the head)
-  const int h = x / (p.ntok * p.group), row = x % (p.ntok * p.group);
   if (h >= p.v.n_kv || row >= n * p.group) return;
-  const long long total = total_s, ctas = grid < total ? grid : total;
-  const long long i0 = before_s + static_cast<long long>(h * nrt + row / kRows) * tiles, i1 = i0 + tiles - 1;
-  const int c0 = static_cast<int>(((i0 + 1) * ctas - 1) / total), c1 = static_cast<int>(((i1 + 1) * ctas - 1) / total);
+  const int nrt = (n * p.group + kRows - 1) / kRows;
+  const Shares sh(total, static_cast<int>(grid < total ? grid : total));
+  const long long i0 = first + static_cast<long long>(h * nrt + row / kRows) * tiles;
+  const int c0 = sh.holder(i0), c1 = sh.holder(i0 + tiles - 1);
   if (c0 == c1) return;  // one CTA held it whole and wrote it
   // only the first of the item's CTAs can have begun before it
-  const float *rest = p.parts + (row % kRows) * (kD + 2);
-  const float *head = rest + (c0 * total / ctas >= i0 ? 0 : kPart);
-  float top = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, (c == c0 ? head : rest)[2ll * c * kPart + kD]);
-  top = warp_max_all(top);
-  const float ref = top == -INFINITY ? 0.0f : top;
+  const float *rest = p.parts + (row % kRows) * (kD + 4);
+  const float *head = rest + (sh.begin(c0) >= i0 ? 0 : kPart);
+  auto part = [&](int c) { return (c == c0 ? head : rest) + 2 * kPart * c; };
+  float top = -INFINITY, den = 0.0f;
   float4 y[NB / 4] = {};
-  float den = 0.0f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const float *q = (c == c0 ? head : rest) + 2ll * c * kPart;
-    const float2 ml = *reinterpret_cast<const float2 *>(q + kD);
-    const float f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
-    den = fmaf(f, ml.y, den);
+  for (int b = c0; b <= c1; b += 32) {  // 32 parts at a time: a lane holds the maximum and sum of one
+    const int m = min(32, c1 - b + 1);
+    const float2 ml = lane < m ? *reinterpret_cast<const float2 *>(part(b + lane) + kD) : make_float2(-INFINITY, 0.0f);
+    const float up = fmaxf(top, warp_max_all(ml.x));
+    const float ref = up == -INFINITY ? 0.0f : up;
+    const float keep = exp2f(top - ref), f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
+    top = up;
+    den = fmaf(den, keep, warp_sum_xor<32>(f * ml.y));
 #pragma unroll
-    for (int e = 0; e < NB / 4; ++e) {
-      const float2 a = *reinterpret_cast<const float2 *>(q + 128 * e + 4 * lane);
-      const float2 b = *reinterpret_cast<const float2 *>(q + 128 * e + 4 * lane + 2);
-      y[e].x = fmaf(f, a.x, y[e].x);
-      y[e].y = fmaf(f, a.y, y[e].y);
-      y[e].z = fmaf(f, b.x, y[e].z);
-      y[e].w = fmaf(f, b.y, y[e].w);
+    for (int e = 0; e < NB / 4; ++e) y[e].x *= keep, y[e].y *= keep, y[e].z *= keep, y[e].w *= keep;
+#pragma unroll 8
+    for (int c = 0; c < m; ++c) {
+      const float fc = __shfl_sync(0xffffffffu, f, c);
+      const float4 *src = reinterpret_cast<const float4 *>(part(b + c)) + lane;
+#pragma unroll
+      for (int e = 0; e < NB / 4; ++e) {
+        const float4 a = src[32 * e];
+        y[e].x = fmaf(fc, a.x, y[e].x);
+        y[e].y = fmaf(fc, a.y, y[e].y);
+        y[e].z = fmaf(fc, a.z, y[e].z);
+        y[e].w = fmaf(fc, a.w, y[e].w);
+      }
     }
   }
   float *out = p.out + (static_cast<int64_t>(s) * p.ntok + row / p.group) * p.n_heads * kD +
@@ -698,13 +816,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         den != 0.0f ? make_float4(y[e].x / den, y[e].y / den, y[e].z / den, y[e].w / den) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+constexpr size_t kHeadBytes = 8 * (kMaxSeq + 8);
+
 // rows of a row tile for ntok tokens of `group` heads
 inline int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
-template <int NB, int MT>
+template <int NB, int WM>
 cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t s) {
-  using L = Plan<NB, MT>;
-  auto k = tree_kernel<NB, MT>;
+  using L = Plan<NB, WM>;
+  auto k = tree_kernel<NB, WM>;
   static LaunchOnce once;
   int per_sm = 0;
   cudaError_t e = once.prepare(dev.device, k, L::kThreads, L::kSmem, false, &per_sm);
@@ -713,7 +833,7 @@ cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t
   e = launch_pdl(k, dim3(grid), dim3(L::kThreads), L::kSmem, s, p);
   if (e != cudaSuccess) return e;
   const int rows = p.v.n_kv * p.ntok * p.group;
-  return launch_pdl(join_kernel<NB, MT>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.v.n_seq),
+  return launch_pdl(join_kernel<NB, WM>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.v.n_seq),
                     dim3(kJoinThreads), 0, s, p, grid);
 }
 
@@ -727,7 +847,8 @@ extern "C" size_t epq_attention_tree_workspace_bytes(const epq_pages *pages, int
       n_heads / pages->n_kv_heads > kMaxGroupTree || ntok < 1 || ntok > kMaxTree)
     return 0;
   const int group = n_heads / pages->n_kv_heads;
-  return 2 * sizeof(float) * kMaxCtas * static_cast<size_t>(tile_rows(ntok * group)) * (pages->head_dim + 2);
+  return kHeadBytes +
+         2 * sizeof(float) * kMaxCtas * static_cast<size_t>(tile_rows(ntok * group)) * (pages->head_dim + 4);
 }
 
 extern "C" epq_status epq_attention_tree(const epq_pages *pages, int layer, const float *q, const float *k_new,
@@ -767,7 +888,8 @@ extern "C" epq_status epq_attention_tree(const epq_pages *pages, int layer, cons
   p.ntok = ntok;
   p.scale = scale;
   p.out = out;
-  p.parts = static_cast<float *>(ws);
+  p.before = static_cast<long long *>(ws);
+  p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeadBytes);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool small = tile_rows(ntok * p.group) == 16;
   cudaError_t e = D == 128 ? (small ? launch_tree<4, 1>(p, dev, s) : launch_tree<4, 2>(p, dev, s))
