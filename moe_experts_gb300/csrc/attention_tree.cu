@@ -541,15 +541,9 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
     };
 
-    // The scores of a tile are computed in the iteration before its values,
-    // which leaves one barrier per tile; the first iteration is scores only.
-#pragma unroll 1
-    for (int tile = first - 1; tile < last; ++tile) {
-      if (tile < first) {
-        scores(first, k);
-        __syncthreads();
-        continue;
-      }
+    scores(first, k);
+    __syncthreads();
+    for (int tile = first; tile < last; ++tile, ++k) {
       const int st = k % kStages;
       const bool special = tile * kTile + kTile > it.len;
       // ------------------------------------------------------------ weights
