@@ -22,11 +22,12 @@
 //            part's product: 2^-22 of it, or 2^-39 of the largest one.  That
 //            floor would show where every larger weight meets a code 0, so it
 //            is only used where a row has at least 12 weights within 2^-16 of
-//            its largest; the others (and tiles with drafted tokens, whose
-//            factors may not be finite) take 16 positions at a time with
-//            float32 products in three bf16 parts, which lose nothing.
+//            its largest; a tile with another row (or with drafted tokens, whose
+//            factors may not be finite) takes float32 products in three bf16
+//            parts, which lose nothing.
 // Work: the tiles of all (sequence, head, row tile) items in a row, cut into
-// equal shares, one per CTA.  A CTA's part of an item that it does not hold
+// equal shares, one per CTA.  An item counts kExtra tiles more than it has:
+// beginning it, and its last tile with the new rows, take that long.  A CTA's part of an item that it does not hold
 // whole goes to the workspace (maximum, sum, unnormalised output), and a
 // second launch joins the parts in the order of their positions.
 // Warp 0 streams the rows of a tile (contiguous within a page) with bulk
@@ -50,6 +51,7 @@ constexpr int kTile = 64;  // positions of a tile
 constexpr int kStages = 3;
 constexpr int kMaxCtas = 512;
 constexpr int kJoinThreads = 128;
+constexpr int kExtra = 2;            // tiles' worth of work that an item has besides its tiles
 constexpr float kUp = 14.0f;         // log2 of the largest weight of a row as it is held
 constexpr float kWeighty = 0.25f;    // a weight that counts: 2^-16 of the largest
 constexpr float kWeightyMin = 3.0f;  // of them, in each of a row's four lanes
@@ -72,10 +74,9 @@ __device__ __forceinline__ int tree_size(const TreeParams &p, int s) {
   return p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
 }
 
-// Tiles of one row tile of a sequence with n tokens.
-__device__ __forceinline__ int sequence_tiles(const TreeParams &p, int s, int n) {
-  return n ? (seq_length(p.v, s) + n + kTile - 1) / kTile : 0;
-}
+// Tiles of one row tile of a sequence with n tokens; what the item counts in
+// the shares is kExtra more.
+__device__ __forceinline__ int sequence_tiles(int len, int n) { return n ? (len + n + kTile - 1) / kTile : 0; }
 
 __device__ __forceinline__ uint64_t token_mask(const TreeParams &p, int s, int i, int n) {
   const uint64_t m = p.mask ? p.mask[s * p.ntok + i] : ~0ull >> (63 - i);
@@ -186,7 +187,8 @@ struct Plan {
   static constexpr uint32_t oMask = oSum + 4u * NB * kRows;         // [rows] mask words
   static constexpr uint32_t oScale = oMask + 8u * kRows;            // [rows] score factors (log2 units)
   static constexpr uint32_t oTiles = oScale + 4u * kRows;           // [n_seq + 1] tiles before a sequence, begin, end
-  static constexpr uint32_t oBar = oTiles + 8u * (kMaxSeq + 8);     // full
+  static constexpr uint32_t oSeq = oTiles + 8u * (kMaxSeq + 8);     // [n_seq] length, tokens
+  static constexpr uint32_t oBar = oSeq + 8u * kMaxSeq;             // full
   static constexpr uint32_t oFactor = oBar + 8u * (kStages + 1);    // [2][NB] largest value factor
   static constexpr uint32_t oWide = oFactor + 2u * 4u * NB;         // [2][warps] three parts wanted
   static constexpr uint32_t oMiss = oWide + 2u * 4u * kWarps;       // [stages] missing pieces
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   const int g = lane >> 2, t = lane & 3;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::oBar);
   long long *before = reinterpret_cast<long long *>(smem + L::oTiles);
+  int2 *seq = reinterpret_cast<int2 *>(smem + L::oSeq);
   unsigned *miss = reinterpret_cast<unsigned *>(smem + L::oMiss);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
@@ -231,20 +234,16 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   pdl_launch_dependents();
   pdl_wait();
 
-  // tiles before each sequence
-  auto rows_tiles = [&](int s, int *nrt) {
-    const int n = tree_size(p, s);
-    *nrt = (n * p.group + kRows - 1) / kRows;
-    return sequence_tiles(p, s, n);
-  };
+  // lengths, tokens, tiles before each sequence
   if (warp == 0) {
     long long run = 0;
     for (int s0 = 0; s0 < p.v.n_seq; s0 += 32) {
       long long x = 0;
       if (s0 + lane < p.v.n_seq) {
-        int nrt;
-        const int tiles = rows_tiles(s0 + lane, &nrt);
-        x = static_cast<long long>(tiles) * nrt * p.v.n_kv;
+        const int n = tree_size(p, s0 + lane), len = seq_length(p.v, s0 + lane);
+        seq[s0 + lane] = make_int2(len, n);
+        const int tiles = sequence_tiles(len, n);
+        x = static_cast<long long>(tiles ? tiles + kExtra : 0) * ((n * p.group + kRows - 1) / kRows) * p.v.n_kv;
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   // tokens beyond a sequence's tree: 0
   if (p.n_tok)
     for (int r = blockIdx.x; r < p.v.n_seq * p.ntok; r += gridDim.x) {
-      if (r % p.ntok < tree_size(p, r / p.ntok)) continue;
+      if (r % p.ntok < seq[r / p.ntok].y) continue;
       float4 *o = reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(r) * p.n_heads * kD);
       for (int i = tid; i < p.n_heads * kD / 4; i += L::kThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -287,19 +286,20 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       if (before[mid] <= x) lo = mid;
       else hi = mid - 1;
     }
-    int nrt;
     it.s = lo;
-    it.tiles = rows_tiles(lo, &nrt);
-    it.len = seq_length(p.v, lo);
-    it.n = tree_size(p, lo);
+    it.len = seq[lo].x;
+    it.n = seq[lo].y;
+    it.tiles = sequence_tiles(it.len, it.n);
+    const int nrt = (it.n * p.group + kRows - 1) / kRows;
     const long long rel = x - before[lo];
     int k, tile;
+    const int units = it.tiles + kExtra;
     if (rel >> 31) {
-      k = static_cast<int>(rel / it.tiles);
-      tile = static_cast<int>(rel % it.tiles);
+      k = static_cast<int>(rel / units);
+      tile = static_cast<int>(rel % units);
     } else {
-      k = static_cast<int>(rel) / it.tiles;
-      tile = static_cast<int>(rel) - k * it.tiles;
+      k = static_cast<int>(rel) / units;
+      tile = static_cast<int>(rel) - k * units;
     }
     it.h = k / nrt;
     it.rt = k - it.h * nrt;
@@ -316,8 +316,16 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   long long load_x = begin;
   uint32_t load_k = 0;
   auto look_ahead = [&]() {
+    // to the next tile that there is (none of what an item counts beyond them)
+    while (load_x < end && (load_x == begin || load_tile >= load_it.tiles)) {
+      if (load_x != begin) load_x += load_it.tiles + kExtra - load_tile;
+      if (load_x >= end) break;
+      load_tile = find(load_x, load_it);
+      if (load_tile < load_it.tiles) break;
+      load_x += load_it.tiles + kExtra - load_tile;
+      load_tile = load_it.tiles + kExtra;  // the next turn finds the item that begins here
+    }
     if (load_x >= end) return;
-    if (load_x == begin || load_tile == load_it.tiles) load_tile = find(load_x, load_it);
     const int pos = load_tile * kTile + (lane >> 1) * piece_rows;
     load_rows = (lane >> 1) < kTile / piece_rows ? min(max(load_it.len - pos, 0), piece_rows) : 0;
     load_page = load_rows > 0 ? p.v.table[static_cast<int64_t>(load_it.s) * p.v.max_pages + pos / p.v.P] : 0;
@@ -362,7 +370,8 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
     const int first = find(x, it);
     const int last = static_cast<int>(min(static_cast<long long>(it.tiles), first + (end - x)));
     const long long x0 = x;
-    x += last - first;
+    x += it.tiles + kExtra - first;
+    if (first >= it.tiles) continue;
     const int n_rows = min(kRows, it.n * p.group - it.rt * kRows);
 
     // -------------------------------------------------------------- queries
@@ -420,49 +429,75 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
     auto scores = [&](int tile, uint32_t kk) {
       const int st = kk % kStages;
       uint8_t *kt = smem + L::oStage + st * L::kStageBytes, *vt = kt + kTile * kRow;
-      if (ok) ok = mbar_wait_poll(&full[st], (kk / kStages) & 1, p.err, DEVERR_FULL_WAIT, kk);
       const int t0 = tile * kTile;
-      const unsigned lost = miss[st];
-      const bool special = t0 + kTile > it.len || lost;
+      bool special = t0 + kTile > it.len;
       if (special) {
-        // rows that hold nothing: their factors are 0
+        // While the committed rows are on their way (none of what is written
+        // here is in their copies): the factors of rows that hold nothing are 0,
         for (int i = tid; i < 2 * kTile; i += L::kThreads) {
           const int r = i >> 1, pos = t0 + r;
-          if (pos >= it.len + it.n || (pos < it.len && lost >> (2 * (r / piece_rows)) & 1)) {
-            uint2 *f = reinterpret_cast<uint2 *>((i & 1 ? vt : kt) + r * kRow);
+          uint8_t *dst = (i & 1 ? vt : kt) + r * kRow;
+          if (pos >= it.len + it.n) {
 #pragma unroll
-            for (int b = 0; b < NB / 4; ++b) f[b] = make_uint2(0, 0);
+            for (int b = 0; b < NB / 4; ++b) reinterpret_cast<uint2 *>(dst)[b] = make_uint2(0, 0);
           } else if (pos == it.len - 1 && ((r % piece_rows + 1) * kRow & 8)) {
-            // the end of an odd number of rows (a bulk copy moves 16 bytes)
-            *reinterpret_cast<uint2 *>((i & 1 ? vt : kt) + r * kRow + kRow - 8) = *reinterpret_cast<const uint2 *>(
-                page_row(p.v, p.layer, seq_page(p.v, it.s, pos / p.v.P), it.h, i & 1, pos % p.v.P) + kRow - 8);
+            // the end of an odd number of rows (a bulk copy moves 16 bytes),
+            const int page = seq_page(p.v, it.s, pos / p.v.P);
+            if (page >= 0)
+              *reinterpret_cast<uint2 *>(dst + kRow - 8) =
+                  *reinterpret_cast<const uint2 *>(page_row(p.v, p.layer, page, it.h, i & 1, pos % p.v.P) + kRow - 8);
           }
         }
-        // the new rows
+        // and the new rows
         const int r0 = max(it.len - t0, 0), r1 = min(it.len + it.n - t0, kTile);
-#pragma unroll 2
-        for (int rr = 2 * r0 + warp; rr < 2 * r1; rr += L::kWarps) {
-          const int r = rr >> 1, c = rr & 1, pos = t0 + r;
-          const float *src = (c ? p.v_new : p.k_new) + it.s * p.kv_seq_ld + (pos - it.len) * p.kv_ld + it.h * kD;
-          uint8_t *dst = (c ? vt : kt) + r * kRow, *row = nullptr;
-          if (it.rt == 0) {
-            const int page = seq_page(p.v, it.s, pos / p.v.P);
-            if (page >= 0) row = page_row(p.v, p.layer, page, it.h, c, pos % p.v.P);
-            else if (lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(it.s));
+        constexpr int kBatch = NB == 4 ? 4 : 2;  // row planes of a warp whose loads are in flight together
+        for (int rr0 = 2 * r0 + warp; rr0 < 2 * r1; rr0 += kBatch * L::kWarps) {
+          float4 x[kBatch][NB / 4];
+          int page[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int rr = min(rr0 + u * L::kWarps, 2 * r1 - 1), pos = t0 + (rr >> 1);
+            const float *src = (rr & 1 ? p.v_new : p.k_new) + it.s * p.kv_seq_ld + (pos - it.len) * p.kv_ld + it.h * kD;
+#pragma unroll
+            for (int b = 0; b < NB / 4; ++b) x[u][b] = *reinterpret_cast<const float4 *>(src + 128 * b + 4 * lane);
+            page[u] = it.rt == 0 ? seq_page(p.v, it.s, pos / p.v.P) : -1;
           }
 #pragma unroll
-          for (int b = 0; b < NB / 4; ++b) {
-            __half d;
-            const uint32_t word = quantize4(*reinterpret_cast<const float4 *>(src + 128 * b + 4 * lane), &d);
-            const int at = kD / 16 + 128 * b + 4 * lane, fat = 2 * (4 * b + (lane >> 3));
-            *reinterpret_cast<uint32_t *>(dst + at) = word;
-            if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(dst + fat) = __half_as_ushort(d);
-            if (row) {
-              *reinterpret_cast<uint32_t *>(row + at) = word;
-              if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(row + fat) = __half_as_ushort(d);
+          for (int u = 0; u < kBatch; ++u) {
+            const int rr = rr0 + u * L::kWarps;
+            if (rr >= 2 * r1) break;
+            const int r = rr >> 1, c = rr & 1, pos = t0 + r;
+            uint8_t *dst = (c ? vt : kt) + r * kRow, *row = nullptr;
+            if (page[u] >= 0) row = page_row(p.v, p.layer, page[u], it.h, c, pos % p.v.P);
+            else if (it.rt == 0 && lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(it.s));
+#pragma unroll
+            for (int b = 0; b < NB / 4; ++b) {
+              __half d;
+              const uint32_t word = quantize4(x[u][b], &d);
+              const int at = kD / 16 + 128 * b + 4 * lane, fat = 2 * (4 * b + (lane >> 3));
+              *reinterpret_cast<uint32_t *>(dst + at) = word;
+              if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(dst + fat) = __half_as_ushort(d);
+              if (row) {
+                *reinterpret_cast<uint32_t *>(row + at) = word;
+                if ((lane & 7) == 0) *reinterpret_cast<uint16_t *>(row + fat) = __half_as_ushort(d);
+              }
             }
           }
         }
+      }
+      if (ok) ok = mbar_wait_poll(&full[st], (kk / kStages) & 1, p.err, DEVERR_FULL_WAIT, kk);
+      const unsigned lost = miss[st];
+      if (lost) {  // rows of a missing page: no factors, and masked below
+        special = true;
+        for (int i = tid; i < 2 * kTile; i += L::kThreads) {
+          const int r = i >> 1;
+          if (t0 + r < it.len && lost >> (2 * (r / piece_rows)) & 1)
+#pragma unroll
+            for (int b = 0; b < NB / 4; ++b)
+              reinterpret_cast<uint2 *>((i & 1 ? vt : kt) + r * kRow)[b] = make_uint2(0, 0);
+        }
+      }
+      if (special) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
       }
@@ -624,31 +659,28 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       // round every sum towards zero, which over a long context would add up.
       float acc[4][4] = {};
       const uint8_t *vt = smem + L::oStage + st * L::kStageBytes + kTile * kRow;
-      const __half2 unit2 = __float2half2_rn(unit);
+      bool slow = false;
 #pragma unroll
-      for (int kg = 0; kg < kTile / 16; ++kg) {
-        const uint8_t *r = vt + (16 * kg + 4 * t) * kRow;
-        uint32_t cw[4];
+      for (int c = 0; c < NB; ++c) slow = slow || wide[c];
+      // A operands of 16 positions: the lane's 4 are 16 kg + 4 t ..., of rows g
+      // and g + 8; B operands: column n of MMA tile j is element 4 n + j of the
+      // block.
+      if (!slow) {
+        const __half2 unit2 = __float2half2_rn(unit);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          cw[j] = *reinterpret_cast<const uint32_t *>(r + j * kRow + kD / 16 + 32 * wb + 4 * g);
-        const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
-        const uint4 x0 = *reinterpret_cast<const uint4 *>(w + g * kTile + col);
-        const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
-        const bool mine = kNT == 2 ? wide[kg] : wide[2 * kg + (t >> 1)];  // how the lane's weights are held
-        const bool slow = kNT == 2 ? wide[kg] : wide[2 * kg] || wide[2 * kg + 1];
-        // column n of MMA tile j: element 4 n + j of the block
-        if (!slow) {
-          uint32_t f01, f23;  // factors of positions 4 t ...
-          {
-            const uint32_t a0 = *reinterpret_cast<const unsigned short *>(r + 2 * wb);
-            const uint32_t a1 = *reinterpret_cast<const unsigned short *>(r + kRow + 2 * wb);
-            const uint32_t a2 = *reinterpret_cast<const unsigned short *>(r + 2 * kRow + 2 * wb);
-            const uint32_t a3 = *reinterpret_cast<const unsigned short *>(r + 3 * kRow + 2 * wb);
-            f01 = __byte_perm(a0, a1, 0x5410);
-            f23 = __byte_perm(a2, a3, 0x5410);
+        for (int kg = 0; kg < kTile / 16; ++kg) {
+          const uint8_t *r = vt + (16 * kg + 4 * t) * kRow;
+          uint32_t cw[4], f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            cw[j] = *reinterpret_cast<const uint32_t *>(r + j * kRow + kD / 16 + 32 * wb + 4 * g) ^ 0x80808080u;
+            f[j] = *reinterpret_cast<const unsigned short *>(r + j * kRow + 2 * wb);
           }
-          const __half2 d01 = __hmul2(as_half2(f01), unit2), d23 = __hmul2(as_half2(f23), unit2);
+          const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
+          const uint4 x0 = *reinterpret_cast<const uint4 *>(w + g * kTile + col);
+          const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
+          const __half2 d01 = __hmul2(as_half2(__byte_perm(f[0], f[1], 0x5410)), unit2);
+          const __half2 d23 = __hmul2(as_half2(__byte_perm(f[2], f[3], 0x5410)), unit2);
           auto times = [](uint32_t h, uint32_t l, __half2 d, uint32_t &hi, uint32_t &lo) {
             const __half2 y = __hmul2(as_half2(h), d);
             hi = as_bits(y);
@@ -659,8 +691,6 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           times(x1.x, x1.z, d01, hi.y, lo.y);
           times(x0.y, x0.w, d23, hi.z, lo.z);
           times(x1.y, x1.w, d23, hi.w, lo.w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) cw[j] ^= 0x80808080u;
           const uint32_t a = __byte_perm(cw[0], cw[1], 0x5140), b = __byte_perm(cw[0], cw[1], 0x7362);
           const uint32_t c = __byte_perm(cw[2], cw[3], 0x5140), e = __byte_perm(cw[2], cw[3], 0x7362);
 #pragma unroll
@@ -670,10 +700,17 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
             mma_f16(acc[j], hi, v0, v1);
             mma_f16(acc[j], lo, v0, v1);
           }
-        } else {
+        }
+      } else {
+#pragma unroll 2
+        for (int kg = 0; kg < kTile / 16; ++kg) {
+          const uint8_t *r = vt + (16 * kg + 4 * t) * kRow;
+          const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
+          const uint4 x0 = *reinterpret_cast<const uint4 *>(w + g * kTile + col);
+          const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
           float y0[4] = {__uint_as_float(x0.x), __uint_as_float(x0.y), __uint_as_float(x0.z), __uint_as_float(x0.w)};
           float y1[4] = {__uint_as_float(x1.x), __uint_as_float(x1.y), __uint_as_float(x1.z), __uint_as_float(x1.w)};
-          if (kNT == 1 && !mine) {
+          if (!wide[kNT == 2 ? kg : 2 * kg + (t >> 1)]) {  // held as two parts
             auto whole = [](uint32_t h, uint32_t l, float *y) {
               const float2 a = __half22float2(as_half2(h)), b = __half22float2(as_half2(l));
               y[0] = a.x + b.x;
@@ -684,8 +721,10 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
             whole(x1.x, x1.z, y1);
             whole(x1.y, x1.w, y1 + 2);
           }
+          uint32_t cw[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            cw[j] = *reinterpret_cast<const uint32_t *>(r + j * kRow + kD / 16 + 32 * wb + 4 * g);
             const float d = f16_at(r + j * kRow + 2 * wb) * unit;
             // a weight of 0 (a masked position) stays 0 whatever the factor
             y0[j] = y0[j] != 0.0f ? y0[j] * d : 0.0f;
@@ -771,11 +810,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   const int rows = p.ntok * p.group, h = x / rows, row = x - h * rows;
   const long long first = p.before[s], total = p.before[p.v.n_seq];
   const int n = tree_size(p, s);
-  const int tiles = sequence_tiles(p, s, n);
+  const int tiles = sequence_tiles(seq_length(p.v, s), n);
   if (h >= p.v.n_kv || row >= n * p.group) return;
   const int nrt = (n * p.group + kRows - 1) / kRows;
   const Shares sh(total, static_cast<int>(grid < total ? grid : total));
-  const long long i0 = first + static_cast<long long>(h * nrt + row / kRows) * tiles;
+  const long long i0 = first + static_cast<long long>(h * nrt + row / kRows) * (tiles + kExtra);
   const int c0 = sh.holder(i0), c1 = sh.holder(i0 + tiles - 1);
   if (c0 == c1) return;  // one CTA held it whole and wrote it
   // only the first of the item's CTAs can have begun before it
