@@ -15,6 +15,12 @@ prologue).  Attention is either
 Every step below is one C-ABI call; this module holds device buffers and the
 order of the calls, nothing else.
 
+TreeDecoder verifies a tree of drafted tokens in one dense step over a paged
+Q8_0 cache: the drafted tokens are the GEMVs' columns, every layer appends
+their keys and values and attends over the cache and the tree, and the walk
+over the logits and the commit of the accepted rows end the step -- all of it
+queued (or captured in one graph) without a host synchronisation.
+
 `timers` (optional) brackets each call of the first layer with a pair of
 CUDA events, so that per-kernel durations can be read after a graph replay.
 """
@@ -204,3 +210,85 @@ class MoEDecoder:
                 L.epq_moe_forward(moe, h, c.topk, y=y, workspace=self.ws, rms_prenorm=True, rms_eps=c.rms_eps,
                                   topk_idx=None if idx_out is None else idx_out[li:li + 1], stream=stream)
         return out
+
+
+def paged_cache(caches, ctx, n_seq=1, room=128, spare_pages=0, page_size=64):
+    """A PagedKVCache of all layers whose sequence 0 holds positions 0..ctx-1
+    of `caches` (one KVCache per layer); `room`: further positions of every
+    sequence, for which the pool has pages (plus spare_pages)."""
+    c0 = caches[0]
+    dev = c0.k.device
+    have, each = -(-ctx // page_size), -(-(ctx + room) // page_size)
+    pages = L.PagedKVCache(len(caches), each + (n_seq - 1) * (each - ctx // page_size) + spare_pages, c0.n_kv_heads,
+                           c0.head_dim, n_seq, each, page_size, dev)
+    for li, c in enumerate(caches):
+        for plane, rows in enumerate((c.k, c.v)):
+            x = torch.zeros((c.n_kv_heads, have * page_size, rows.shape[2]), dtype=torch.uint8, device=dev)
+            x[:, :ctx] = rows[:, :ctx]
+            pages.pool[li, :have, :, plane] = x.view(c.n_kv_heads, have, page_size, -1).transpose(0, 1)
+    pages.table[0, :have] = torch.arange(have, dtype=torch.int32, device=dev)
+    pages.refs[:have] = 1
+    pages.length[0] = ctx
+    return pages
+
+
+class TreeDecoder:
+    """A dense decoder that verifies ntok (1..8) drafted tokens per step.
+
+    layers, head: packed weights as in DenseDecoder; cache: a PagedKVCache of
+    all layers (one sequence).  Token 0 of a step is the last committed token,
+    the others its drafted continuations; parent names their tree."""
+
+    def __init__(self, cfg, fmt, layers, head, cache, ntok, device):
+        if not 1 <= ntok <= 8 or cache.n_seq != 1:
+            raise ValueError("1..8 drafted tokens of one sequence")
+        self.cfg, self.fmt, self.layers, self.head, self.cache, self.ntok = cfg, fmt, layers, head, cache, ntok
+        f32 = dict(dtype=torch.float32, device=device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.qkv = torch.empty((1, ntok, cfg.q_rows + 2 * cfg.kv_rows), **f32)
+        self.attn = torch.empty((1, ntok, cfg.q_rows), **f32)
+        self.m = torch.empty((ntok, cfg.inter), **f32)
+        self.h = torch.empty((ntok, cfg.hidden), **f32)
+        self.logits = torch.empty((1, ntok, cfg.vocab), **f32)
+        self.mask = torch.empty((1, ntok), dtype=torch.int64, device=device)
+        self.extra = torch.full((1,), ntok, **i32)
+        self.status = torch.zeros(1, **i32)
+        self.path, self.n_accept, self.next_token = (torch.empty(n, **i32) for n in ((1, ntok), (1,), (1,)))
+        self.lse = torch.empty((1, ntok), **f32)
+        self.attn_ws = L.epq_attention_tree_workspace(cache, cfg.heads, ntok)
+        self.verify_ws = L.epq_verify_tree_workspace(self.logits)
+
+    def forward(self, x, parent, stream=None):
+        """x [ntok, H] (the tokens' embeddings), parent int32 [1, ntok] ->
+        logits [1, ntok, vocab]; the tokens' rows lie behind the committed
+        positions.  status is nonzero when the cache had no room."""
+        c, f, H, nq, nkv = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows
+        h, qkv, attn = self.h, self.qkv, self.attn
+        L.epq_pages_reserve(self.cache, self.extra, self.status, stream=stream)
+        L.epq_tree_mask(parent, self.mask, stream=stream)
+        q, k, v = qkv[..., :nq], qkv[..., nq:nq + nkv], qkv[..., nq + nkv:]
+        for li, (wqkv, wo, wgu, wd) in enumerate(self.layers):
+            src = x if li == 0 else h
+            L.epq_gemv_ex(f, wqkv, src, nq + 2 * nkv, H, y=qkv[0], rms_prenorm=True, rms_eps=c.rms_eps,
+                          weights_ready=True, stream=stream)
+            L.epq_attention_tree(q, k, v, self.cache, li, c.heads, 1.0 / math.sqrt(c.head_dim), mask=self.mask, out=attn,
+                                 workspace=self.attn_ws, stream=stream)
+            L.epq_gemv_ex(f, wo, attn[0], H, nq, y=h, residual=src, weights_ready=True, stream=stream)
+            L.epq_gemv_ex(f, wgu, h, 2 * c.inter, H, y=self.m, rms_prenorm=True, rms_eps=c.rms_eps, swiglu=True,
+                          weights_ready=True, stream=stream)
+            L.epq_gemv_ex(f, wd, self.m, H, c.inter, y=h, residual=h, weights_ready=True, stream=stream)
+        L.epq_gemv_ex(f, self.head, h, c.vocab, H, y=self.logits[0], rms_prenorm=True, rms_eps=c.rms_eps,
+                      weights_ready=True, stream=stream)
+        return self.logits
+
+    def step(self, x, tokens, parent, u, draft=None, temperature=1.0, stream=None):
+        """One verification step: forward, the walk, the commit.  tokens,
+        parent int32 and u float32 [1, ntok], draft None or float32 [1, ntok,
+        vocab] -> (path, n_accept, next_token); the cache then holds the
+        accepted tokens, and next_token is the root of the next step."""
+        self.forward(x, parent, stream=stream)
+        L.epq_verify_tree(self.logits, tokens, parent, u, draft=draft, temperature=temperature, path=self.path,
+                          n_accept=self.n_accept, next_token=self.next_token, lse=self.lse, workspace=self.verify_ws,
+                          stream=stream)
+        L.epq_pages_compact(self.cache, self.path, self.n_accept, stream=stream)
+        return self.path, self.n_accept, self.next_token
