@@ -46,16 +46,12 @@
 namespace epq {
 namespace {
 
-constexpr int kMaxGroupTree = 16;
 constexpr int kTile = 64;  // positions of a tile
 constexpr int kStages = 3;
+constexpr int kMaxGroupTree = 16;
 constexpr int kMaxCtas = 512;
 constexpr int kJoinThreads = 128;
 constexpr int kExtra = 2;            // tiles' worth of work that an item has besides its tiles
-constexpr float kUp = 14.0f;         // log2 of the largest weight of a row as it is held
-constexpr float kWeighty = 0.25f;    // a weight that counts: 2^-16 of the largest
-constexpr float kWeightyMin = 3.0f;  // of them, in each of a row's four lanes
-
 struct TreeParams {
   PagesView v;
   const float *q, *k_new, *v_new;
@@ -74,8 +70,8 @@ __device__ __forceinline__ int tree_size(const TreeParams &p, int s) {
   return p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
 }
 
-// Tiles of one row tile of a sequence with n tokens; what the item counts in
-// the shares is kExtra more.
+// Tiles of one row tile of a sequence with n tokens; what
+// the item counts in the shares is kExtra more.
 __device__ __forceinline__ int sequence_tiles(int len, int n) { return n ? (len + n + kTile - 1) / kTile : 0; }
 
 __device__ __forceinline__ uint64_t token_mask(const TreeParams &p, int s, int i, int n) {
@@ -94,18 +90,105 @@ struct Shares {
   }
 };
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+constexpr float kUp = 14.0f;         // log2 of the largest weight of a row as it is held
+constexpr float kWeighty = 0.25f;    // a weight that counts: 2^-16 of the largest
+constexpr float kWeightyMin = 3.0f;  // of them, in each of a row's four lanes
+
+// What a work item is: row tile rt of head h of sequence s.
+struct Item {
+  int s, h, rt, tiles, len, n;
+};
+
+// The work of a launch, in shared memory: lengths and tokens of the sequences,
+// the tiles (kExtra more per item) before each of them, and the CTA's share.
+struct Work {
+  long long before[kMaxSeq + 1], begin, end;
+  int2 seq[kMaxSeq];
+};
+
+// Filled by warp 0; ends with a CTA barrier.
+template <int kRows>
+__device__ __forceinline__ void find_work(const TreeParams &p, Work &wk) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    long long run = 0;
+    for (int s0 = 0; s0 < p.v.n_seq; s0 += 32) {
+      long long x = 0;
+      if (s0 + lane < p.v.n_seq) {
+        const int n = tree_size(p, s0 + lane), len = seq_length(p.v, s0 + lane);
+        wk.seq[s0 + lane] = make_int2(len, n);
+        const int tiles = sequence_tiles(len, n);
+        x = static_cast<long long>(tiles ? tiles + kExtra : 0) * ((n * p.group + kRows - 1) / kRows) * p.v.n_kv;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (s0 + lane < p.v.n_seq) wk.before[s0 + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) {
+      wk.before[0] = 0;
+      const int ctas = static_cast<int>(run < gridDim.x ? run : gridDim.x);
+      wk.begin = wk.end = 0;
+      if (blockIdx.x < ctas) {
+        const Shares sh(run, ctas);
+        wk.begin = sh.begin(blockIdx.x);
+        wk.end = sh.begin(blockIdx.x + 1);
+      }
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)  // for the join
+    for (int s = threadIdx.x; s <= p.v.n_seq; s += blockDim.x) p.before[s] = wk.before[s];
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+// The item that holds unit x of the work, and the unit's place in it (from
+// it.tiles on: none of its tiles).
+template <int kRows>
+__device__ __forceinline__ int find_item(const TreeParams &p, const Work &wk, long long x, Item &it) {
+  int lo = 0, hi = p.v.n_seq - 1;
+  while (lo < hi) {  // the last sequence with before[s] <= x (empty ones are passed over)
+    const int mid = (lo + hi + 1) / 2;
+    if (wk.before[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  it.s = lo;
+  it.len = wk.seq[lo].x;
+  it.n = wk.seq[lo].y;
+  it.tiles = sequence_tiles(it.len, it.n);
+  const int nrt = (it.n * p.group + kRows - 1) / kRows;
+  const long long rel = x - wk.before[lo];
+  const int units = it.tiles + kExtra;
+  int k, tile;
+  if (rel >> 31) {
+    k = static_cast<int>(rel / units);
+    tile = static_cast<int>(rel % units);
+  } else {
+    k = static_cast<int>(rel) / units;
+    tile = static_cast<int>(rel) - k * units;
+  }
+  it.h = k / nrt;
+  it.rt = k - it.h * nrt;
+  return tile;
+}
+
+// The outputs of tokens beyond a sequence's tree are 0.
+__device__ __forceinline__ void clear_unused(const TreeParams &p, const Work &wk) {
+  if (!p.n_tok) return;
+  const int width = p.n_heads * p.v.D;
+  for (int r = blockIdx.x; r < p.v.n_seq * p.ntok; r += gridDim.x) {
+    if (r % p.ntok < wk.seq[r / p.ntok].y) continue;
+    float4 *o = reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(r) * width);
+    for (int i = threadIdx.x; i < width / 4; i += blockDim.x) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+// Where row `row` of head h of sequence s goes.
+__device__ __forceinline__ float *out_row(const TreeParams &p, int s, int h, int row) {
+  return p.out + (static_cast<int64_t>(s) * p.ntok + row / p.group) * p.n_heads * p.v.D +
+         (h * p.group + row % p.group) * p.v.D;
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
@@ -115,28 +198,6 @@ __device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cas
 // 1024 + u.
 __device__ __forceinline__ uint32_t codes_to_half2(uint32_t x, uint32_t sel) {
   return as_bits(__hsub2(as_half2(__byte_perm(x, 0x64646464u, sel)), __half2half2(__ushort_as_half(0x6480))));
-}
-
-// Two codes (bytes c of x picked by sel) as bf16: under the byte 0x43 the low
-// seven bits are 128 + (c & 127), and 0x4300 | (c & 128) is 128, or 256 for a
-// negative code; their difference is c, exactly.
-__device__ __forceinline__ uint32_t codes_to_bf162(uint32_t x, uint32_t sel) {
-  const uint32_t h = __byte_perm(x, 0x43434343u, sel);
-  const uint32_t m = h & 0xff7fff7fu, n = h & 0xff80ff80u;
-  const __nv_bfloat162 r =
-      __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), *reinterpret_cast<const __nv_bfloat162 *>(&n));
-  return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// x, y as the sum of three bf16 parts: 8 bits of the significand each.
-__device__ __forceinline__ void split_bf162(float x, float y, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
-  p1 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-  x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-  y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-  p2 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-  x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-  y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-  p3 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
@@ -162,10 +223,123 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// What a work item is: rows [16 WM rt, ...) of head h of sequence s.
-struct Item {
-  int s, h, rt, tiles, len, n;
-};
+// Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127), codes rint(x /
+// factor) in +-127, 0 for a zero factor) of 4 elements a lane, 8 lanes a block.
+__device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
+  const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
+  float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
+#pragma unroll
+  for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
+  const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
+  const float d = __half2float(dh);
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
+    word |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xffu) << (8 * j);
+  }
+  *factor = dh;
+  return word;
+}
+
+// Joins the parts of the items that more than one CTA holds: one warp per
+// (item, row), the parts in the order of their positions.
+template <int kD, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p, int grid) {
+  constexpr long long kPart = kRows * (kD + 4);
+  pdl_launch_dependents();
+  pdl_wait();
+  const int s = blockIdx.y, lane = threadIdx.x & 31;
+  const int x = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // (head, row of the head)
+  const int rows = p.ntok * p.group, h = x / rows, row = x - h * rows;
+  const long long first = p.before[s], total = p.before[p.v.n_seq];
+  const int n = tree_size(p, s);
+  const int tiles = sequence_tiles(seq_length(p.v, s), n);
+  if (h >= p.v.n_kv || row >= n * p.group) return;
+  const int nrt = (n * p.group + kRows - 1) / kRows;
+  const Shares sh(total, static_cast<int>(grid < total ? grid : total));
+  const long long i0 = first + static_cast<long long>(h * nrt + row / kRows) * (tiles + kExtra);
+  const int c0 = sh.holder(i0), c1 = sh.holder(i0 + tiles - 1);
+  if (c0 == c1) return;  // one CTA held it whole and wrote it
+  // only the first of the item's CTAs can have begun before it
+  const float *rest = p.parts + (row % kRows) * (kD + 4);
+  const float *head = rest + (sh.begin(c0) >= i0 ? 0 : kPart);
+  auto part = [&](int c) { return (c == c0 ? head : rest) + 2 * kPart * c; };
+  float top = -INFINITY, den = 0.0f;
+  float4 y[kD / 128] = {};
+  for (int b = c0; b <= c1; b += 32) {  // 32 parts at a time: a lane holds the maximum and sum of one
+    const int m = min(32, c1 - b + 1);
+    const float2 ml = lane < m ? *reinterpret_cast<const float2 *>(part(b + lane) + kD) : make_float2(-INFINITY, 0.0f);
+    const float up = fmaxf(top, warp_max_all(ml.x));
+    const float ref = up == -INFINITY ? 0.0f : up;
+    const float keep = exp2f(top - ref), f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
+    top = up;
+    den = fmaf(den, keep, warp_sum_xor<32>(f * ml.y));
+#pragma unroll
+    for (int e = 0; e < kD / 128; ++e) y[e].x *= keep, y[e].y *= keep, y[e].z *= keep, y[e].w *= keep;
+#pragma unroll 8
+    for (int c = 0; c < m; ++c) {
+      const float fc = __shfl_sync(0xffffffffu, f, c);
+      const float4 *src = reinterpret_cast<const float4 *>(part(b + c)) + lane;
+#pragma unroll
+      for (int e = 0; e < kD / 128; ++e) {
+        const float4 a = src[32 * e];
+        y[e].x = fmaf(fc, a.x, y[e].x);
+        y[e].y = fmaf(fc, a.y, y[e].y);
+        y[e].z = fmaf(fc, a.z, y[e].z);
+        y[e].w = fmaf(fc, a.w, y[e].w);
+      }
+    }
+  }
+  float *out = p.out + (static_cast<int64_t>(s) * p.ntok + row / p.group) * p.n_heads * kD +
+               (h * p.group + row % p.group) * kD;
+#pragma unroll
+  for (int e = 0; e < kD / 128; ++e)
+    *reinterpret_cast<float4 *>(out + 128 * e + 4 * lane) =
+        den != 0.0f ? make_float4(y[e].x / den, y[e].y / den, y[e].z / den, y[e].w / den) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <int kD, int kRows>
+cudaError_t launch_join(const TreeParams &p, int grid, cudaStream_t s) {
+  const int rows = p.v.n_kv * p.ntok * p.group, per = kJoinThreads / 32;
+  return launch_pdl(join_kernel<kD, kRows>, dim3((rows + per - 1) / per, p.v.n_seq), dim3(kJoinThreads), 0, s, p, grid);
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// Two codes (bytes c of x picked by sel) as bf16: under the byte 0x43 the low
+// seven bits are 128 + (c & 127), and 0x4300 | (c & 128) is 128, or 256 for a
+// negative code; their difference is c, exactly.
+__device__ __forceinline__ uint32_t codes_to_bf162(uint32_t x, uint32_t sel) {
+  const uint32_t h = __byte_perm(x, 0x43434343u, sel);
+  const uint32_t m = h & 0xff7fff7fu, n = h & 0xff80ff80u;
+  const __nv_bfloat162 r =
+      __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&m), *reinterpret_cast<const __nv_bfloat162 *>(&n));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// x, y as the sum of three bf16 parts: 8 bits of the significand each.
+__device__ __forceinline__ void split_bf162(float x, float y, uint32_t &p1, uint32_t &p2, uint32_t &p3) {
+  p1 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+  p2 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  x -= __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  y -= __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+  p3 = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
 
 template <int NB, int WM>
 struct Plan {
@@ -186,33 +360,13 @@ struct Plan {
   static constexpr uint32_t oSum = oMax + 2u * 4u * NB * kRows;     // [NB][rows]
   static constexpr uint32_t oMask = oSum + 4u * NB * kRows;         // [rows] mask words
   static constexpr uint32_t oScale = oMask + 8u * kRows;            // [rows] score factors (log2 units)
-  static constexpr uint32_t oTiles = oScale + 4u * kRows;           // [n_seq + 1] tiles before a sequence, begin, end
-  static constexpr uint32_t oSeq = oTiles + 8u * (kMaxSeq + 8);     // [n_seq] length, tokens
-  static constexpr uint32_t oBar = oSeq + 8u * kMaxSeq;             // full
+  static constexpr uint32_t oWork = oScale + 4u * kRows;            // Work
+  static constexpr uint32_t oBar = oWork + sizeof(Work);            // full
   static constexpr uint32_t oFactor = oBar + 8u * (kStages + 1);    // [2][NB] largest value factor
   static constexpr uint32_t oWide = oFactor + 2u * 4u * NB;         // [2][warps] three parts wanted
   static constexpr uint32_t oMiss = oWide + 2u * 4u * kWarps;       // [stages] missing pieces
   static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
-
-// Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127), codes rint(x /
-// factor) in +-127, 0 for a zero factor) of 4 elements a lane, 8 lanes a block.
-__device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
-  const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
-  float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
-#pragma unroll
-  for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-  const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
-  const float d = __half2float(dh);
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
-    word |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xffu) << (8 * j);
-  }
-  *factor = dh;
-  return word;
-}
 
 template <int NB, int WM>
 __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3 : 2) : 1)
@@ -224,8 +378,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   const int wm = warp / NB, wb = warp % NB;  // rows 16 wm ..., positions wb kKeys ..., columns 32 wb ...
   const int g = lane >> 2, t = lane & 3;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::oBar);
-  long long *before = reinterpret_cast<long long *>(smem + L::oTiles);
-  int2 *seq = reinterpret_cast<int2 *>(smem + L::oSeq);
+  Work &wk = *reinterpret_cast<Work *>(smem + L::oWork);
   unsigned *miss = reinterpret_cast<unsigned *>(smem + L::oMiss);
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
@@ -234,77 +387,11 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
   pdl_launch_dependents();
   pdl_wait();
 
-  // lengths, tokens, tiles before each sequence
-  if (warp == 0) {
-    long long run = 0;
-    for (int s0 = 0; s0 < p.v.n_seq; s0 += 32) {
-      long long x = 0;
-      if (s0 + lane < p.v.n_seq) {
-        const int n = tree_size(p, s0 + lane), len = seq_length(p.v, s0 + lane);
-        seq[s0 + lane] = make_int2(len, n);
-        const int tiles = sequence_tiles(len, n);
-        x = static_cast<long long>(tiles ? tiles + kExtra : 0) * ((n * p.group + kRows - 1) / kRows) * p.v.n_kv;
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (s0 + lane < p.v.n_seq) before[s0 + lane + 1] = run + x;
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) {
-      before[0] = 0;
-      const int ctas = static_cast<int>(run < gridDim.x ? run : gridDim.x);
-      long long b = 0, e = 0;
-      if (blockIdx.x < ctas) {
-        const Shares sh(run, ctas);
-        b = sh.begin(blockIdx.x);
-        e = sh.begin(blockIdx.x + 1);
-      }
-      before[p.v.n_seq + 1] = b;
-      before[p.v.n_seq + 2] = e;
-    }
-  }
-  __syncthreads();
-  if (blockIdx.x == 0)  // for the join
-    for (int s = tid; s <= p.v.n_seq; s += L::kThreads) p.before[s] = before[s];
-  // tokens beyond a sequence's tree: 0
-  if (p.n_tok)
-    for (int r = blockIdx.x; r < p.v.n_seq * p.ntok; r += gridDim.x) {
-      if (r % p.ntok < seq[r / p.ntok].y) continue;
-      float4 *o = reinterpret_cast<float4 *>(p.out + static_cast<int64_t>(r) * p.n_heads * kD);
-      for (int i = tid; i < p.n_heads * kD / 4; i += L::kThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  const long long begin = before[p.v.n_seq + 1], end = before[p.v.n_seq + 2];
+  find_work<kRows>(p, wk);
+  clear_unused(p, wk);
+  const long long begin = wk.begin, end = wk.end;
   if (begin == end) return;
-  // the item that holds tile x, and the tile's place in it
-  auto find = [&](long long x, Item &it) {
-    int lo = 0, hi = p.v.n_seq - 1;
-    while (lo < hi) {  // the last sequence with before[s] <= x (empty ones are passed over)
-      const int mid = (lo + hi + 1) / 2;
-      if (before[mid] <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    it.s = lo;
-    it.len = seq[lo].x;
-    it.n = seq[lo].y;
-    it.tiles = sequence_tiles(it.len, it.n);
-    const int nrt = (it.n * p.group + kRows - 1) / kRows;
-    const long long rel = x - before[lo];
-    int k, tile;
-    const int units = it.tiles + kExtra;
-    if (rel >> 31) {
-      k = static_cast<int>(rel / units);
-      tile = static_cast<int>(rel % units);
-    } else {
-      k = static_cast<int>(rel) / units;
-      tile = static_cast<int>(rel) - k * units;
-    }
-    it.h = k / nrt;
-    it.rt = k - it.h * nrt;
-    return tile;
-  };
+  auto find = [&](long long x, Item &it) { return find_item<kRows>(p, wk, x, it); };
   const int piece_rows = min(p.v.P, kTile);
 
   // ---------------------------------------------------------------- loads
@@ -780,8 +867,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       float *dst = part + r * (kD + 4);
       if (whole) {
         f = l != 0.0f ? f / l : 0.0f;
-        dst = p.out + (static_cast<int64_t>(it.s) * p.ntok + row / p.group) * p.n_heads * kD +
-              (it.h * p.group + row % p.group) * kD;
+        dst = out_row(p, it.s, it.h, row);
       } else if (wb == 0 && t == 0) {
         *reinterpret_cast<float2 *>(dst + kD) = make_float2(m_run[b], l);
       }
@@ -797,67 +883,9 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       mbar_wait(&full[i % kStages], (i / kStages) & 1, p.err, DEVERR_DRAIN_WAIT, i);
 }
 
-// Joins the parts of the items that more than one CTA holds: one warp per
-// (item, row), the parts in the order of their positions.
-template <int NB, int WM>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ TreeParams p, int grid) {
-  constexpr int kRows = 16 * WM, kD = 32 * NB;
-  constexpr long long kPart = Plan<NB, WM>::kPart;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
-  const int x = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);  // (head, row of the head)
-  const int rows = p.ntok * p.group, h = x / rows, row = x - h * rows;
-  const long long first = p.before[s], total = p.before[p.v.n_seq];
-  const int n = tree_size(p, s);
-  const int tiles = sequence_tiles(seq_length(p.v, s), n);
-  if (h >= p.v.n_kv || row >= n * p.group) return;
-  const int nrt = (n * p.group + kRows - 1) / kRows;
-  const Shares sh(total, static_cast<int>(grid < total ? grid : total));
-  const long long i0 = first + static_cast<long long>(h * nrt + row / kRows) * (tiles + kExtra);
-  const int c0 = sh.holder(i0), c1 = sh.holder(i0 + tiles - 1);
-  if (c0 == c1) return;  // one CTA held it whole and wrote it
-  // only the first of the item's CTAs can have begun before it
-  const float *rest = p.parts + (row % kRows) * (kD + 4);
-  const float *head = rest + (sh.begin(c0) >= i0 ? 0 : kPart);
-  auto part = [&](int c) { return (c == c0 ? head : rest) + 2 * kPart * c; };
-  float top = -INFINITY, den = 0.0f;
-  float4 y[NB / 4] = {};
-  for (int b = c0; b <= c1; b += 32) {  // 32 parts at a time: a lane holds the maximum and sum of one
-    const int m = min(32, c1 - b + 1);
-    const float2 ml = lane < m ? *reinterpret_cast<const float2 *>(part(b + lane) + kD) : make_float2(-INFINITY, 0.0f);
-    const float up = fmaxf(top, warp_max_all(ml.x));
-    const float ref = up == -INFINITY ? 0.0f : up;
-    const float keep = exp2f(top - ref), f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
-    top = up;
-    den = fmaf(den, keep, warp_sum_xor<32>(f * ml.y));
-#pragma unroll
-    for (int e = 0; e < NB / 4; ++e) y[e].x *= keep, y[e].y *= keep, y[e].z *= keep, y[e].w *= keep;
-#pragma unroll 8
-    for (int c = 0; c < m; ++c) {
-      const float fc = __shfl_sync(0xffffffffu, f, c);
-      const float4 *src = reinterpret_cast<const float4 *>(part(b + c)) + lane;
-#pragma unroll
-      for (int e = 0; e < NB / 4; ++e) {
-        const float4 a = src[32 * e];
-        y[e].x = fmaf(fc, a.x, y[e].x);
-        y[e].y = fmaf(fc, a.y, y[e].y);
-        y[e].z = fmaf(fc, a.z, y[e].z);
-        y[e].w = fmaf(fc, a.w, y[e].w);
-      }
-    }
-  }
-  float *out = p.out + (static_cast<int64_t>(s) * p.ntok + row / p.group) * p.n_heads * kD +
-               (h * p.group + row % p.group) * kD;
-#pragma unroll
-  for (int e = 0; e < NB / 4; ++e)
-    *reinterpret_cast<float4 *>(out + 128 * e + 4 * lane) =
-        den != 0.0f ? make_float4(y[e].x / den, y[e].y / den, y[e].z / den, y[e].w / den) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
 constexpr size_t kHeadBytes = 8 * (kMaxSeq + 8);
 
-// rows of a row tile for ntok tokens of `group` heads
+// rows of a row tile for `rows` rows per key/value head (tokens times group)
 inline int tile_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
 template <int NB, int WM>
@@ -871,9 +899,7 @@ cudaError_t launch_tree(const TreeParams &p, const DeviceInfo &dev, cudaStream_t
   const int grid = std::min(kMaxCtas, dev.sm_count * per_sm);
   e = launch_pdl(k, dim3(grid), dim3(L::kThreads), L::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  const int rows = p.v.n_kv * p.ntok * p.group;
-  return launch_pdl(join_kernel<NB, WM>, dim3((rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.v.n_seq),
-                    dim3(kJoinThreads), 0, s, p, grid);
+  return launch_join<L::kD, L::kRows>(p, grid, s);
 }
 
 }  // namespace
@@ -931,7 +957,7 @@ extern "C" epq_status epq_attention_tree(const epq_pages *pages, int layer, cons
   p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kHeadBytes);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool small = tile_rows(ntok * p.group) == 16;
-  cudaError_t e = D == 128 ? (small ? launch_tree<4, 1>(p, dev, s) : launch_tree<4, 2>(p, dev, s))
-                           : (small ? launch_tree<8, 1>(p, dev, s) : launch_tree<8, 2>(p, dev, s));
+  const cudaError_t e = D == 128 ? (small ? launch_tree<4, 1>(p, dev, s) : launch_tree<4, 2>(p, dev, s))
+                                 : (small ? launch_tree<8, 1>(p, dev, s) : launch_tree<8, 2>(p, dev, s));
   return e == cudaSuccess ? EPQ_OK : cuda_fail(e);
 }
