@@ -19,12 +19,15 @@
 //            multiplies the weights by that block's factors.  A weight is kept
 //            as two fp16 parts, so a product is three half2 operations: its
 //            rounded value, what the rounding lost (exact), plus the second
-//            part's product: 2^-22 of it, or 2^-39 of the largest one.  That
-//            floor would show where every larger weight meets a code 0, so it
-//            is only used where a row has at least 12 weights within 2^-16 of
-//            its largest; a tile with another row (or with drafted tokens, whose
-//            factors may not be finite) takes float32 products in three bf16
-//            parts, which lose nothing.
+//            part's product: 2^-22 of it, or 2^-34 of one at the reference.
+//            That floor would show where every larger weight meets a code 0, so
+//            a tile with a weight below 2^-14 in a row that has not had 12
+//            larger ones takes float32 products in three bf16 parts, which lose
+//            nothing.
+// The weights of a row are relative to its maximum at some earlier tile (the
+// reference), which moves, and the sums with it, only when a weight passes 2^6:
+// so the warps need not agree on a maximum before they form weights, and one
+// barrier per tile is enough.
 // Work: the tiles of all (sequence, head, row tile) items in a row, cut into
 // equal shares, one per CTA.  An item counts kExtra tiles more than it has:
 // beginning it, and its last tile with the new rows, take that long.  A CTA's part of an item that it does not hold
@@ -90,9 +93,10 @@ struct Shares {
   }
 };
 
-constexpr float kUp = 14.0f;         // log2 of the largest weight of a row as it is held
-constexpr float kWeighty = 0.25f;    // a weight that counts: 2^-16 of the largest
-constexpr float kWeightyMin = 3.0f;  // of them, in each of a row's four lanes
+constexpr float kUp = 9.0f;           // log2 of a weight at its row's reference as it is held
+constexpr float kPast = 32768.0f;     // largest weight as it is held: 2^6 at the reference
+constexpr float kWeighty = 0.03125f;  // a weight that counts, as it is held: 2^-14 at the reference
+constexpr float kWeightyMin = 12.0f;  // of them, among a warp's positions
 
 // What a work item is: row tile rt of head h of sequence s.
 struct Item {
@@ -356,15 +360,14 @@ struct Plan {
   static constexpr uint32_t oStage = 0;
   static constexpr uint32_t oQ = oStage + kStages * kStageBytes;    // query fragments, two parts
   static constexpr uint32_t oW = oQ + 2u * 2u * kRows * kD;         // [2][rows][64] weights
-  static constexpr uint32_t oMax = oW + 2u * 4u * kRows * kTile;    // [2][NB][rows] tile maxima
-  static constexpr uint32_t oSum = oMax + 2u * 4u * NB * kRows;     // [NB][rows]
+  static constexpr uint32_t oMax = oW + 2u * 4u * kRows * kTile;    // [NB][rows] maxima
+  static constexpr uint32_t oSum = oMax + 4u * NB * kRows;          // [NB][rows]
   static constexpr uint32_t oMask = oSum + 4u * NB * kRows;         // [rows] mask words
   static constexpr uint32_t oScale = oMask + 8u * kRows;            // [rows] score factors (log2 units)
   static constexpr uint32_t oWork = oScale + 4u * kRows;            // Work
   static constexpr uint32_t oBar = oWork + sizeof(Work);            // full
-  static constexpr uint32_t oFactor = oBar + 8u * (kStages + 1);    // [2][NB] largest value factor
-  static constexpr uint32_t oWide = oFactor + 2u * 4u * NB;         // [2][warps] three parts wanted
-  static constexpr uint32_t oMiss = oWide + 2u * 4u * kWarps;       // [stages] missing pieces
+  static constexpr uint32_t oTell = oBar + 8u * (kStages + 1);      // [2][warps] see `tell`
+  static constexpr uint32_t oMiss = oTell + 2u * 8u * kWarps;       // [stages] missing pieces
   static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
 
@@ -507,12 +510,13 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
     }
     __syncthreads();
 
-    float o[4][4] = {}, s[2][kOwn];  // s: scores of rows g, g + 8 at the lane's positions
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {}, weighty[2] = {};
+    float o[4][4] = {}, s[2][kOwn];  // s: scores, then weights, of rows g, g + 8 at the lane's positions
+    float ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {}, weighty[2] = {};
     const float c_row[2] = {row_scale[16 * wm + g], row_scale[16 * wm + 8 + g]};
-    float unit = 1.0f, d_min = 0.0f;  // power of two on the value factors; smallest factor of the warp's positions
+    float unit = 1.0f;     // power of two on the value factors: the largest of a tile comes into [1, 2)
+    uint32_t factors = 0;  // of the warp's positions: the largest (upper half) and smallest (lower) value factor, fp16
 
-    // Scores of tile `tile` (pipeline step kk) into s, its row maxima into oMax.
+    // Scores of tile `tile` (pipeline step kk) into s.
     auto scores = [&](int tile, uint32_t kk) {
       const int st = kk % kStages;
       uint8_t *kt = smem + L::oStage + st * L::kStageBytes, *vt = kt + kTile * kRow;
@@ -627,6 +631,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         }
       }
       // the largest value factor of each of the warp's positions: their range
+      // (positions without any do not count)
       {
         const uint8_t *r = vt + (wb * L::kKeys + (lane & (L::kKeys - 1))) * kRow;
         __half2 a = __half2half2(__ushort_as_half(0));
@@ -635,77 +640,109 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           const uint2 f = *reinterpret_cast<const uint2 *>(r + 8 * b);
           a = __hmax2(a, __hmax2(__habs2(as_half2(f.x)), __habs2(as_half2(f.y))));
         }
-        const uint32_t bits = __float_as_uint(fmaxf(__low2float(a), __high2float(a)));
-        d_min = __uint_as_float(__reduce_min_sync(0xffffffffu, bits));
-        const uint32_t top = __reduce_max_sync(0xffffffffu, bits);
-        if (wm == 0 && lane == 0) reinterpret_cast<uint32_t *>(smem + L::oFactor)[(kk & 1) * NB + wb] = top;
+        uint32_t bits = __half_as_ushort(__hmax(__low2half(a), __high2half(a)));
+        if (special && bits == 0x7c00u) bits = 0;  // not finite: not in the products
+        factors = __reduce_max_sync(0xffffffffu, bits) << 16 | __reduce_min_sync(0xffffffffu, bits ? bits : 0x7c00u);
       }
-      float *mx = reinterpret_cast<float *>(smem + L::oMax) + ((kk & 1) * NB + wb) * kRows + 16 * wm;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float m = -INFINITY;
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int j = 0; j < kOwn; ++j) s[b][j] *= c_row[b];
-        if (special) {
-          const uint64_t may = row_mask[16 * wm + 8 * b + g];
+      if (special) {
+        // A value factor that is not finite counts as 0 in the products; a row
+        // that sees it, or a score that is not finite, becomes NaN here, which
+        // moves no reference: the other rows' results stay as they are.
 #pragma unroll
-          for (int j = 0; j < kOwn; ++j) {
-            const int r = wb * L::kKeys + kOwn * t + j, i = t0 + r - it.len;
+        for (int j = 0; j < kOwn; ++j) {
+          const int r = wb * L::kKeys + kOwn * t + j, i = t0 + r - it.len;
+          float bad = 0.0f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) bad += 0.0f * f16_at(vt + r * kRow + 2 * b);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint64_t may = row_mask[16 * wm + 8 * b + g];
             const bool see = i < 0 ? !(lost >> (2 * (r / piece_rows)) & 1) : i < 64 && (may >> i & 1);
-            if (!see) s[b][j] = -INFINITY;
+            s[b][j] = see ? s[b][j] + fmaf(s[b][j], 0.0f, bad) : -INFINITY;
           }
         }
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) m = fmaxf(m, s[b][j]);
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        if (t == 0) mx[8 * b + g] = m;
       }
     };
 
-    scores(first, k);
-    __syncthreads();
-    for (int tile = first; tile < last; ++tile, ++k) {
+    // A turn: scores and weights of a tile, the barrier, its values; a turn whose
+    // weights pass the reference too far begins again with a new one.
+    bool fresh = true;
+#pragma unroll 1
+    for (int tile = first; tile < last;) {
       const int st = k % kStages;
-      const bool special = tile * kTile + kTile > it.len;
-      // ------------------------------------------------------------ weights
-      float keep[2];  // on the sums so far (keep) and on the output so far (keep * moved)
-      float *w = reinterpret_cast<float *>(smem + L::oW) + ((k & 1) * kRows + 16 * wm) * kTile;
-      int *wide = reinterpret_cast<int *>(smem + L::oWide) + (k & 1) * L::kWarps + wm * NB;
-      float moved;
-      {
-        uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < NB; ++c)
-          top = max(top, reinterpret_cast<const uint32_t *>(smem + L::oFactor)[(k & 1) * NB + c]);
-        // the largest factor of the tile times new_unit is in [1, 2)
-        const float new_unit = exp2i(min(max(127 - static_cast<int>(top >> 23), -15), 15));
-        moved = new_unit * (1.0f / unit);
-        unit = new_unit;
-        const float *mx = reinterpret_cast<const float *>(smem + L::oMax) + (k & 1) * NB * kRows + 16 * wm;
-        float e[2][kOwn];
-        bool few = special || !(d_min * unit >= kWeighty);
+      scores(tile, k);
+      if (fresh) {  // new references
+        float *mx = reinterpret_cast<float *>(smem + L::oMax) + 16 * wm + g;
+        float m[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float m = m_run[b];
+          m[b] = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NB; ++c) m = fmaxf(m, mx[c * kRows + 8 * b + g]);
-          const float ref = m == -INFINITY ? 0.0f : m - kUp;
-          keep[b] = m_run[b] == m ? 1.0f : exp2_approx(m_run[b] - m);
-          m_run[b] = m;
-          float sum = 0.0f, many = 0.0f;
+          for (int j = 0; j < kOwn; ++j) m[b] = fmaxf(m[b], s[b][j]);
+          m[b] = fmaxf(m[b], __shfl_xor_sync(0xffffffffu, m[b], 1));
+          m[b] = fmaxf(m[b], __shfl_xor_sync(0xffffffffu, m[b], 2));
+          if (t == 0) mx[wb * kRows + 8 * b] = m[b];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float top = ref[b];
+#pragma unroll
+          for (int c = 0; c < NB; ++c) top = fmaxf(top, mx[c * kRows + 8 * b]);
+          const float keep = ref[b] == top ? 1.0f : exp2_approx(ref[b] - top);
+          ref[b] = top;
+          l_run[b] *= keep;
+          weighty[b] *= keep;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[j][2 * b] *= keep;
+            o[j][2 * b + 1] *= keep;
+          }
+        }
+      }
+      // ------------------------------------------------------------ weights
+      float *w = reinterpret_cast<float *>(smem + L::oW) + ((k & 1) * kRows + 16 * wm) * kTile;
+      // of a warp: its positions' value factors; bit 0: a weight past the
+      // reference, bit 1: held in float32
+      uint2 *tell = reinterpret_cast<uint2 *>(smem + L::oTell) + (k & 1) * L::kWarps;
+      float sum[2], now[2] = {weighty[0], weighty[1]};
+      {
+        float over = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float from = ref[b] == -INFINITY ? 0.0f : ref[b] - kUp;
+          sum[b] = 0.0f;
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {
-            e[b][j] = exp2_approx(s[b][j] - ref);
-            sum += e[b][j];
-            many += e[b][j] >= kWeighty ? 1.0f : 0.0f;
+            s[b][j] = exp2_approx(s[b][j] - from);
+            sum[b] += s[b][j];
+            over = fmaxf(over, s[b][j]);
           }
-          l_run[b] = fmaf(l_run[b], keep[b], sum);
-          weighty[b] = fmaf(weighty[b], keep[b], many);
-          few = few || weighty[b] < kWeightyMin;
+        }
+        // weights that count, until a row has enough of them
+        bool few = false;
+        if (__any_sync(0xffffffffu, fminf(weighty[0], weighty[1]) < kWeightyMin)) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float many = 0.0f, small = kPast;
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+              many += s[b][j] < kWeighty ? 0.0f : 1.0f;  // NaN counts
+              small = fminf(small, s[b][j] > 0.0f ? s[b][j] : kPast);
+            }
+            many += __shfl_xor_sync(0xffffffffu, many, 1);
+            many += __shfl_xor_sync(0xffffffffu, many, 2);
+            now[b] += many;
+            few = few || (now[b] < kWeightyMin && small < kWeighty);
+          }
         }
         few = __any_sync(0xffffffffu, few);
-        if (lane == 0) wide[wb] = few;
+        const bool past = __any_sync(0xffffffffu, over > kPast);
+        if (lane == 0) tell[warp] = make_uint2(factors, (past ? 1u : 0u) | (few ? 2u : 0u));
         // the 16-byte chunks of odd rows are stored with bit 2 of their index
         // flipped; a chunk is 4 weights, or their first parts, then the second
         const int col = (wb * L::kKeys + kOwn * t) ^ ((g & 1) << 4);
@@ -714,19 +751,19 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           float *dst = w + (8 * b + g) * kTile + col;
           if constexpr (kNT == 2) {
             if (few) {
-              *reinterpret_cast<float4 *>(dst) = make_float4(e[b][0], e[b][1], e[b][2], e[b][3]);
+              *reinterpret_cast<float4 *>(dst) = make_float4(s[b][0], s[b][1], s[b][2], s[b][3]);
             } else {
               uint4 h;
-              split_half2(e[b][0], e[b][1], h.x, h.z);
-              split_half2(e[b][2], e[b][3], h.y, h.w);
+              split_half2(s[b][0], s[b][1], h.x, h.z);
+              split_half2(s[b][2], s[b][3], h.y, h.w);
               *reinterpret_cast<uint4 *>(dst) = h;
             }
           } else {
             if (few) {
-              *reinterpret_cast<float2 *>(dst) = make_float2(e[b][0], e[b][1]);
+              *reinterpret_cast<float2 *>(dst) = make_float2(s[b][0], s[b][1]);
             } else {
               uint32_t h0, h1;
-              split_half2(e[b][0], e[b][1], h0, h1);
+              split_half2(s[b][0], s[b][1], h0, h1);
               uint32_t *u = reinterpret_cast<uint32_t *>(dst - 2 * (t & 1)) + (t & 1);
               u[0] = h0;
               u[2] = h1;
@@ -734,21 +771,45 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           }
         }
       }
-      if (tile + 1 < last) scores(tile + 1, k + 1);
       __syncthreads();
       // every warp is past the values of the tile before: its stage is free
+      uint32_t top = 0, bottom = 0x7c00u, flags = 0;
+      uint32_t wide = 0;  // bit c: warp c of the row group holds its weights in float32
+#pragma unroll
+      for (int c = 0; c < L::kWarps; ++c) {
+        const uint2 x = tell[c];
+        flags |= x.y & 1;
+        if (c / NB == wm) wide |= (x.y >> 1) << (c % NB);
+        if (c < NB) {
+          top = max(top, x.x >> 16);
+          bottom = min(bottom, x.x & 0xffffu);
+        }
+      }
+      fresh = flags;
+      if (fresh) {
+        __syncthreads();  // `tell` and the maxima are written again
+        continue;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        l_run[b] += sum[b];
+        weighty[b] = now[b];
+      }
       if (warp == 0) {
         load();
         look_ahead();
       }
+      const float new_unit = exp2i(min(max(15 - static_cast<int>(top >> 10), -15), 15));
+      const float moved = new_unit * (1.0f / unit);
+      unit = new_unit;
+      // factors that differ by more than 2^11 in a tile: float32, too
+      const bool slow = wide || (top >> 10) > (bottom >> 10) + 11;
+      const bool special = tile * kTile + kTile > it.len;
       // ------------------------------------------------------------ values
       // The tile's products go to accumulators of their own: the tensor cores
       // round every sum towards zero, which over a long context would add up.
       float acc[4][4] = {};
       const uint8_t *vt = smem + L::oStage + st * L::kStageBytes + kTile * kRow;
-      bool slow = false;
-#pragma unroll
-      for (int c = 0; c < NB; ++c) slow = slow || wide[c];
       // A operands of 16 positions: the lane's 4 are 16 kg + 4 t ..., of rows g
       // and g + 8; B operands: column n of MMA tile j is element 4 n + j of the
       // block.
@@ -766,6 +827,10 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           const int col = (16 * kg + 4 * t) ^ ((g & 1) << 4);
           const uint4 x0 = *reinterpret_cast<const uint4 *>(w + g * kTile + col);
           const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
+          if (special) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = (f[j] & 0x7c00u) == 0x7c00u ? 0u : f[j];
+          }
           const __half2 d01 = __hmul2(as_half2(__byte_perm(f[0], f[1], 0x5410)), unit2);
           const __half2 d23 = __hmul2(as_half2(__byte_perm(f[2], f[3], 0x5410)), unit2);
           auto times = [](uint32_t h, uint32_t l, __half2 d, uint32_t &hi, uint32_t &lo) {
@@ -797,7 +862,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           const uint4 x1 = *reinterpret_cast<const uint4 *>(w + (8 + g) * kTile + col);
           float y0[4] = {__uint_as_float(x0.x), __uint_as_float(x0.y), __uint_as_float(x0.z), __uint_as_float(x0.w)};
           float y1[4] = {__uint_as_float(x1.x), __uint_as_float(x1.y), __uint_as_float(x1.z), __uint_as_float(x1.w)};
-          if (!wide[kNT == 2 ? kg : 2 * kg + (t >> 1)]) {  // held as two parts
+          if (!(wide >> (kNT == 2 ? kg : 2 * kg + (t >> 1)) & 1)) {  // held as two parts
             auto whole = [](uint32_t h, uint32_t l, float *y) {
               const float2 a = __half22float2(as_half2(h)), b = __half22float2(as_half2(l));
               y[0] = a.x + b.x;
@@ -834,14 +899,12 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           }
         }
       }
-      const float k0 = keep[0] * moved, k1 = keep[1] * moved;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o[j][0] = fmaf(o[j][0], k0, acc[j][0]);
-        o[j][1] = fmaf(o[j][1], k0, acc[j][1]);
-        o[j][2] = fmaf(o[j][2], k1, acc[j][2]);
-        o[j][3] = fmaf(o[j][3], k1, acc[j][3]);
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[j][c] = fmaf(o[j][c], moved, acc[j][c]);
+      ++tile;
+      ++k;
     }
 
     // -------------------------------------------------------------- the item's rows
@@ -869,7 +932,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         f = l != 0.0f ? f / l : 0.0f;
         dst = out_row(p, it.s, it.h, row);
       } else if (wb == 0 && t == 0) {
-        *reinterpret_cast<float2 *>(dst + kD) = make_float2(m_run[b], l);
+        *reinterpret_cast<float2 *>(dst + kD) = make_float2(ref[b], l);
       }
       // the lane's 8 columns 8 t ... of the warp's block
       float4 *d4 = reinterpret_cast<float4 *>(dst + 32 * wb + 8 * t);
