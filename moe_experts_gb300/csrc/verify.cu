@@ -226,21 +226,29 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
     lx[tid] = known ? p.logits[static_cast<int64_t>(base + a) * p.ld + x] : -INFINITY;
     qx[tid] = known && use_draft ? p.draft[static_cast<int64_t>(base + a) * p.draft_ld + x] : 1.0f;
   }
-  for (int r = warp; r < n; r += kWalkWarps) {
-    const int64_t i = static_cast<int64_t>(base + r) * p.splits;
-    float m = -INFINITY, z = 0.0f;
-    int at = 0x7fffffff;
-    for (int k = lane; k < p.splits; k += 32) take_max(m, at, p.part_max[i + k], p.part_arg[i + k]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      take_max(m, at, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, at, o));
-    for (int k = lane; k < p.splits; k += 32) z += join_sum(p.part_max[i + k], p.part_sum[i + k], m, p.c_hi);
-    z = warp_sum_xor<32>(z);
-    if (lane == 0) {
-      top[r] = m;
-      sum[r] = z;
-      arg[r] = at < p.vocab ? at : 0;  // a row without a finite logit
-      if (writer && p.lse) p.lse[base + r] = m * p.inv_t + logf(z);
+  // A row's chunks joined by half a warp (a whole one when there are more than
+  // 16), so that 64 rows take two rounds of loads.
+  {
+    const int width = p.splits <= 16 ? 16 : 32, rows = 32 / width, l = lane & (width - 1);
+    for (int r0 = warp * rows; r0 < n; r0 += kWalkWarps * rows) {  // the same turns for both halves
+      const int r = r0 + lane / width;
+      const int64_t i = static_cast<int64_t>(base + min(r, n - 1)) * p.splits;
+      float m = -INFINITY, z = 0.0f;
+      int at = 0x7fffffff;
+      auto join = [&](float m2, float z2, int at2) {
+        const float up = fmaxf(m, m2);
+        z = join_sum(m, z, up, p.c_hi) + join_sum(m2, z2, up, p.c_hi);
+        take_max(m, at, m2, at2);
+      };
+      for (int k = l; k < p.splits; k += width) join(p.part_max[i + k], p.part_sum[i + k], p.part_arg[i + k]);
+      for (int o = width / 2; o > 0; o >>= 1)
+        join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, z, o), __shfl_xor_sync(0xffffffffu, at, o));
+      if (l == 0 && r < n) {
+        top[r] = m;
+        sum[r] = z;
+        arg[r] = at < p.vocab ? at : 0;  // a row without a finite logit
+        if (writer && p.lse) p.lse[base + r] = m * p.inv_t + logf(z);
+      }
     }
   }
   __syncthreads();
