@@ -348,7 +348,7 @@ extern "C" epq_status epq_pages_reserve(const epq_pages *pages, const int32_t *e
   if (!err) return EPQ_ERR_DEVICE;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_pdl(reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, v, extra, status);
-  if (e == cudaSuccess && v.n_seq > 1) {  // a page of a single sequence is never shared
+  if (e == cudaSuccess) {  // also for one sequence: another cache over the pool may hold its page
     // all branches in one CTA, unless that leaves SMs idle
     const int units = v.n_layers * v.n_kv * 2;
     const int groups = std::min(v.n_seq, std::max(1, 8 * dev.sm_count / units));

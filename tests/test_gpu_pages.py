@@ -178,3 +178,26 @@ def test_bad_state_is_not_followed(epq_lib, cuda_dev):
     assert c.table.tolist() == [[9, -5, 2], [0, 1, -1]] and c.refs.tolist() == [1, 1, 1, 0]
     epq_lib.epq_pages_truncate(c, i32([0, 0]))
     assert c.refs.tolist() == [0, 0, 0, 0] and epq_lib.epq_device_error() == 0
+
+
+@pytest.mark.parametrize("P, D, rows", [(16, 128, 5), (64, 256, 63)])
+def test_one_sequence_over_a_shared_page(epq_lib, cuda_dev, P, D, rows):
+    """Two caches over one pool and its reference counts, the second with a
+    single sequence: its partly filled page, which the first holds too, is
+    copied before it is written."""
+    b = Both(epq_lib, cuda_dev, D=D, P=P)
+    b.reserve([rows, 0, 0, 0])
+    for i in range(rows):
+        b.write(0, i)
+    b.compact([list(range(rows))] + [[-1] * rows] * 3, [rows, 0, 0, 0])
+    b.same()
+    shared = b.o.table[0][0]
+    b.c.refs[shared] += 1
+    one = epq_lib.PagedKVCache.over(b.c.pool, b.c.table[:1].clone(), b.c.length[:1].clone(), b.c.refs)
+    kept = b.c.pool[:, shared].clone()
+    assert epq_lib.epq_pages_reserve(one, b.i32([1])).tolist() == [0]
+    own = one.table[0, 0].item()
+    assert own != shared and b.c.refs.tolist()[shared] == b.c.refs.tolist()[own] == 1
+    assert torch.equal(b.c.pool[:, own, :, :, :rows], kept[:, :, :, :rows])
+    assert torch.equal(b.c.pool[:, shared], kept)
+    assert epq_lib.epq_device_error() == 0
