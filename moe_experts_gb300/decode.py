@@ -253,6 +253,7 @@ class TreeDecoder:
         self.mask = torch.empty((1, ntok), dtype=torch.int64, device=device)
         self.extra = torch.full((1,), ntok, **i32)
         self.status = torch.zeros(1, **i32)
+        self.n_tok = torch.zeros(1, **i32)  # ntok, or 0 when the cache has no room
         self.path, self.n_accept, self.next_token = (torch.empty(n, **i32) for n in ((1, ntok), (1,), (1,)))
         self.lse = torch.empty((1, ntok), **f32)
         self.attn_ws = L.epq_attention_tree_workspace(cache, cfg.heads, ntok)
@@ -261,18 +262,22 @@ class TreeDecoder:
     def forward(self, x, parent, stream=None):
         """x [ntok, H] (the tokens' embeddings), parent int32 [1, ntok] ->
         logits [1, ntok, vocab]; the tokens' rows lie behind the committed
-        positions.  status is nonzero when the cache had no room."""
+        positions.  status is nonzero when the cache had no room: nothing is
+        stored then, and the logits mean nothing."""
         c, f, H, nq, nkv = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows
         h, qkv, attn = self.h, self.qkv, self.attn
         L.epq_pages_reserve(self.cache, self.extra, self.status, stream=stream)
+        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(on):
+            torch.mul(self.extra, self.status == 0, out=self.n_tok)
         L.epq_tree_mask(parent, self.mask, stream=stream)
         q, k, v = qkv[..., :nq], qkv[..., nq:nq + nkv], qkv[..., nq + nkv:]
         for li, (wqkv, wo, wgu, wd) in enumerate(self.layers):
             src = x if li == 0 else h
             L.epq_gemv_ex(f, wqkv, src, nq + 2 * nkv, H, y=qkv[0], rms_prenorm=True, rms_eps=c.rms_eps,
                           weights_ready=True, stream=stream)
-            L.epq_attention_tree(q, k, v, self.cache, li, c.heads, 1.0 / math.sqrt(c.head_dim), mask=self.mask, out=attn,
-                                 workspace=self.attn_ws, stream=stream)
+            L.epq_attention_tree(q, k, v, self.cache, li, c.heads, 1.0 / math.sqrt(c.head_dim), mask=self.mask,
+                                 n_tok=self.n_tok, out=attn, workspace=self.attn_ws, stream=stream)
             L.epq_gemv_ex(f, wo, attn[0], H, nq, y=h, residual=src, weights_ready=True, stream=stream)
             L.epq_gemv_ex(f, wgu, h, 2 * c.inter, H, y=self.m, rms_prenorm=True, rms_eps=c.rms_eps, swiglu=True,
                           weights_ready=True, stream=stream)
@@ -285,10 +290,11 @@ class TreeDecoder:
         """One verification step: forward, the walk, the commit.  tokens,
         parent int32 and u float32 [1, ntok], draft None or float32 [1, ntok,
         vocab] -> (path, n_accept, next_token); the cache then holds the
-        accepted tokens, and next_token is the root of the next step."""
+        accepted tokens, and next_token is the root of the next step.  A cache
+        without room stays as it is: n_accept 0, next_token -1, status nonzero."""
         self.forward(x, parent, stream=stream)
-        L.epq_verify_tree(self.logits, tokens, parent, u, draft=draft, temperature=temperature, path=self.path,
-                          n_accept=self.n_accept, next_token=self.next_token, lse=self.lse, workspace=self.verify_ws,
+        L.epq_verify_tree(self.logits, tokens, parent, u, draft=draft, n_tok=self.n_tok, temperature=temperature,
+                          path=self.path, n_accept=self.n_accept, next_token=self.next_token, lse=self.lse, workspace=self.verify_ws,
                           stream=stream)
         L.epq_pages_compact(self.cache, self.path, self.n_accept, stream=stream)
         return self.path, self.n_accept, self.next_token

@@ -112,3 +112,20 @@ def test_committed_step_and_graph(epq_lib, cuda_dev, setup, monkeypatch):
         if i == 0:
             assert t2.path.tolist() == [[0, 2, 4, -1, -1, -1]] and torch.equal(t2.logits, t.logits)
     assert epq_lib.epq_device_error() == 0
+
+
+def test_cache_without_room(epq_lib, cuda_dev, setup):
+    """A step that cannot reserve its rows stores, accepts and commits nothing, on another stream too."""
+    t = _tree(epq_lib, cuda_dev, setup)
+    t.cache.refs[t.cache.refs == 0] = 1  # every other page is held elsewhere
+    t.cache.length.fill_(95)             # one row is left in the last page
+    pool = t.cache.pool.clone()
+    parent = torch.arange(-1, NTOK - 1, dtype=torch.int32, device=cuda_dev).view(1, -1)
+    tokens, u = torch.zeros((1, NTOK), dtype=torch.int32, device=cuda_dev), torch.zeros((1, NTOK), device=cuda_dev)
+    torch.cuda.synchronize()
+    for stream in (None, torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        path, n, nxt = t.step(setup[3], tokens, parent, u, temperature=0.0, stream=stream)
+        torch.cuda.synchronize()
+        assert t.status.item() == 1 and n.item() == 0 and nxt.item() == -1 and path.tolist() == [[-1] * NTOK]
+        assert t.cache.length.item() == 95 and torch.equal(t.cache.pool, pool)
+    assert epq_lib.epq_device_error() == 0
