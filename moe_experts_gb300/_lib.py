@@ -157,6 +157,13 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _own_scratch(t: torch.Tensor, stream) -> torch.Tensor:
+    """Scratch that a call allocates for itself, kept from reuse until `stream` (not the current one) is done with it."""
+    if stream is not None and t.is_cuda:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
 def _check(fn: str, st: int):
     if st != 0:
         raise EpqError(fn, st)
@@ -540,7 +547,7 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = epq_attention_tree_workspace(cache, n_heads, ntok)
+        workspace = _own_scratch(epq_attention_tree_workspace(cache, n_heads, ntok), stream)
     o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok)),
                           None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq),
                           q_tok, q_seq, kv_tok, kv_seq)
@@ -580,7 +587,7 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     next_token = torch.empty(each, dtype=i32, device=dev) if next_token is None else next_token
     lse = torch.empty(tree, dtype=f32, device=dev) if lse is None else lse
     if workspace is None:
-        workspace = epq_verify_tree_workspace(logits)
+        workspace = _own_scratch(epq_verify_tree_workspace(logits), stream)
     o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full),
                    None if n_tok is None else _need(n_tok, "n_tok", i32, each), temperature, 0, 0)
     st = lib.epq_verify_tree(
