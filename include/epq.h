@@ -6,7 +6,9 @@
  * formats, the fused dequantize-and-matrix-vector product y = deq(W) x (one to
  * eight activation vectors), and the mixture-of-experts layer built on it
  * (router softmax + top-K, gate/up with SwiGLU, down, weighted combine plus
- * residual).
+ * residual); attention over a Q8_0 key/value cache for one token, and for a
+ * tree of drafted tokens over pages that sequences share, with the acceptance
+ * of the drafted tokens and the pages' upkeep.
  *
  * Sources, cited by page title and section:
  *   [H]  "端侧推理：llama.cpp 与 GGUF、MLX、ExecuTorch" (edge-inference handbook),
@@ -421,7 +423,8 @@ epq_status epq_attention_decode(const float *q, const float *k_new, const float 
  *   table   int32 [n_seq][max_pages]: page ids, -1 = none; a sequence's pages
  *           are a prefix of its row
  *   length  int32 [n_seq]: committed positions
- *   refs    int32 [n_pages]: how many sequences hold a page (0 = free)
+ *   refs    int32 [n_pages]: how many sequences hold a page (0 = free), those
+ *           of other caches over the same pool and refs included
  *   work    device scratch of epq_pages_work_bytes() bytes, zero-filled before
  *           its first use; calls that share it must be ordered on one stream
  * An empty cache has table -1, length 0 and refs 0.  All state lives on the
@@ -431,8 +434,9 @@ epq_status epq_attention_decode(const float *q, const float *k_new, const float 
  * 256, n_kv_heads 1..256, max_pages * page_size <= 2^30 (EPQ_ERR_SHAPE),
  * 16-byte aligned pointers (EPQ_ERR_ALIGN).  Page ids, lengths and indices
  * are checked on the device: an entry outside its range counts as missing
- * and is never followed; a position that has to be read or written but has
- * no page is left out and recorded (epq_device_error code 5). */
+ * and is never followed.  A committed position without a page is left out; a
+ * drafted row without one is attended in its call but not stored.  Both are
+ * recorded (epq_device_error code 5). */
 typedef struct {
   void *pool;
   int32_t *table;
@@ -468,7 +472,8 @@ epq_status epq_pages_fork(const epq_pages *pages, const int32_t *src, const int3
  * write; of the holders in one call the last one left keeps the page).
  * status (int32 [n_seq]): 0 = done; 1 = not enough free pages (from the first
  * sequence that does not fit on, every later one with extra > 0 too), 2 =
- * longer than max_pages; such a sequence is unchanged. */
+ * longer than max_pages; such a sequence is unchanged, and has to be left out
+ * of the step (n_tok 0): its last page may still be shared. */
 epq_status epq_pages_reserve(const epq_pages *pages, const int32_t *extra, int32_t *status, epq_stream_t stream);
 
 /* epq_pages_compact: commits drafted rows.  For i < n_keep[s] the row at
@@ -521,8 +526,11 @@ size_t epq_attention_tree_workspace_bytes(const epq_pages *pages, int n_heads, i
  *                 16-byte aligned, needs no initialisation; calls that share
  *                 it must be ordered on one stream.
  * Requirements: ntok 1..64, n_heads a multiple of n_kv_heads, at most 16
- * heads per key/value head, scale > 0 and finite, finite q.  A drafted key or value
- * that is not finite reaches only the tokens that attend to it. */
+ * heads per key/value head, scale > 0 and finite, finite q.  A drafted key or
+ * value with a block whose factor is not finite (an element too large or
+ * infinite, or a block of NaN) makes the outputs of the tokens that attend to
+ * it NaN, in the heads that read it, and changes no other output.  A NaN among
+ * other elements is quantized as the packer does.  Two launches. */
 epq_status epq_attention_tree(const epq_pages *pages, int layer, const float *q, const float *k_new,
                               const float *v_new, int n_heads, int ntok, float scale,
                               const epq_attention_tree_opts *opts, float *out, void *ws, size_t ws_bytes,

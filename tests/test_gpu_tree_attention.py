@@ -173,6 +173,21 @@ def test_not_finite_where_masked(epq_lib, cuda_dev):
     assert epq_lib.epq_device_error() == 0
 
 
+@pytest.mark.parametrize("what", ["key", "value"])
+def test_rows_of_nan(epq_lib, cuda_dev, what):
+    """A drafted key or value of nothing but NaN: NaN for the tokens that attend to it, no other bit changed."""
+    c = Case(epq_lib, cuda_dev, [70], 6, 8, 2, 128, 16)
+    masks = [[1, 3, 4, 12, 17, 33]]
+    clean = c.run(masks=masks)
+    a = c.heads * c.D + (c.kv * c.D if what == "value" else 0)
+    c.qkv[0, 2, a:a + c.kv * c.D] = np.nan
+    got = c.run(masks=masks)
+    for i in (0, 1, 4, 5):
+        assert torch.equal(got[0, i], clean[0, i])
+    assert torch.isnan(got[0, 2]).all() and torch.isnan(got[0, 3]).all()
+    assert epq_lib.epq_device_error() == 0
+
+
 @pytest.mark.parametrize("kw", [dict(vscale=1e-4), dict(vscale=3e4), dict(kscale=1e-3), dict(kscale=1e3), dict(qscale=1e-12),
                                 dict(qscale=1e12), dict(spread=40.0)], ids=str)
 def test_magnitudes(epq_lib, cuda_dev, kw):
