@@ -41,8 +41,8 @@
 // The new rows are quantized into their tile by the CTAs that read it (the
 // one of row tile 0 also stores them in the cache).
 // Measured with 32 query and 8 key/value heads of 128 (both launches, from a
-// graph): 64 tokens over 8193 positions 110 us, four sequences of 8 tokens over
-// 32 k positions 181 us (280 MB of cache, 1.5 TB/s), 8 tokens over 1024
+// graph): 64 tokens over 8193 positions 107 us, four sequences of 8 tokens over
+// 32 k positions 173 us (280 MB of cache, 1.6 TB/s), 8 tokens over 1024
 // positions 17 us, one token over 37 positions 10 us.  The long ones are bound
 // by instructions between the products, 0.51 issued per cycle of a scheduler
 // with 4 warps each (the MMA pipe is 30 % busy): a warp spends ~900 on a tile
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         __syncthreads();
       }
       const uint8_t *kw = kt + wb * L::kKeys * kRow;
+      uint2 four[kOwn];
 #pragma unroll
       for (int j = 0; j < kOwn; ++j) s[0][j] = s[1][j] = 0.0f;
 #pragma unroll
@@ -629,9 +630,13 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
             mma_f16(acc[j], lo, kb[j][2 * ks], kb[j][2 * ks + 1]);
           }
         }
-        float d[kOwn];  // factors of the lane's positions kOwn t ...
+        float d[kOwn];  // factors of the lane's positions kOwn t ..., read four blocks at a time
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) d[j] = f16_at(kw + (kOwn * t + j) * kRow + 2 * b);
+        for (int j = 0; j < kOwn; ++j) {
+          if (b % 4 == 0) four[j] = *reinterpret_cast<const uint2 *>(kw + (kOwn * t + j) * kRow + 2 * b);
+          const float2 two = __half22float2(as_half2(b & 2 ? four[j].y : four[j].x));
+          d[j] = b & 1 ? two.y : two.x;
+        }
 #pragma unroll
         for (int j = 0; j < kNT; ++j) {
           s[0][j] = fmaf(d[j], acc[j][0], s[0][j]);
@@ -783,19 +788,12 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
       __syncthreads();
       // every warp is past the values of the tile before: its stage is free
-      uint32_t top = 0, bottom = 0x7c00u, flags = 0;
-      uint32_t wide = 0;  // bit c: warp c of the row group holds its weights in float32
-#pragma unroll
-      for (int c = 0; c < L::kWarps; ++c) {
-        const uint2 x = tell[c];
-        flags |= x.y & 1;
-        if (c / NB == wm) wide |= (x.y >> 1) << (c % NB);
-        if (c < NB) {
-          top = max(top, x.x >> 16);
-          bottom = min(bottom, x.x & 0xffffu);
-        }
-      }
-      fresh = flags;
+      const uint2 told = tell[lane % L::kWarps];
+      fresh = __any_sync(0xffffffffu, told.y & 1);
+      // bit c: warp c of the row group holds its weights in float32
+      const uint32_t wide = __ballot_sync(0xffffffffu, told.y & 2) >> (wm * NB) & ((1u << NB) - 1);
+      const uint32_t top = __reduce_max_sync(0xffffffffu, told.x >> 16);
+      const uint32_t bottom = __reduce_min_sync(0xffffffffu, told.x & 0xffffu);
       if (fresh) {
         __syncthreads();  // `tell` and the maxima are written again
         continue;
