@@ -108,24 +108,17 @@ __global__ void __launch_bounds__(kStatThreads) row_stats_kernel(const __grid_co
       x[k].w = v + 3 >= 0 && v + 3 < p.vocab ? row[v + 3] : -INFINITY;
     }
   }
-  float m = -INFINITY;
-  int at = 0x7fffffff;
+  float mine = -INFINITY;
 #pragma unroll
-  for (int k = 0; k < VEC; ++k) {  // rising indices: a later one replaces only a smaller value
-    const int v = v0 + 1024 * k;
-    if (x[k].x > m) m = x[k].x, at = v;
-    if (x[k].y > m) m = x[k].y, at = v + 1;
-    if (x[k].z > m) m = x[k].z, at = v + 2;
-    if (x[k].w > m) m = x[k].w, at = v + 3;
-  }
+  for (int k = 0; k < VEC; ++k) mine = fmaxf(mine, fmaxf(fmaxf(x[k].x, x[k].y), fmaxf(x[k].z, x[k].w)));
+  float m = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    take_max(m, at, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, at, o));
-  if (lane == 0) sm[warp] = m, si[warp] = at;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sm[warp] = m;
   __syncthreads();
-  m = sm[0], at = si[0];
+  m = sm[0];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) take_max(m, at, sm[w], si[w]);
+  for (int w = 1; w < 8; ++w) m = fmaxf(m, sm[w]);
   const float ref = m == -INFINITY ? 0.0f : m;
   float z = 0.0f;
 #pragma unroll
@@ -133,11 +126,27 @@ __global__ void __launch_bounds__(kStatThreads) row_stats_kernel(const __grid_co
     z += (exp2_fast((x[k].x - ref) * p.c_hi) + exp2_fast((x[k].y - ref) * p.c_hi)) +
          (exp2_fast((x[k].z - ref) * p.c_hi) + exp2_fast((x[k].w - ref) * p.c_hi));
   z = warp_sum_xor<32>(z);
-  if (lane == 0) ss[warp] = z;
+  // the lowest index of the maximum, where a thread of the warp has it
+  int at = 0x7fffffff;
+  if (__any_sync(0xffffffffu, mine == m)) {
+#pragma unroll
+    for (int k = VEC - 1; k >= 0; --k) {
+      const int v = v0 + 1024 * k;
+      if (x[k].w == m) at = v + 3;
+      if (x[k].z == m) at = v + 2;
+      if (x[k].y == m) at = v + 1;
+      if (x[k].x == m) at = v;
+    }
+    at = __reduce_min_sync(0xffffffffu, m == -INFINITY ? 0x7fffffff : at);
+  }
+  if (lane == 0) ss[warp] = z, si[warp] = at;
   __syncthreads();
   if (threadIdx.x == 0) {
     z = 0.0f;
-    for (int w = 0; w < 8; ++w) z += ss[w];
+    for (int w = 0; w < 8; ++w) {
+      z += ss[w];
+      at = min(at, si[w]);
+    }
     const int64_t i = static_cast<int64_t>(r) * p.splits + blockIdx.x;
     p.part_max[i] = m;
     p.part_sum[i] = z;
