@@ -11,10 +11,10 @@
 // rejection, and once to draw the next token (its weights then stay in shared
 // memory).
 //
-// Measured (128256 tokens, both launches from a graph): one row 12.7 us, of
+// Measured (128256 tokens, both launches from a graph): one row 12.5 us, of
 // which the walk's dependent steps are the larger part (with 8 CTAs per
 // sequence that read the row again to draw: 25 us); 8 rows with draft
-// probabilities 22.4 us; 4 sequences of 64 rows 54 us, 131 MB.
+// probabilities 22 us; 4 sequences of 64 rows 54 us, 131 MB.
 //
 // Drawing compares a partial sum of up to 2^18 weights with u times their
 // total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
@@ -81,8 +81,9 @@ __device__ __forceinline__ float join_sum(float m, float z, float top, float c) 
 
 // Grid (splits, rows).  A CTA reads 1024 VEC consecutive floats of a row,
 // 16 bytes at a time from 16-byte boundaries (a row may begin between two).
-// Bound by the loads' latency over short-lived CTAs: 131 MB in 28 us, 4.7 TB/s
-// (0.69 of the copy bandwidth).
+// Bound by what a CTA does after its loads have landed, over four CTAs an SM:
+// 131 MB in 26.5 us, 5.0 TB/s (0.73 of the copy bandwidth); chunks of 4096 the
+// same, of 16384 41 us.
 template <int VEC>
 __global__ void __launch_bounds__(kStatThreads) row_stats_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ float sm[8], ss[8];

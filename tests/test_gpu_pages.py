@@ -201,3 +201,17 @@ def test_one_sequence_over_a_shared_page(epq_lib, cuda_dev, P, D, rows):
     assert torch.equal(b.c.pool[:, own, :, :, :rows], kept[:, :, :, :rows])
     assert torch.equal(b.c.pool[:, shared], kept)
     assert epq_lib.epq_device_error() == 0
+
+
+def test_copy_past_32_bits(epq_lib, cuda_dev):
+    """The only free pages lie more than 2^32 bytes into the pool."""
+    c = epq_lib.PagedKVCache(2, 17000, 8, 128, 2, 4, 128, cuda_dev)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    c.refs[:16990] = 1
+    assert epq_lib.epq_pages_reserve(c, i32([9, 0])).tolist() == [0, 0] and c.table[0, 0].item() == 16990
+    c.pool[:, 16990, :, :, :9] = torch.randint(0, 256, c.pool[:, 0, :, :, :9].shape, dtype=torch.uint8, device=cuda_dev)
+    c.length[0] = 9
+    epq_lib.epq_pages_fork(c, i32([0]), i32([1]))
+    assert epq_lib.epq_pages_reserve(c, i32([0, 3])).tolist() == [0, 0] and c.table[1, 0].item() == 16991
+    assert torch.equal(c.pool[:, 16991, :, :, :9], c.pool[:, 16990, :, :, :9]) and not c.pool[:, 16992].any()
+    assert epq_lib.epq_device_error() == 0

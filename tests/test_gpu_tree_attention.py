@@ -265,3 +265,25 @@ def test_missing_pages(epq_lib, cuda_dev):
     got = c.run()
     assert torch.isfinite(got).all() and epq_lib.epq_device_error() == 5
     assert torch.equal(before, c.c.pool)
+
+
+def test_pages_past_32_bits(epq_lib, cuda_dev):
+    """Pages more than 2^32 bytes into a pool, of its second layer: the same outputs, stored and committed rows."""
+    c = Case(epq_lib, cuda_dev, [300], 8, 16, 8, 128, 128)
+    want = c.check()
+    ids = torch.tensor([16999, 15800, 16001], device=cuda_dev)
+    big = epq_lib.PagedKVCache(2, 17000, 8, 128, 1, c.c.max_pages, 128, cuda_dev)
+    small = c.c.table[0, :3].long()
+    big.table[0, :3] = ids.int()
+    big.pool[1, ids] = c.c.pool[0, small]
+    big.length.fill_(300)
+    big.refs[ids] = 1
+    big.pool[1, ids[2], :, :, 44:52] = 0  # the new rows
+    c.c, kept, c.layer = big, c.c, 1
+    assert torch.equal(c.run(), want) and torch.equal(big.pool[1, ids], kept.pool[0, small])
+    path = torch.tensor([[0, 2, 3, 6, 7, -1, -1, -1]], dtype=torch.int32, device=cuda_dev)
+    n = torch.tensor([5], dtype=torch.int32, device=cuda_dev)
+    for cache in (kept, big):
+        epq_lib.epq_pages_compact(cache, path, n)
+        assert cache.length.tolist() == [305]
+    assert torch.equal(big.pool[1, ids], kept.pool[0, small]) and epq_lib.epq_device_error() == 0
