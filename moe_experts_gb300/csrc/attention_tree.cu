@@ -44,8 +44,8 @@
 // graph): 64 tokens over 8193 positions 107 us, four sequences of 8 tokens over
 // 32 k positions 173 us (280 MB of cache, 1.6 TB/s), 8 tokens over 1024
 // positions 17 us, one token over 37 positions 10 us.  The long ones are bound
-// by instructions between the products, 0.51 issued per cycle of a scheduler
-// with 4 warps each (the MMA pipe is 30 % busy): a warp spends ~900 on a tile
+// by instructions between the products, 0.52 issued per cycle of a scheduler
+// with 4 warps each (the MMA pipe is 31 % busy): a warp spends ~870 on a tile
 // of 16 rows, 64 of them MMAs.  Short ones are one chain of tile, parts and
 // join.  32 rows per warp take a third fewer instructions but leave half the
 // warps: 113, 167, 20 us.
