@@ -19,11 +19,13 @@
 //            multiplies the weights by that block's factors.  A weight is kept
 //            as two fp16 parts, so a product is three half2 operations: its
 //            rounded value, what the rounding lost (exact), plus the second
-//            part's product: 2^-22 of it, or 2^-34 of one at the reference.
+//            part's product: 2^-22 of it, or 2^-34 of one at the reference with
+//            the largest factor that block b has in the tile (a power of two
+//            brings that factor into [1, 2)).
 //            That floor would show where every larger weight meets a code 0, so
 //            a tile with a weight below 2^-14 in a row that has not had 12
 //            larger ones takes float32 products in three bf16 parts, which lose
-//            nothing.
+//            nothing; so does a warp whose block has factors more than 2^11 apart.
 // The weights of a row are relative to its maximum at some earlier tile (the
 // reference), which moves, and the sums with it, only when a weight passes 2^6:
 // so the warps need not agree on a maximum before they form weights, and one
@@ -231,6 +233,10 @@ __device__ __forceinline__ float f16_at(const uint8_t *p) {
   return __half2float(__ushort_as_half(*reinterpret_cast<const unsigned short *>(p)));
 }
 
+__device__ __forceinline__ float half_value(uint32_t bits) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -377,7 +383,7 @@ struct Plan {
   static constexpr uint32_t oWork = oScale + 4u * kRows;            // Work
   static constexpr uint32_t oBar = oWork + sizeof(Work);            // full
   static constexpr uint32_t oTell = oBar + 8u * (kStages + 1);      // [2][warps] see `tell`
-  static constexpr uint32_t oMiss = oTell + 2u * 8u * kWarps;       // [stages] missing pieces
+  static constexpr uint32_t oMiss = oTell + 2u * 4u * kWarps;       // [stages] missing pieces
   static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
 
@@ -523,8 +529,8 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
     float o[4][4] = {}, s[2][kOwn];  // s: scores, then weights, of rows g, g + 8 at the lane's positions
     float ref[2] = {-INFINITY, -INFINITY}, l_run[2] = {}, weighty[2] = {};
     const float c_row[2] = {row_scale[16 * wm + g], row_scale[16 * wm + 8 + g]};
-    float unit = 1.0f;     // power of two on the value factors: the largest of a tile comes into [1, 2)
-    uint32_t factors = 0;  // of the warp's positions: the largest (upper half) and smallest (lower) value factor, fp16
+    float unit = 1.0f;  // power of two on the value factors of the warp's columns: a tile's largest comes into [1, 2)
+    uint32_t largest = 0, smallest = 0;  // of these factors (fp16) in the tile
 
     // Scores of tile `tile` (pipeline step kk) into s.
     auto scores = [&](int tile, uint32_t kk) {
@@ -645,19 +651,18 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           s[1][kNT + j] = fmaf(d[kNT + j], acc[j][3], s[1][kNT + j]);
         }
       }
-      // the largest value factor of each of the warp's positions: their range
-      // (positions without any do not count)
+      // the range of the value factors that the warp's columns have in the tile
+      // (a factor of 0 does not count)
       {
-        const uint8_t *r = vt + (wb * L::kKeys + (lane & (L::kKeys - 1))) * kRow;
-        __half2 a = __half2half2(__ushort_as_half(0));
-#pragma unroll
-        for (int b = 0; b < NB / 4; ++b) {
-          const uint2 f = *reinterpret_cast<const uint2 *>(r + 8 * b);
-          a = __hmax2(a, __hmax2(__habs2(as_half2(f.x)), __habs2(as_half2(f.y))));
+        const uint8_t *r = vt + lane * kRow + 2 * wb;
+        uint32_t x = *reinterpret_cast<const unsigned short *>(r) & 0x7fffu;
+        uint32_t y = *reinterpret_cast<const unsigned short *>(r + 32 * kRow) & 0x7fffu;
+        if (special) {  // not finite: not in the products
+          x = x < 0x7c00u ? x : 0u;
+          y = y < 0x7c00u ? y : 0u;
         }
-        uint32_t bits = __half_as_ushort(__hmax(__low2half(a), __high2half(a)));
-        if (special && bits >= 0x7c00u) bits = 0;  // not finite: not in the products
-        factors = __reduce_max_sync(0xffffffffu, bits) << 16 | __reduce_min_sync(0xffffffffu, bits ? bits : 0x7c00u);
+        largest = __reduce_max_sync(0xffffffffu, max(x, y));
+        smallest = __reduce_min_sync(0xffffffffu, min(x ? x : 0x7c00u, y ? y : 0x7c00u));
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b)
@@ -721,9 +726,8 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
       // ------------------------------------------------------------ weights
       float *w = reinterpret_cast<float *>(smem + L::oW) + ((k & 1) * kRows + 16 * wm) * kTile;
-      // of a warp: its positions' value factors; bit 0: a weight past the
-      // reference, bit 1: held in float32
-      uint2 *tell = reinterpret_cast<uint2 *>(smem + L::oTell) + (k & 1) * L::kWarps;
+      // of a warp: bit 0: a weight past the reference, bit 1: held in float32
+      unsigned *tell = reinterpret_cast<unsigned *>(smem + L::oTell) + (k & 1) * L::kWarps;
       float sum[2], now[2] = {weighty[0], weighty[1]};
       {
         float over = 0.0f;
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         }
         few = __any_sync(0xffffffffu, few);
         const bool past = __any_sync(0xffffffffu, over > kPast);
-        if (lane == 0) tell[warp] = make_uint2(factors, (past ? 1u : 0u) | (few ? 2u : 0u));
+        if (lane == 0) tell[warp] = (past ? 1u : 0u) | (few ? 2u : 0u);
         // the 16-byte chunks of odd rows are stored with bit 2 of their index
         // flipped; a chunk is 4 weights, or their first parts, then the second
         const int col = (wb * L::kKeys + kOwn * t) ^ ((g & 1) << 4);
@@ -788,12 +792,10 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
       __syncthreads();
       // every warp is past the values of the tile before: its stage is free
-      const uint2 told = tell[lane % L::kWarps];
-      fresh = __any_sync(0xffffffffu, told.y & 1);
+      const unsigned told = tell[lane % L::kWarps];
+      fresh = __any_sync(0xffffffffu, told & 1);
       // bit c: warp c of the row group holds its weights in float32
-      const uint32_t wide = __ballot_sync(0xffffffffu, told.y & 2) >> (wm * NB) & ((1u << NB) - 1);
-      const uint32_t top = __reduce_max_sync(0xffffffffu, told.x >> 16);
-      const uint32_t bottom = __reduce_min_sync(0xffffffffu, told.x & 0xffffu);
+      const uint32_t wide = __ballot_sync(0xffffffffu, told & 2) >> (wm * NB) & ((1u << NB) - 1);
       if (fresh) {
         __syncthreads();  // `tell` and the maxima are written again
         continue;
@@ -807,11 +809,12 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         load();
         look_ahead();
       }
-      const float new_unit = exp2i(min(max(15 - static_cast<int>(top >> 10), -15), 15));
+      const float new_unit = exp2i(min(max(15 - static_cast<int>(largest >> 10), -15), 15));
       const float moved = new_unit * (1.0f / unit);
       unit = new_unit;
-      // factors that differ by more than 2^11 in a tile: float32, too
-      const bool slow = wide || (top >> 10) > (bottom >> 10) + 11;
+      // factors of the warp's columns that differ by more than 2^11 in a tile:
+      // float32, too
+      const bool slow = wide || !(half_value(largest) <= 2048.0f * half_value(smallest));
       const bool special = tile * kTile + kTile > it.len;
       // ------------------------------------------------------------ values
       // The tile's products go to accumulators of their own: the tensor cores

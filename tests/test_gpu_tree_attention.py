@@ -287,3 +287,28 @@ def test_pages_past_32_bits(epq_lib, cuda_dev):
         epq_lib.epq_pages_compact(cache, path, n)
         assert cache.length.tolist() == [305]
     assert torch.equal(big.pool[1, ids], kept.pool[0, small]) and epq_lib.epq_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("largest", [6, 14])
+@pytest.mark.parametrize("apart", [10, 14, 18, 22])
+def test_uneven_blocks(epq_lib, cuda_dev, apart, largest, D):
+    """Blocks of one value row that are powers of two apart, the largest factor below and above 2: the same blocks in
+    every row, then others from row to row.  The outputs of the small blocks count by themselves."""
+    for moving in (False, True):
+        c = Case(epq_lib, cuda_dev, [300], 5, 4, 1, D, 32, seed=apart)
+        NB, a = D // 32, (c.heads + c.kv) * D
+        up = 2.0 ** largest
+
+        def scaled(x, p):
+            f = np.array([up if (b + (p if moving else 0)) % 3 == 0 else up * 2.0 ** (-apart / (1 + b % 2)) for b in range(NB)])
+            return (x.reshape(-1, NB, 32) * f[:, None]).reshape(x.shape).astype(np.float32)
+
+        for p in range(300):
+            r = _rows(scaled(c.rng.standard_normal((1, D)), p))
+            c.V[0][:, p] = r
+            c.pool[0, c.table[0, p // 32], :, 1, p % 32] = r
+        for i in range(c.ntok):
+            c.qkv[0, i, a:] = scaled(c.qkv[0, i, a:], 300 + i)
+        c.c.pool.copy_(torch.from_numpy(c.pool))
+        c.check()
