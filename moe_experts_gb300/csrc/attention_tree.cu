@@ -733,7 +733,9 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
         float over = 0.0f;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float from = ref[b] == -INFINITY ? 0.0f : ref[b] - kUp;
+          // a row that has seen nothing yet has no reference: whatever it sees now
+          // is past the lowest float, and the turn begins again with a reference
+          const float from = ref[b] == -INFINITY ? -3.402823466e38f : ref[b] - kUp;
           sum[b] = 0.0f;
 #pragma unroll
           for (int j = 0; j < kOwn; ++j) {

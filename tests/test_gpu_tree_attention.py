@@ -312,3 +312,47 @@ def test_uneven_blocks(epq_lib, cuda_dev, apart, largest, D):
             c.qkv[0, i, a:] = scaled(c.qkv[0, i, a:], 300 + i)
         c.c.pool.copy_(torch.from_numpy(c.pool))
         c.check()
+
+
+def _check_without(epq, c, gone):
+    """The outputs are those of a cache without the positions of sequence s in its pages gone[s]."""
+    for s, pages in enumerate(gone):
+        c.c.table[s, pages] = -1
+    got = c.run().cpu().numpy().reshape(len(c.lengths), c.ntok, c.heads, c.D).astype(np.float64)
+    assert epq.epq_device_error() == (5 if any(gone) else 0)
+    x = c.qkv.reshape(len(c.lengths), c.ntok, c.heads + 2 * c.kv, c.D)
+    for s, n in enumerate(c.lengths):
+        keep = [p for p in range(n) if p // c.P not in gone[s]]
+        for g in range(c.heads):
+            h = g // (c.heads // c.kv)
+            K, V = (np.concatenate([_values((c.K, c.V)[k][s][h][keep]), _values(_rows(x[s, :, c.heads + k * c.kv + h]))])
+                    for k in (0, 1))
+            ref, wabs, smag = T.tree_attention_f64(x[s, :, g], K, V, len(keep), c.masks[s], c.scale)
+            e, b = np.abs(got[s, :, g] - ref), T.attention_bound(wabs, smag, len(keep) + c.ntok, c.D)
+            assert (e <= b).all(), f"seq {s} head {g}: {(e / b).max():.3g}"
+
+
+@pytest.mark.parametrize("low", [0.0, 10.0, 300.0])
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_missing_pages_leave_the_others(epq_lib, cuda_dev, P, low):
+    """Missing pages in sequences of many tiles, several to a CTA, the first ones among them; scores near 0 and far below
+    it.  A sequence whose every page is missing attends to its drafted tokens alone."""
+    lengths, heads, kv, D = [2500, 2437, 700, 2000], 16, 16, 128
+    c = Case(epq_lib, cuda_dev, lengths, 2, heads, kv, D, P, max_extra=0)
+    if low:  # every score is about -low: keys near one direction, queries against it
+        axis = c.rng.choice([-1.0, 1.0], D)
+        c.qkv[..., :heads * D] = np.tile(-low * axis, heads) * (1 + 0.02 * c.rng.standard_normal(c.qkv[..., :heads * D].shape))
+        c.scale = 1.0 / D
+        c.qkv[..., heads * D:(heads + kv) * D] = np.tile(axis, kv) * (1 + 0.02 * c.rng.standard_normal(
+            c.qkv[..., heads * D:(heads + kv) * D].shape))
+        for s, n in enumerate(lengths):
+            r = _rows((axis * (1 + 0.02 * c.rng.standard_normal((kv, n, D)))).astype(np.float32))
+            c.K[s] = r
+            for p in range(n):
+                c.pool[0, c.table[s, p // P], :, 0, p % P] = r[:, p]
+        c.c.pool.copy_(torch.from_numpy(c.pool))
+    last = [n // P for n in lengths]
+    gone = [[j for j in range(last[0]) if j * P // 128 % 3 == 0],         # every third stretch of 128 positions
+            list(range(last[1] - 3)),                                     # all but the last ones
+            list(range(last[2])) + ([last[2]] if 700 % P else []), []]  # all
+    _check_without(epq_lib, c, gone)
