@@ -398,25 +398,35 @@ def epq_attention_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
 # ------------------------------------------------------------------ paged cache
 # The calls of a speculative step are short next to what Python costs, so the
 # functions below compare shapes as tuples and pass addresses as integers.
-def _wrong(t, name, dtype, shape):
+def _wrong(t, name, dtype, shape, dev):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _need(t, name, dtype, shape):
-    """t is a contiguous tensor of this type and shape."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _wrong(t, name, dtype, shape)
+def _need(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on this device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _wrong(t, name, dtype, shape, dev)
     return t.data_ptr()
+
+
+def _scratch(t, dev):
+    """A workspace that the caller holds: its address and bytes."""
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return t.data_ptr(), t.numel()
 
 
 class PagedKVCache:
     """Q8_0 key/value cache in pages shared by sequences (epq_pages): pool
     uint8 [n_layers, n_pages, n_kv_heads, 2, page_size, epq_kv_row_bytes(head_dim)],
     table int32 [n_seq, max_pages], length int32 [n_seq], refs int32 [n_pages],
-    all on the device.  The positions of a sequence are appended by
-    epq_attention_tree and committed by epq_pages_compact."""
+    all on one device, as are the tensors of every call on the cache.  The
+    positions of a sequence are appended by epq_attention_tree and committed
+    by epq_pages_compact."""
 
     def __init__(self, n_layers: int, n_pages: int, n_kv_heads: int, head_dim: int, n_seq: int, max_pages: int,
                  page_size: int = 64, device="cuda"):
@@ -437,22 +447,23 @@ class PagedKVCache:
     def _bind(self, pool, table, length, refs):
         if pool.dim() != 6 or pool.shape[3] != 2 or table.dim() != 2:
             raise ValueError("pool must be [layers, pages, heads, 2, page_size, row] and table [n_seq, max_pages]")
-        _need(pool, "pool", torch.uint8, pool.shape)
-        _need(table, "table", torch.int32, table.shape)
-        _need(length, "length", torch.int32, (table.shape[0],))
-        _need(refs, "refs", torch.int32, (pool.shape[1],))
+        dev = pool.device
+        _need(pool, "pool", torch.uint8, pool.shape, dev)
+        _need(table, "table", torch.int32, table.shape, dev)
+        _need(length, "length", torch.int32, (table.shape[0],), dev)
+        _need(refs, "refs", torch.int32, (pool.shape[1],), dev)
         self.n_layers, self.n_pages, self.n_kv_heads, _, self.page_size, rb = pool.shape
         self.head_dim = rb * 16 // 17
         if epq_kv_row_bytes(self.head_dim) != rb:
             raise ValueError(f"rows of {rb} bytes are no cache rows")
         self.n_seq, self.max_pages = table.shape
-        self.pool, self.table, self.length, self.refs = pool, table, length, refs
+        self.pool, self.table, self.length, self.refs, self.device = pool, table, length, refs, dev
         self._p = Pages(_addr(pool), _addr(table), _addr(length), _addr(refs), None, self.n_layers, self.n_pages,
                         self.n_kv_heads, self.head_dim, self.page_size, self.n_seq, self.max_pages)
         n = int(load().epq_pages_work_bytes(ctypes.byref(self._p)))
         if n == 0:
             raise ValueError("sizes of the paged cache not supported")
-        self.work = torch.zeros(n, dtype=torch.uint8, device=pool.device)
+        self.work = torch.zeros(n, dtype=torch.uint8, device=dev)
         self._p.work = self.work.data_ptr()
         self._ref = ctypes.byref(self._p)
         self._per_seq = (self.n_seq,)
@@ -460,7 +471,7 @@ class PagedKVCache:
 
 def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=None) -> None:
     """new_length int32 [n_seq] (negative: leave): shorten sequences and give their pages back (0 frees one)."""
-    n = _need(new_length, "new_length", torch.int32, cache._per_seq)
+    n = _need(new_length, "new_length", torch.int32, cache._per_seq, cache.device)
     st = _lib.epq_pages_truncate(cache._ref, n, _stream(stream))
     if st:
         raise EpqError("epq_pages_truncate", st)
@@ -469,9 +480,9 @@ def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=Non
 def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, status: torch.Tensor | None = None,
                    stream=None) -> None:
     """Sequences dst (int32 [n], empty) become copies of src, sharing their pages; no entries: nothing happens."""
-    n = dst.shape[0]
-    a, b = _need(src, "src", torch.int32, (n,)), _need(dst, "dst", torch.int32, (n,))
-    c = None if status is None else _need(status, "status", torch.int32, (n,))
+    n, dev = dst.shape[0], cache.device
+    a, b = _need(src, "src", torch.int32, (n,), dev), _need(dst, "dst", torch.int32, (n,), dev)
+    c = None if status is None else _need(status, "status", torch.int32, (n,), dev)
     if n:
         st = _lib.epq_pages_fork(cache._ref, a, b, n, c, _stream(stream))
         if st:
@@ -481,10 +492,11 @@ def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, st
 def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """Make extra (int32 [n_seq]) more positions of every sequence writable -> status int32 [n_seq]."""
-    e = _need(extra, "extra", torch.int32, cache._per_seq)
+    e = _need(extra, "extra", torch.int32, cache._per_seq, cache.device)
     if status is None:
         status = torch.empty_like(extra)
-    st = _lib.epq_pages_reserve(cache._ref, e, _need(status, "status", torch.int32, cache._per_seq), _stream(stream))
+    st = _lib.epq_pages_reserve(cache._ref, e, _need(status, "status", torch.int32, cache._per_seq, cache.device),
+                                _stream(stream))
     if st:
         raise EpqError("epq_pages_reserve", st)
     return status
@@ -493,8 +505,8 @@ def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Te
 def epq_pages_compact(cache: PagedKVCache, path: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
     """Commit the drafted rows path (int32 [n_seq, ntok], n_keep int32 [n_seq] of them) in every layer."""
     ntok = path.shape[-1]
-    a = _need(path, "path", torch.int32, (cache.n_seq, ntok))
-    st = _lib.epq_pages_compact(cache._ref, a, _need(n_keep, "n_keep", torch.int32, cache._per_seq), ntok,
+    a = _need(path, "path", torch.int32, (cache.n_seq, ntok), cache.device)
+    st = _lib.epq_pages_compact(cache._ref, a, _need(n_keep, "n_keep", torch.int32, cache._per_seq, cache.device), ntok,
                                 _stream(stream))
     if st:
         raise EpqError("epq_pages_compact", st)
@@ -505,10 +517,10 @@ def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream
     """parent int32 [n_seq, ntok] -> mask int64 [n_seq, ntok] (bit j: token j is i or an ancestor of i)."""
     if parent.dim() != 2:
         raise ValueError("parent must be [n_seq, ntok]")
-    a = _need(parent, "parent", torch.int32, parent.shape)
+    a = _need(parent, "parent", torch.int32, parent.shape, parent.device)
     if mask is None:
         mask = torch.empty(parent.shape, dtype=torch.int64, device=parent.device)
-    b = _need(mask, "mask", torch.int64, parent.shape)
+    b = _need(mask, "mask", torch.int64, parent.shape, parent.device)
     _check("epq_tree_mask", load().epq_tree_mask(a, parent.shape[0], parent.shape[1], b, _stream(stream)))
     return mask
 
@@ -518,13 +530,13 @@ def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int) -
     n = int(load().epq_attention_tree_workspace_bytes(cache._ref, n_heads, ntok))
     if n == 0:
         raise ValueError("sizes of the tree attention not supported")
-    return torch.empty(n, dtype=torch.uint8, device=cache.pool.device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
-def _token_strides(t, name, shape):
+def _token_strides(t, name, shape, dev):
     """Floats between sequences and tokens of t [n_seq, ntok, n] (0: a dimension of one entry says nothing)."""
-    if t.dtype is not torch.float32 or t.shape != shape:
-        raise ValueError(f"{name}: expected float32 {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.dtype is not torch.float32 or t.shape != shape or t.device != dev:
+        raise ValueError(f"{name}: expected float32 {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
     a, b, c = t.stride()
     if c != 1 or (a == 0 and shape[0] > 1) or (b == 0 and shape[1] > 1):
         raise ValueError(f"{name}: rows must be contiguous and not broadcast")
@@ -537,23 +549,23 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [n_seq, ntok, n_heads*D], k_new/v_new [n_seq, ntok, n_kv*D] (float32; views of one wider buffer are
     read in place) -> out [n_seq, ntok, n_heads*D]; the new rows are stored behind the committed positions."""
-    ntok, nseq, D = q.shape[1], cache.n_seq, cache.head_dim
+    ntok, nseq, D, dev = q.shape[1], cache.n_seq, cache.head_dim, cache.device
     shape = (nseq, ntok, n_heads * D)
-    q_seq, q_tok = _token_strides(q, "q", shape)
+    q_seq, q_tok = _token_strides(q, "q", shape, dev)
     kv = (nseq, ntok, cache.n_kv_heads * D)
-    kv_seq, kv_tok = _token_strides(k_new, "k_new", kv)
-    if _token_strides(v_new, "v_new", kv) != (kv_seq, kv_tok):
+    kv_seq, kv_tok = _token_strides(k_new, "k_new", kv, dev)
+    if _token_strides(v_new, "v_new", kv, dev) != (kv_seq, kv_tok):
         raise ValueError("k_new and v_new must have the same strides")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _own_scratch(epq_attention_tree_workspace(cache, n_heads, ntok), stream)
-    o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok)),
-                          None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq),
+    o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), dev),
+                          None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, dev),
                           q_tok, q_seq, kv_tok, kv_seq)
     st = _lib.epq_attention_tree(cache._ref, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), n_heads, ntok,
-                                 scale, ctypes.byref(o), _need(out, "out", torch.float32, shape),
-                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
+                                 scale, ctypes.byref(o), _need(out, "out", torch.float32, shape, dev),
+                                 *_scratch(workspace, dev), _stream(stream))
     if st:
         raise EpqError("epq_attention_tree", st)
     return out
@@ -588,13 +600,14 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     lse = torch.empty(tree, dtype=f32, device=dev) if lse is None else lse
     if workspace is None:
         workspace = _own_scratch(epq_verify_tree_workspace(logits), stream)
-    o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full),
-                   None if n_tok is None else _need(n_tok, "n_tok", i32, each), temperature, 0, 0)
+    o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full, dev),
+                   None if n_tok is None else _need(n_tok, "n_tok", i32, each, dev), temperature, 0, 0)
     st = lib.epq_verify_tree(
-        _need(logits, "logits", f32, full), vocab, _need(tokens, "tokens", i32, tree), _need(parent, "parent", i32, tree),
-        None if u is None else _need(u, "u", f32, tree), nseq, ntok, ctypes.byref(o), _need(path, "path", i32, tree),
-        _need(n_accept, "n_accept", i32, each), _need(next_token, "next_token", i32, each), _need(lse, "lse", f32, tree),
-        workspace.data_ptr(), workspace.numel(), _stream(stream))
+        _need(logits, "logits", f32, full, dev), vocab, _need(tokens, "tokens", i32, tree, dev),
+        _need(parent, "parent", i32, tree, dev), None if u is None else _need(u, "u", f32, tree, dev), nseq, ntok,
+        ctypes.byref(o), _need(path, "path", i32, tree, dev), _need(n_accept, "n_accept", i32, each, dev),
+        _need(next_token, "next_token", i32, each, dev), _need(lse, "lse", f32, tree, dev), *_scratch(workspace, dev),
+        _stream(stream))
     if st:
         raise EpqError("epq_verify_tree", st)
     return path, n_accept, next_token, lse

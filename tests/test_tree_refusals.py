@@ -142,3 +142,40 @@ def test_tree_mask_refusals(epq_lib):
     assert lib.epq_tree_mask(t.data_ptr(), 1, 65, t.data_ptr(), None) == EPQ_ERR_SHAPE
     with pytest.raises(ValueError):
         epq_lib.epq_tree_mask(torch.zeros(1, 4, dtype=torch.int64), stream=0)
+
+
+@pytest.mark.parametrize("call", [
+    lambda epq, c, t: epq.epq_pages_truncate(c, t(3), stream=0),
+    lambda epq, c, t: epq.epq_pages_fork(c, t(2), torch.zeros(2, dtype=torch.int32), stream=0),
+    lambda epq, c, t: epq.epq_pages_fork(c, torch.zeros(2, dtype=torch.int32), t(2), stream=0),
+    lambda epq, c, t: epq.epq_pages_fork(c, *[torch.zeros(2, dtype=torch.int32)] * 2, status=t(2), stream=0),
+    lambda epq, c, t: epq.epq_pages_reserve(c, t(3), stream=0),
+    lambda epq, c, t: epq.epq_pages_reserve(c, torch.zeros(3, dtype=torch.int32), t(3), stream=0),
+    lambda epq, c, t: epq.epq_pages_compact(c, t(3, 4), torch.zeros(3, dtype=torch.int32), stream=0),
+    lambda epq, c, t: epq.epq_pages_compact(c, torch.zeros((3, 4), dtype=torch.int32), t(3), stream=0),
+    lambda epq, c, t: epq.epq_tree_mask(torch.zeros((3, 4), dtype=torch.int32), t(3, 4, dtype=torch.int64), stream=0),
+    lambda epq, c, t: epq.PagedKVCache.over(c.pool, t(3, 4), c.length, c.refs),
+    lambda epq, c, t: epq.PagedKVCache.over(c.pool, c.table, t(3), c.refs),
+    lambda epq, c, t: epq.PagedKVCache.over(c.pool, c.table, c.length, t(6)),
+    *[lambda epq, c, t, a=a: _attn(epq, c, layer=-1, **{a[0]: t(*a[1], dtype=a[2])}) for a in (
+        ("q", (3, 4, 512), torch.float32), ("k", (3, 4, 256), torch.float32), ("v", (3, 4, 256), torch.float32),
+        ("mask", (3, 4), torch.int64), ("n_tok", (3,), torch.int32), ("out", (3, 4, 512), torch.float32),
+        ("workspace", (1 << 22,), torch.uint8))],
+    *[lambda epq, c, t, a=a: _verify(epq, temperature=-1.0, **{a[0]: t(*a[1], dtype=a[2])}) for a in (
+        ("logits", (2, 3, 40), torch.float32), ("draft", (2, 3, 40), torch.float32), ("tokens", (2, 3), torch.int32),
+        ("parent", (2, 3), torch.int32), ("u", (2, 3), torch.float32), ("n_tok", (2,), torch.int32),
+        ("path", (2, 3), torch.int32), ("n_accept", (2,), torch.int32), ("next_token", (2,), torch.int32),
+        ("lse", (2, 3), torch.float32), ("workspace", (1 << 16,), torch.uint8))],
+])
+def test_tensors_of_another_device(epq_lib, call):
+    """One tensor elsewhere than the others (on `meta`, next to a cache on the host) is refused before any launch."""
+    with pytest.raises(ValueError):
+        call(epq_lib, _cache(epq_lib), lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="meta"))
+
+
+def test_workspace_of_one_byte_repeated(epq_lib):
+    """A broadcast workspace has its size but not its memory."""
+    with pytest.raises(ValueError):
+        _attn(epq_lib, _cache(epq_lib), layer=-1, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+    with pytest.raises(ValueError):
+        _verify(epq_lib, temperature=-1.0, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
