@@ -157,10 +157,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _own_scratch(t: torch.Tensor, stream) -> torch.Tensor:
-    """Scratch that a call allocates for itself, kept from reuse until `stream` (not the current one) is done with it."""
-    if stream is not None and t.is_cuda:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """Memory that a call on `stream` (None: the current one) allocates for its results or scratch.  It comes from that
+    stream's memory, which nothing before the call can still be using, and is not given out again before the current
+    stream is done with it either."""
+    if stream is None or dev.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -494,7 +499,7 @@ def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Te
     """Make extra (int32 [n_seq]) more positions of every sequence writable -> status int32 [n_seq]."""
     e = _need(extra, "extra", torch.int32, cache._per_seq, cache.device)
     if status is None:
-        status = torch.empty_like(extra)
+        status = _empty(cache._per_seq, torch.int32, cache.device, stream)
     st = _lib.epq_pages_reserve(cache._ref, e, _need(status, "status", torch.int32, cache._per_seq, cache.device),
                                 _stream(stream))
     if st:
@@ -519,18 +524,18 @@ def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream
         raise ValueError("parent must be [n_seq, ntok]")
     a = _need(parent, "parent", torch.int32, parent.shape, parent.device)
     if mask is None:
-        mask = torch.empty(parent.shape, dtype=torch.int64, device=parent.device)
+        mask = _empty(parent.shape, torch.int64, parent.device, stream)
     b = _need(mask, "mask", torch.int64, parent.shape, parent.device)
     _check("epq_tree_mask", load().epq_tree_mask(a, parent.shape[0], parent.shape[1], b, _stream(stream)))
     return mask
 
 
-def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int) -> torch.Tensor:
-    """A workspace for epq_attention_tree, to be kept between calls."""
+def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int, stream=None) -> torch.Tensor:
+    """A workspace for epq_attention_tree (on `stream`), to be kept between calls."""
     n = int(load().epq_attention_tree_workspace_bytes(cache._ref, n_heads, ntok))
     if n == 0:
         raise ValueError("sizes of the tree attention not supported")
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return _empty(n, torch.uint8, cache.device, stream)
 
 
 def _token_strides(t, name, shape, dev):
@@ -557,9 +562,9 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     if _token_strides(v_new, "v_new", kv, dev) != (kv_seq, kv_tok):
         raise ValueError("k_new and v_new must have the same strides")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _empty(shape, torch.float32, dev, stream)
     if workspace is None:
-        workspace = _own_scratch(epq_attention_tree_workspace(cache, n_heads, ntok), stream)
+        workspace = epq_attention_tree_workspace(cache, n_heads, ntok, stream)
     o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), dev),
                           None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, dev),
                           q_tok, q_seq, kv_tok, kv_seq)
@@ -571,12 +576,12 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
     return out
 
 
-def epq_verify_tree_workspace(logits: torch.Tensor) -> torch.Tensor:
-    """A workspace for epq_verify_tree on logits of this shape."""
+def epq_verify_tree_workspace(logits: torch.Tensor, stream=None) -> torch.Tensor:
+    """A workspace for epq_verify_tree (on `stream`) on logits of this shape."""
     n = int(load().epq_verify_tree_workspace_bytes(logits.shape[0], logits.shape[1], logits.shape[2]))
     if n == 0:
         raise ValueError("sizes of the verification not supported")
-    return torch.empty(n, dtype=torch.uint8, device=logits.device)
+    return _empty(n, torch.uint8, logits.device, stream)
 
 
 def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, u: torch.Tensor | None = None,
@@ -594,12 +599,12 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     full = logits.shape
     nseq, ntok, vocab = full
     tree, each = (nseq, ntok), (nseq,)
-    path = torch.empty(tree, dtype=i32, device=dev) if path is None else path
-    n_accept = torch.empty(each, dtype=i32, device=dev) if n_accept is None else n_accept
-    next_token = torch.empty(each, dtype=i32, device=dev) if next_token is None else next_token
-    lse = torch.empty(tree, dtype=f32, device=dev) if lse is None else lse
+    path = _empty(tree, i32, dev, stream) if path is None else path
+    n_accept = _empty(each, i32, dev, stream) if n_accept is None else n_accept
+    next_token = _empty(each, i32, dev, stream) if next_token is None else next_token
+    lse = _empty(tree, f32, dev, stream) if lse is None else lse
     if workspace is None:
-        workspace = _own_scratch(epq_verify_tree_workspace(logits), stream)
+        workspace = epq_verify_tree_workspace(logits, stream)
     o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full, dev),
                    None if n_tok is None else _need(n_tok, "n_tok", i32, each, dev), temperature, 0, 0)
     st = lib.epq_verify_tree(

@@ -215,3 +215,54 @@ def test_copy_past_32_bits(epq_lib, cuda_dev):
     assert epq_lib.epq_pages_reserve(c, i32([0, 3])).tolist() == [0, 0] and c.table[1, 0].item() == 16991
     assert torch.equal(c.pool[:, 16991, :, :, :9], c.pool[:, 16990, :, :, :9]) and not c.pool[:, 16992].any()
     assert epq_lib.epq_device_error() == 0
+
+
+def test_results_of_a_call_on_another_stream(epq_lib, cuda_dev):
+    """What a call on another stream allocates for its results is memory that no earlier work of the current stream can
+    still be using, and is given out again, once the caller drops it, only after both streams are done with it."""
+    cache = epq_lib.PagedKVCache(1, 4, 1, 128, 3, 2, 16, cuda_dev)
+    extra = torch.ones(3, dtype=torch.int32, device=cuda_dev)
+    parent = torch.full((3, 2), -1, dtype=torch.int32, device=cuda_dev)
+    q, kv = (torch.zeros((3, 2, 128), device=cuda_dev) for _ in range(2))
+    logits, u = torch.zeros((3, 2, 100), device=cuda_dev), torch.zeros((3, 2), device=cuda_dev)
+    calls = [lambda s: [epq_lib.epq_pages_reserve(cache, extra, stream=s)],
+             lambda s: [epq_lib.epq_tree_mask(parent, stream=s)],
+             lambda s: [epq_lib.epq_attention_tree(q, kv, kv, cache, 0, 1, 1.0, stream=s)],
+             lambda s: list(epq_lib.epq_verify_tree(logits, parent, parent, u, stream=s))]
+
+    def wait():
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+
+    def again(like, stream):
+        """Where the next tensors of these shapes and of this stream's memory lie."""
+        with torch.cuda.stream(stream):
+            fresh = [torch.empty(r[0], dtype=r[1], device=cuda_dev) for r in like for _ in range(4)]
+            return {f.data_ptr() for f in fresh}
+
+    here = torch.cuda.current_stream()
+    for call in calls:
+        results = call(None)
+        like = [(r.shape, r.dtype) for r in results]
+        results.clear()  # memory that the call below could be given
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for s in (side, side.cuda_stream):
+            before = again(like, here)
+            with torch.cuda.stream(side):
+                wait()
+            results = call(s)
+            at = {r.data_ptr() for r in results}
+            assert not at & before
+            results.clear()  # while `side` has yet to write them
+            assert not again(like, here) & at
+            torch.cuda.synchronize()
+            results = call(s)
+            at = {r.data_ptr() for r in results}
+            here.wait_stream(side)
+            wait()  # the current stream reads them
+            results.clear()
+            with torch.cuda.stream(side):
+                wait()
+            assert not again(like, side) & at
+            torch.cuda.synchronize()
+    assert epq_lib.epq_device_error() == 0
