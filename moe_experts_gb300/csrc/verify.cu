@@ -18,9 +18,9 @@
 //
 // Drawing compares a partial sum of up to 2^18 weights with u times their
 // total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
-// about 2^-31 of themselves and summed as 64-bit integers in units of 2^-44:
-// the sums do not depend on their order, and a wrong neighbour needs u within
-// about 1e-10 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
+// 2^-29 of themselves (root mean square 2^-31.5) and summed as 64-bit integers
+// in units of 2^-44 (0 below half a unit): the sums do not depend on their
+// order, and a wrong neighbour needs u within 2e-9 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
 // (n, j integers, |g| <= 1/64, everything that float32 loses of l - max and
 // of the product kept in a second float)
 //   w = 2^n 2^(j/32) (1 + (z + z^2/2 + z^3/6 + ...)),  z = g ln 2,
@@ -164,7 +164,7 @@ struct Table {
 __device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, float c_lo, const Table &tab) {
   const float d = l - m;
   float t = d * c_hi;
-  if (t < -64.0f) return 0;
+  if (t < -46.0f) return 0;  // below half a unit, as are those whose shift is past 63
   const float b = d - l;
   const float e = (l - (d - b)) + (-m - b);  // l - m = d + e
   const float te = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);
@@ -174,8 +174,8 @@ __device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, 
   const float x = fmaf(z * z, fmaf(z, fmaf(z, 0.041666667f, 0.16666667f), 0.5f), z);
   const int ki = static_cast<int>(k), j = ki & 31;
   const long long f = static_cast<long long>(tab.t[j]) + (static_cast<long long>(__float2int_rn(x * tab.f[j])) << 26);
-  const int s = min(18 - (ki >> 5), 63);
-  return static_cast<long long>((static_cast<unsigned long long>(f) + (1ull << (s - 1))) >> s);
+  const int s = 18 - (ki >> 5);
+  return s > 63 ? 0 : static_cast<long long>((static_cast<unsigned long long>(f) + (1ull << (s - 1))) >> s);
 }
 
 // max(w - S q, 0) in the same units, S = s_hi + s_lo.

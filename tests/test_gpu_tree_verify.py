@@ -146,3 +146,36 @@ def test_tree_mask(epq_lib, cuda_dev):
         parent[2, rng.integers(0, n)] = 77
         got = epq_lib.epq_tree_mask(torch.from_numpy(parent).to(cuda_dev)).cpu().numpy().view(np.uint64)
         assert [[int(m) for m in r] for r in got] == [T.ancestors(p) for p in parent.tolist()]
+
+
+def _one(epq, dev, logits, tokens, parent, u, q=None, temperature=1.0):
+    """(path, next token) of one sequence."""
+    t = lambda a, d: torch.from_numpy(np.ascontiguousarray(np.asarray(a, d)[None])).to(dev)  # noqa: E731
+    nxt = torch.full((1,), -7, dtype=torch.int32, device=dev)
+    path, n, _, _ = epq.epq_verify_tree(t(logits, np.float32), t(tokens, np.int32), t(parent, np.int32), t(u, np.float32),
+                                        draft=None if q is None else t(q, np.float32), temperature=temperature, next_token=nxt)
+    return path[0, :n.item()].tolist(), nxt.item()
+
+
+@pytest.mark.parametrize("vocab", [500, 128256])
+@pytest.mark.parametrize("temperature", [1.0, 0.05])
+def test_weights_below_half_a_unit(epq_lib, cuda_dev, vocab, temperature):
+    """Logits more than 45 ln 2 = 31.2 (times the temperature) below the largest weigh nothing: where only they are
+    left, nothing is left, and the state before stands."""
+    rng = np.random.default_rng(vocab)
+    logits = np.zeros((2, vocab))
+    far = rng.random(vocab) < 0.9
+    far[:4] = False
+    logits[:, ~far] = -20.0 - 5.0 * rng.random((~far).sum())
+    logits[:, far] = -31.3 - 13.0 * rng.random(far.sum())  # to 44.3: to 64 ln 2
+    logits[:, :4] = 0.0
+    logits = (logits * temperature).astype(np.float32)
+    q = np.zeros((2, vocab), np.float32)
+    q[:, :4] = 0.2501
+    q[:, ~far] = np.maximum(q[:, ~far], np.float32(1e-5))  # more than the target has
+    without = np.where(far, -np.inf, logits)
+    for u0 in (0.0, 0.3, 0.6, 0.9):
+        u = np.array([u0, 0.99999], np.float32)
+        want = T.verify_tree(without, [0, 2], [-1, 0], u, q, temperature)
+        assert want[0] == [0] and want[1] < 4
+        assert _one(epq_lib, cuda_dev, logits, [0, 2], [-1, 0], u, q, temperature) == (want[0], want[1])
