@@ -157,13 +157,22 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _stream_object(stream):
+    """The torch stream of a `stream` argument that is not None (a handle of 0 is the default stream, for which
+    ExternalStream would make a new one)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
 def _empty(shape, dtype, dev, stream) -> torch.Tensor:
     """Memory that a call on `stream` (None: the current one) allocates for its results or scratch.  It comes from that
     stream's memory, which nothing before the call can still be using, and is not given out again before the current
     stream is done with it either."""
     if stream is None or dev.type != "cuda":
         return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))):
+    with torch.cuda.stream(_stream_object(stream)):
         t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream())
     return t

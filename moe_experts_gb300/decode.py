@@ -267,8 +267,7 @@ class TreeDecoder:
         c, f, H, nq, nkv = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows
         h, qkv, attn = self.h, self.qkv, self.attn
         L.epq_pages_reserve(self.cache, self.extra, self.status, stream=stream)
-        on = stream if stream is None or isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        with torch.cuda.stream(on):
+        with torch.cuda.stream(None if stream is None else L._stream_object(stream)):
             torch.mul(self.extra, self.status == 0, out=self.n_tok)
         L.epq_tree_mask(parent, self.mask, stream=stream)
         q, k, v = qkv[..., :nq], qkv[..., nq:nq + nkv], qkv[..., nq + nkv:]

@@ -129,3 +129,20 @@ def test_cache_without_room(epq_lib, cuda_dev, setup):
         assert t.status.item() == 1 and n.item() == 0 and nxt.item() == -1 and path.tolist() == [[-1] * NTOK]
         assert t.cache.length.item() == 95 and torch.equal(t.cache.pool, pool)
     assert epq_lib.epq_device_error() == 0
+
+
+def test_step_on_the_default_stream_by_its_handle(epq_lib, cuda_dev, setup):
+    """stream=0: every part of the step is queued on the default stream, after what is queued there."""
+    t = _tree(epq_lib, cuda_dev, setup)
+    parent = torch.arange(-1, NTOK - 1, dtype=torch.int32, device=cuda_dev).view(1, -1)
+    tokens, u = torch.zeros((1, NTOK), dtype=torch.int32, device=cuda_dev), torch.zeros((1, NTOK), device=cuda_dev)
+    want = [x.clone() for x in t.step(setup[3], tokens, parent, u, temperature=0.0)]
+    length = t.cache.length.clone()
+    t = _tree(epq_lib, cuda_dev, setup)
+    t.status.fill_(1)  # what a part ahead of the reservation would take for its answer
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    got = t.step(setup[3], tokens, parent, u, temperature=0.0, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(t.cache.length, length)
+    assert t.n_tok.item() == NTOK and epq_lib.epq_device_error() == 0

@@ -179,3 +179,16 @@ def test_workspace_of_one_byte_repeated(epq_lib):
         _attn(epq_lib, _cache(epq_lib), layer=-1, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
     with pytest.raises(ValueError):
         _verify(epq_lib, temperature=-1.0, workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+
+
+def test_stream_arguments(epq_lib, monkeypatch):
+    """Torch streams, objects with a handle, and handles; 0 is the default stream and no other."""
+    from moe_experts_gb300 import _lib
+
+    class Handle:
+        cuda_stream = 4096
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: ("external", h))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    assert _lib._stream_object(0) == "default"
+    assert _lib._stream_object(4096) == _lib._stream_object(Handle()) == ("external", 4096)
