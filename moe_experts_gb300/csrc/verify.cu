@@ -8,8 +8,9 @@
 // same decisions from the same numbers.  An acceptance needs only w(x) of the
 // drafted token, which the CTA gathers for all tokens at the start; the row
 // itself is read again only where a draft row has to be subtracted after a
-// rejection, and once to draw the next token (its weights then stay in shared
-// memory).
+// rejection, where a given child is judged after another was taken out, where
+// u is within 2^-16 of a child's border, and once to draw the next token (its
+// weights then stay in shared memory).
 //
 // Measured (128256 tokens, both launches from a graph): one row 12.5 us, of
 // which the walk's dependent steps are the larger part (with 8 CTAs per
@@ -41,6 +42,11 @@ constexpr int kWalkCluster = 16;  // CTAs of one sequence; more than 8 need the 
 constexpr int kGroup = 256;       // entries that a warp reads at a time
 constexpr int64_t kMaxVocab = 262144;
 constexpr double kUnit = 17592186044416.0;  // 2^44
+// A row's float32 sum of exponentials is within 2^-16 of the integer weights'
+// sum: up to 93 roundings of 2^-24 on the way of a term (23 in its chunk, 10
+// joins of 7), 2^-22 of ex2.approx, and arguments of up to 64 binary orders that
+// are off by 3 x 2^-24 of themselves, all together below 1.4e-5.
+constexpr float kSumError = 1.52587890625e-5f;
 // CTAs from which row_stats_kernel takes long chunks (two per SM of a GB300)
 constexpr int64_t kManyChunks = 304;
 
@@ -288,7 +294,8 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
     long long t = 0;
     if (filled) {
 #pragma unroll 4
-      for (int i = lane; i < w1 - w0; i += 32) t += subtract_fixed(w_row[i], s_hi, s_lo, q_row[i]);
+      for (int i = lane; i < w1 - w0; i += 32)
+        t += use_draft ? subtract_fixed(w_row[i], s_hi, s_lo, q_row[i]) : w_row[i];
     } else {  // S is 0
       for (int g = lane; g < w1 - w0; g += kGroup) {
         float l[kGroup / 32], d[kGroup / 32];
@@ -334,72 +341,89 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
   };
   // The walk: warp 0 takes the decisions (they are scalar, some in double
   // precision, of which an SM has two lanes) and asks all warps for a sum
-  // where it needs one.
-  int cur = 0, count = 1, n_gone = 0, i = 1, state = 0;  // state 1: sum of the whole row wanted, 2: of what is left
-  double R = sum[0], S = 0.0, kept = 0.0;                // in units of the largest weight
-  long long all = -1;                                    // the last sum, while it is that of the current state
-  bool filled = false;
+  // where it needs one.  A row's sum from row_stats_kernel (kSumError) decides
+  // where that error does not matter; a child nearer to its border, one that a
+  // draft row has to be subtracted for and one after a given child that was
+  // taken out are judged by the integer sum.
+  // state 1: the sum of what is left wanted (S as it is), 2: of what a draft row leaves, 3: to draw from
+  int cur = 0, count = 1, n_gone = 0, i = 1, state = 0;
+  double R = 0.0, S = 0.0, kept = 0.0;  // in units of the largest weight; R once it is exact
+  long long all = -1;                   // the last sum, while it is that of the current state
+  long long left = 0;                   // R in units of 2^-44
+  bool exact = false, filled = false, rejected = false;
   if (writer && tid == 0) path[0] = 0;
   constexpr double kInv = 1.0 / kUnit;
   for (;;) {
     if (warp == 0) {
-      if (state == 1) {  // a first rejection: from here on R is exact to the unit
-        R = static_cast<double>(all) * kInv;
-        kept = S;
-        S += R;
-        state = 2;
-      } else {
-        if (state == 2) {
-          if (all > 0) R = static_cast<double>(all) * kInv;
-          else S = kept, all = -1;
-        }
-        const bool done = state == 3;
-        state = 0;
-        for (; i < n && state == 0; ++i) {
-          if (up[i] != cur) continue;
-          const int x = tok[i];
-          const bool known = x >= 0 && x < p.vocab;
-          bool yes = false;
-          double here = 0.0;
-          if (p.greedy) {
-            yes = x == arg[cur];
-          } else if (known) {
-            const double w = static_cast<double>(weight_fixed(lx[i], top[cur], p.c_hi, p.c_lo, tab)) * kInv;
-            here = fmax(w - S * static_cast<double>(qx[i]), 0.0);
-            for (int k = 0; k < n_gone; ++k)
-              if (gone[k] == x) here = 0.0;
-            yes = static_cast<double>(us[i]) * static_cast<double>(qx[i]) * R < here;
-          }
-          if (yes) {
-            cur = i;
-            n_gone = 0;
-            S = 0.0;
-            R = sum[i];
-            all = -1;
-            filled = false;
-            if (writer && lane == 0) path[count] = i;
-            ++count;
-          } else if (!p.greedy && use_draft) {
-            state = S == 0.0 ? 1 : 2;
-            if (state == 2) kept = S, S += R;
-          } else if (!p.greedy && known && here > 0.0) {
-            R -= here;
-            __syncwarp();
-            if (lane == 0) gone[n_gone] = x;
-            ++n_gone;
-            __syncwarp();
-          }
-        }
-        if (state == 0 && !done && !p.greedy && all < 0) state = 3;  // the sum to draw from
+      const bool done = state == 3;
+      if (state == 1 || (state == 2 && all > 0)) {
+        left = all;
+        R = static_cast<double>(left) * kInv;
+        exact = true;
+      } else if (state == 2) {
+        S = kept, all = -1;
       }
+      state = 0;
+      for (; i < n; ++i) {
+        if (up[i] != cur) continue;
+        const int x = tok[i];
+        const bool known = x >= 0 && x < p.vocab;
+        bool yes = false;
+        long long here = 0;  // r(x) without a draft row
+        if (p.greedy) {
+          yes = x == arg[cur];
+        } else if (known && !rejected) {
+          here = weight_fixed(lx[i], top[cur], p.c_hi, p.c_lo, tab);
+          for (int k = 0; k < n_gone; ++k)
+            if (gone[k] == x) here = 0;
+          if (!exact) {
+            const float w = static_cast<float>(here) * static_cast<float>(kInv), bar = us[i] * qx[i] * sum[cur];
+            yes = bar < w * (1.0f - kSumError);
+            if (here > 0 && (n_gone > 0 || !(yes || bar > w * (1.0f + kSumError)))) state = 1;
+          } else {
+            double r = static_cast<double>(here) * kInv;
+            if (use_draft) r = fmax(r - S * static_cast<double>(qx[i]), 0.0);
+            yes = static_cast<double>(us[i]) * static_cast<double>(qx[i]) * R < r;
+          }
+        }
+        if (state == 0 && !p.greedy && use_draft && !exact && !yes) state = 1, rejected = true;
+        if (state == 1) break;  // and this child again
+        if (yes) {
+          cur = i;
+          n_gone = 0;
+          S = 0.0;
+          all = -1;
+          exact = filled = false;
+          if (writer && lane == 0) path[count] = i;
+          ++count;
+        } else if (!p.greedy && use_draft) {
+          rejected = false;
+          kept = S;
+          S += R;
+          state = 2;
+          ++i;
+          break;
+        } else if (!p.greedy && here > 0) {  // taken out
+          if (exact) {  // R is worked out before the next child otherwise
+            left -= here;
+            R = static_cast<double>(left) * kInv;
+          }
+          all = -1;
+          __syncwarp();
+          if (lane == 0) gone[n_gone] = x;
+          ++n_gone;
+          __syncwarp();
+        }
+      }
+      if (state == 0 && !done && !p.greedy && all < 0) state = 3;
       if (lane == 0) {
         const float s_hi = static_cast<float>(S);
         ask.state = state;
         ask.cur = cur;
         ask.n_gone = n_gone;
         ask.filled = filled;
-        ask.s_hi = state == 1 ? 0.0f : s_hi;
-        ask.s_lo = state == 1 ? 0.0f : static_cast<float>(S - static_cast<double>(s_hi));
+        ask.s_hi = s_hi;
+        ask.s_lo = static_cast<float>(S - static_cast<double>(s_hi));
         ask.u_all = static_cast<long long>(floor(static_cast<double>(us[0]) * static_cast<double>(all)));
         ask.next = arg[cur];
         ask.draw = !p.greedy && all > 0;

@@ -179,3 +179,63 @@ def test_weights_below_half_a_unit(epq_lib, cuda_dev, vocab, temperature):
         want = T.verify_tree(without, [0, 2], [-1, 0], u, q, temperature)
         assert want[0] == [0] and want[1] < 4
         assert _one(epq_lib, cuda_dev, logits, [0, 2], [-1, 0], u, q, temperature) == (want[0], want[1])
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_siblings_after_a_dominating_one(epq_lib, cuda_dev, seed):
+    """Given children that hold nearly all the mass: after the first is rejected, the others are judged by what is left,
+    whatever part of the whole it is.  Weights are held in units of 2^-44 of the largest, of which the rest's have about
+    170 each: the walk that is expected has the weights in these units."""
+    rng = np.random.default_rng(seed)
+    vocab, n = 128256, 4
+    rest = rng.random(vocab) * 10.0 ** rng.uniform(-11, -10)  # about 1e-6 to 6e-6 in all
+    logits = np.log(rest)
+    a, b, c = rng.choice(vocab, 3, replace=False)
+    logits[a] = 0.0
+    logits[b], logits[c] = np.log(rest.sum() * 0.5), np.log(rest.sum() * 0.3)
+    logits = np.tile(logits.astype(np.float32), (n, 1))
+    w = np.exp(logits[0].astype(np.float64))
+    with np.errstate(divide="ignore"):
+        held = np.tile(np.log(np.rint(w * 2.0 ** 44) * 2.0 ** -44), (n, 1))
+    left = w.sum() - w[a]
+    for near in (-1e-3, -1e-5, 1e-5, 1e-3):
+        for second in (b, c):
+            third = c if second == b else b
+            for u2, u3 in ((w[second] / left * (1 + near), 0.0), (0.999999, w[third] / (left - w[second]) * (1 + near))):
+                u = np.array([0.4, 1 - 2.0 ** -23, u2, u3], np.float32)
+                want = T.verify_tree(held, [0, a, second, third], [-1, 0, 0, 0], u)
+                assert len(want[0]) == 1 or want[0][1] > 1
+                assert _one(epq_lib, cuda_dev, logits, [0, a, second, third], [-1, 0, 0, 0], u) == (want[0], want[1])
+
+
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("spread", [0.5, 3.0, 8.0])
+def test_next_to_a_threshold(epq_lib, cuda_dev, draft, spread):
+    """The two float32 u on either side of an acceptance's border: accepted and not.  (Weights are good to 2^-29 = 1.9e-9
+    of themselves: a border that close to u is left out.)"""
+    rng = np.random.default_rng(int(10 * spread))
+    vocab, nseq, temperature = 50001, 64, float(np.float32(0.7))  # as the call takes it
+    logits = (spread * rng.standard_normal((nseq, 2, vocab))).astype(np.float32)
+    order = logits[:, 0].argsort(1)
+    x = order[np.arange(nseq), -1 - np.arange(nseq) % 8].astype(np.int32)
+    z = logits.astype(np.float64) / temperature
+    w = np.exp(z - z.max(-1, keepdims=True))
+    at = (w[np.arange(nseq), 0, x] / w[:, 0].sum(1))
+    q = None
+    if draft:
+        q = (np.exp(0.3 * rng.standard_normal(logits.shape)) * w / w.sum(-1, keepdims=True)).astype(np.float32)
+        at = at / q[np.arange(nseq), 0, x].astype(np.float64)
+    lo = at.astype(np.float32)
+    lo = np.where(lo.astype(np.float64) < at, lo, np.nextafter(lo, np.float32(0)))
+    hi = np.nextafter(lo, np.float32(1))
+    t = lambda a, d: torch.from_numpy(np.ascontiguousarray(np.asarray(a, d))).to(cuda_dev)  # noqa: E731
+    judged = 0
+    for u, want in ((lo, 2), (hi, 1)):
+        uu = np.stack([np.full(nseq, 0.5), u], 1)
+        n = epq_lib.epq_verify_tree(t(logits, np.float32), t(np.stack([x * 0, x], 1), np.int32), t([[-1, 0]] * nseq, np.int32),
+                                    t(uu, np.float32), draft=None if q is None else t(q, np.float32),
+                                    temperature=temperature)[1].cpu().numpy()
+        clear = (np.abs(u.astype(np.float64) / at - 1) > 4 * 2.0 ** -29) & (u < 1) & (u > 0)
+        judged += clear.sum()
+        assert (n[clear] == want).all(), np.flatnonzero(clear & (n != want))
+    assert judged > nseq / 2
