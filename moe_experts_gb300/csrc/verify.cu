@@ -170,7 +170,7 @@ struct Table {
 __device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, float c_lo, const Table &tab) {
   const float d = l - m;
   float t = d * c_hi;
-  if (t < -46.0f) return 0;  // below half a unit, as are those whose shift is past 63
+  if (t < -45.015625f) return 0;  // below half a unit; the shift is 63 at most
   const float b = d - l;
   const float e = (l - (d - b)) + (-m - b);  // l - m = d + e
   const float te = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);
@@ -181,7 +181,7 @@ __device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, 
   const int ki = static_cast<int>(k), j = ki & 31;
   const long long f = static_cast<long long>(tab.t[j]) + (static_cast<long long>(__float2int_rn(x * tab.f[j])) << 26);
   const int s = 18 - (ki >> 5);
-  return s > 63 ? 0 : static_cast<long long>((static_cast<unsigned long long>(f) + (1ull << (s - 1))) >> s);
+  return static_cast<long long>((static_cast<unsigned long long>(f) + (1ull << (s - 1))) >> s);
 }
 
 // max(w - S q, 0) in the same units, S = s_hi + s_lo.
