@@ -570,7 +570,8 @@ size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab);
  *               one per row is finite
  *   tokens      int32 [n_seq][ntok] (token 0 is not read; an id outside the
  *               vocabulary is rejected)
- *   parent, u   int32, float32 [n_seq][ntok]; u in [0, 1)
+ *   parent, u   int32, float32 [n_seq][ntok]; u in [0, 1) (what lies outside
+ *               counts as the nearest number in it, NaN as 0)
  *   path        int32 [n_seq][ntok]: accepted token indices, 0 first, then -1
  *   n_accept    int32 [n_seq]: entries of path (0 and next_token -1 for a
  *               sequence of no tokens)

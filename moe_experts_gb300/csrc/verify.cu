@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kWalkThreads) walk_kernel(const __grid_constan
     const int x = p.tokens[base + tid], a = p.parent[base + tid];
     tok[tid] = x;
     up[tid] = a;
-    us[tid] = p.greedy ? 0.0f : p.u[base + tid];
+    us[tid] = p.greedy ? 0.0f : fminf(fmaxf(p.u[base + tid], 0.0f), 0.999999940395355225f);  // [0, 1); NaN: 0
     const bool known = tid > 0 && a >= 0 && a < tid && x >= 0 && x < p.vocab;
     lx[tid] = known ? p.logits[static_cast<int64_t>(base + a) * p.ld + x] : -INFINITY;
     qx[tid] = known && use_draft ? p.draft[static_cast<int64_t>(base + a) * p.draft_ld + x] : 1.0f;

@@ -239,3 +239,17 @@ def test_next_to_a_threshold(epq_lib, cuda_dev, draft, spread):
         judged += clear.sum()
         assert (n[clear] == want).all(), np.flatnonzero(clear & (n != want))
     assert judged > nseq / 2
+
+
+@pytest.mark.parametrize("draft", [False, True])
+def test_random_numbers_outside_their_range(epq_lib, cuda_dev, draft):
+    """u outside [0, 1) is the nearest number in it, NaN is 0: a next token is always written."""
+    logits, tokens, parent, u, q = _case(51, 1, 5, 700, 1.0, draft)
+    last = 1 - 2.0 ** -24
+    for bad, good in ((1.0, last), (1e30, last), (np.inf, last), (-0.5, 0.0), (-np.inf, 0.0), (np.nan, 0.0)):
+        for where in ([0], [0, 1, 2, 3, 4]):
+            ub, ug = u[0].copy(), u[0].copy()
+            ub[where], ug[where] = bad, good
+            want = T.verify_tree(logits[0], tokens[0], parent[0], ug, None if q is None else q[0])
+            got = _one(epq_lib, cuda_dev, logits[0], tokens[0], parent[0], ub, None if q is None else q[0])
+            assert got == (want[0], want[1]), (bad, where)
