@@ -566,8 +566,9 @@ size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab);
  * An accepted child becomes c.  When no child is accepted the next token is
  * the least v with r(0) + ... + r(v) > u[0] * R (where nothing is left, the
  * largest logit).
- *   logits      float32 [n_seq][ntok][vocab]; -inf excludes a token, at least
- *               one per row is finite
+ *   logits      float32 [n_seq][ntok][vocab]; -inf excludes a token, and so
+ *               does NaN (the row's lse is then NaN); at least one per row is
+ *               finite and none is +inf
  *   tokens      int32 [n_seq][ntok] (token 0 is not read; an id outside the
  *               vocabulary is rejected)
  *   parent, u   int32, float32 [n_seq][ntok]; u in [0, 1) (what lies outside

@@ -170,7 +170,7 @@ struct Table {
 __device__ __forceinline__ long long weight_fixed(float l, float m, float c_hi, float c_lo, const Table &tab) {
   const float d = l - m;
   float t = d * c_hi;
-  if (t < -45.015625f) return 0;  // below half a unit; the shift is 63 at most
+  if (!(t >= -45.015625f)) return 0;  // below half a unit (the shift is 63 at most), or a NaN
   const float b = d - l;
   const float e = (l - (d - b)) + (-m - b);  // l - m = d + e
   const float te = fmaf(d, c_hi, -t) + fmaf(d, c_lo, e * c_hi);

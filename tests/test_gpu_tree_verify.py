@@ -253,3 +253,18 @@ def test_random_numbers_outside_their_range(epq_lib, cuda_dev, draft):
             want = T.verify_tree(logits[0], tokens[0], parent[0], ug, None if q is None else q[0])
             got = _one(epq_lib, cuda_dev, logits[0], tokens[0], parent[0], ub, None if q is None else q[0])
             assert got == (want[0], want[1]), (bad, where)
+
+
+@pytest.mark.parametrize("draft", [False, True])
+def test_logits_that_are_nan_are_excluded(epq_lib, cuda_dev, draft):
+    """A NaN logit weighs nothing, as -inf does: the same path and next token (the row's log sum is NaN)."""
+    for seed in range(8):
+        logits, tokens, parent, u, q = _case(60 + seed, 1, 6, 900, 1.0, draft)
+        rng = np.random.default_rng(seed)
+        bad = rng.random(logits.shape) < 0.05
+        if seed % 2:
+            bad[0, parent[0, 1], tokens[0, 1]] = True  # a drafted token among them
+        without = np.where(bad, -np.inf, logits).astype(np.float32)
+        want = T.verify_tree(without[0], tokens[0], parent[0], u[0], None if q is None else q[0])
+        got = _one(epq_lib, cuda_dev, np.where(bad, np.nan, logits)[0], tokens[0], parent[0], u[0], None if q is None else q[0])
+        assert got == (want[0], want[1]), seed
