@@ -28,6 +28,7 @@
 // a table entry of 62 bits plus a small float, shifted right by 18 - n.  (GB300
 // has two double-precision lanes per SM and clock; the same pass in double
 // precision took 0.8 ms for 128256 tokens.)
+#include <algorithm>
 #include <cmath>
 
 #include "pages.cuh"
@@ -547,7 +548,8 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   p.n_seq = n_seq;
   p.ntok = ntok;
   p.splits = static_cast<int>(stats_splits(rows, vocab));
-  const double c = 1.4426950408889634 / (p.greedy ? 1.0 : static_cast<double>(temperature));
+  // finite in float32 for the smallest temperatures too
+  const double c = std::min(1.4426950408889634 / (p.greedy ? 1.0 : static_cast<double>(temperature)), 3.4e38);
   p.c_hi = static_cast<float>(c);
   p.c_lo = static_cast<float>(c - static_cast<double>(p.c_hi));
   p.inv_t = p.greedy ? 1.0f : static_cast<float>(1.0 / static_cast<double>(temperature));

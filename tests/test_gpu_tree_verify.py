@@ -268,3 +268,16 @@ def test_logits_that_are_nan_are_excluded(epq_lib, cuda_dev, draft):
         want = T.verify_tree(without[0], tokens[0], parent[0], u[0], None if q is None else q[0])
         got = _one(epq_lib, cuda_dev, np.where(bad, np.nan, logits)[0], tokens[0], parent[0], u[0], None if q is None else q[0])
         assert got == (want[0], want[1]), seed
+
+
+@pytest.mark.parametrize("draft", [False, True])
+@pytest.mark.parametrize("temperature", [1e-30, 1e-40, 1e30])
+def test_extreme_temperatures(epq_lib, cuda_dev, draft, temperature):
+    """The largest logit has all the weight, or every token the same."""
+    for seed in range(4):
+        logits, tokens, parent, u, q = _case(80 + seed, 1, 6, 700, 1.0, draft)
+        top = logits[0].argmax(1)
+        tokens[0, 1:] = np.where(seed % 2 + np.arange(1, 6) % 2 > 0, top[parent[0, 1:]], tokens[0, 1:])
+        want = T.verify_tree(logits[0], tokens[0], parent[0], u[0], None if q is None else q[0], temperature)
+        got = _one(epq_lib, cuda_dev, logits[0], tokens[0], parent[0], u[0], None if q is None else q[0], temperature)
+        assert got == (want[0], want[1]), seed
