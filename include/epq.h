@@ -580,7 +580,8 @@ size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab);
  *   lse         NULL or float32 [n_seq][ntok]: log sum_v exp(l_v / temperature)
  *               (greedy: temperature 1), 0 for unused rows
  * Weights are held to 2^-44 of the largest and summed as integers, so the
- * result does not depend on the order of summation.  vocab 1..262144. */
+ * result does not depend on the order of summation; the lse is float32
+ * arithmetic.  vocab 1..262144; ws 16-byte aligned (EPQ_ERR_ALIGN). */
 epq_status epq_verify_tree(const float *logits, int64_t vocab, const int32_t *tokens, const int32_t *parent,
                            const float *u, int n_seq, int ntok, const epq_verify_opts *opts, int32_t *path,
                            int32_t *n_accept, int32_t *next_token, float *lse, void *ws, size_t ws_bytes,

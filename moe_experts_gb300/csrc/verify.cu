@@ -534,7 +534,9 @@ extern "C" epq_status epq_verify_tree(const float *logits, int64_t vocab, const 
   p.draft_ld = opts && opts->draft_ld ? opts->draft_ld : vocab;
   if (p.ld < vocab || p.draft_ld < vocab) return EPQ_ERR_SHAPE;
   if (!ws || ws_bytes < need) return EPQ_ERR_WORKSPACE;
-  if (!aligned16(logits) || !aligned16(ws) || (opts && opts->draft && !aligned16(opts->draft))) return EPQ_ERR_ALIGN;
+  if (((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(opts ? opts->draft : nullptr)) & 3) ||
+      !aligned16(ws))
+    return EPQ_ERR_ALIGN;
   DeviceInfo dev;
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int64_t rows = static_cast<int64_t>(n_seq) * ntok;

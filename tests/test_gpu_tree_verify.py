@@ -281,3 +281,20 @@ def test_extreme_temperatures(epq_lib, cuda_dev, draft, temperature):
         want = T.verify_tree(logits[0], tokens[0], parent[0], u[0], None if q is None else q[0], temperature)
         got = _one(epq_lib, cuda_dev, logits[0], tokens[0], parent[0], u[0], None if q is None else q[0], temperature)
         assert got == (want[0], want[1]), seed
+
+
+def test_logits_and_draft_from_any_float(epq_lib, cuda_dev):
+    """Rows that begin between two 16-byte boundaries: a view into a larger tensor."""
+    for shift in (1, 2, 3):
+        logits, tokens, parent, u, q = _case(70 + shift, 2, 5, 1001, 1.0, True)
+        t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(cuda_dev)  # noqa: E731
+
+        def moved(a):
+            wide = torch.full((a.size + 8,), float("nan"), device=cuda_dev)
+            wide[shift:shift + a.size] = t(a).reshape(-1)
+            return wide[shift:shift + a.size].view(a.shape)
+
+        got = epq_lib.epq_verify_tree(moved(logits), t(tokens), t(parent), t(u), draft=moved(q))
+        want = epq_lib.epq_verify_tree(t(logits), t(tokens), t(parent), t(u), draft=t(q))
+        assert all(torch.equal(a, b) for a, b in zip(got[:3], want[:3]))
+        assert torch.equal(got[3], want[3]) or torch.allclose(got[3], want[3], rtol=0, atol=1e-5)

@@ -192,3 +192,14 @@ def test_stream_arguments(epq_lib, monkeypatch):
     monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
     assert _lib._stream_object(0) == "default"
     assert _lib._stream_object(4096) == _lib._stream_object(Handle()) == ("external", 4096)
+
+
+def test_verify_alignment(epq_lib):
+    """Logits and draft rows may begin at any float, the workspace on 16 bytes (a bad address is never read)."""
+    from moe_experts_gb300 import _lib
+
+    lib, n = epq_lib.load(), 1 << 20
+    call = lambda logits, draft, ws: lib.epq_verify_tree(  # noqa: E731
+        logits, 40, n, n, n, 2, 3, ctypes.byref(_lib.VerifyOpts(draft, None, 1.0, 0, 0)), n, n, n, None, ws, 1 << 16, None)
+    for at in ((n + 2, n, n), (n, n + 1, n), (n, n, n + 8)):
+        assert call(*at) == EPQ_ERR_ALIGN
