@@ -23,9 +23,10 @@
 //            the largest factor that block b has in the tile (a power of two
 //            brings that factor into [1, 2)).
 //            That floor would show where every larger weight meets a code 0, so
-//            a tile with a weight below 2^-14 in a row that has not had 12
-//            larger ones takes float32 products in three bf16 parts, which lose
-//            nothing; so does a warp whose block has factors more than 2^11 apart.
+//            a tile with a weight below 2^-14 (times the factor's share of the
+//            tile's largest) in a row that has not had 12 larger ones takes
+//            float32 products in three bf16 parts, which lose nothing; so does
+//            a warp whose block has factors more than 2^6 apart.
 // The weights of a row are relative to its maximum at some earlier tile (the
 // reference), which moves, and the sums with it, only when a weight passes 2^6:
 // so the warps need not agree on a maximum before they form weights, and one
@@ -109,6 +110,7 @@ constexpr float kUp = 9.0f;           // log2 of a weight at its row's reference
 constexpr float kPast = 32768.0f;     // largest weight as it is held: 2^6 at the reference
 constexpr float kWeighty = 0.03125f;  // a weight that counts, as it is held: 2^-14 at the reference
 constexpr float kWeightyMin = 12.0f;  // of them, among a warp's positions
+constexpr float kApart = 0.015625f;   // of a tile's largest factor: 2^-6, from which on fp16 parts do
 
 // What a work item is: row tile rt of head h of sequence s.
 struct Item {
@@ -383,7 +385,7 @@ struct Plan {
   static constexpr uint32_t oWork = oScale + 4u * kRows;            // Work
   static constexpr uint32_t oBar = oWork + sizeof(Work);            // full
   static constexpr uint32_t oTell = oBar + 8u * (kStages + 1);      // [2][warps] see `tell`
-  static constexpr uint32_t oMiss = oTell + 2u * 4u * kWarps;       // [stages] missing pieces
+  static constexpr uint32_t oMiss = oTell + 2u * 8u * kWarps;       // [stages] missing pieces
   static constexpr uint32_t kSmem = oMiss + 4u * kStages + 4u;
 };
 
@@ -726,8 +728,10 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
       // ------------------------------------------------------------ weights
       float *w = reinterpret_cast<float *>(smem + L::oW) + ((k & 1) * kRows + 16 * wm) * kTile;
-      // of a warp: bit 0: a weight past the reference, bit 1: held in float32
-      unsigned *tell = reinterpret_cast<unsigned *>(smem + L::oTell) + (k & 1) * L::kWarps;
+      // of a warp: the least weight in rows without enough that count; bit 0: a
+      // weight past the reference, bit 1: held in float32, bit 2: there is such a
+      // least weight
+      uint2 *tell = reinterpret_cast<uint2 *>(smem + L::oTell) + (k & 1) * L::kWarps;
       float sum[2], now[2] = {weighty[0], weighty[1]};
       {
         float over = 0.0f;
@@ -745,7 +749,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
           }
         }
         // weights that count, until a row has enough of them
-        bool few = false;
+        float least = kPast;
         if (__any_sync(0xffffffffu, fminf(weighty[0], weighty[1]) < kWeightyMin)) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -758,12 +762,13 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
             many += __shfl_xor_sync(0xffffffffu, many, 1);
             many += __shfl_xor_sync(0xffffffffu, many, 2);
             now[b] += many;
-            few = few || (now[b] < kWeightyMin && small < kWeighty);
+            if (now[b] < kWeightyMin) least = fminf(least, small);
           }
+          least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
         }
-        few = __any_sync(0xffffffffu, few);
+        const bool few = least < kWeighty;
         const bool past = __any_sync(0xffffffffu, over > kPast);
-        if (lane == 0) tell[warp] = (past ? 1u : 0u) | (few ? 2u : 0u);
+        if (lane == 0) tell[warp] = make_uint2(__float_as_uint(least), (past ? 1u : 0u) | (few ? 2u : 0u) | (least < kPast ? 4u : 0u));
         // the 16-byte chunks of odd rows are stored with bit 2 of their index
         // flipped; a chunk is 4 weights, or their first parts, then the second
         const int col = (wb * L::kKeys + kOwn * t) ^ ((g & 1) << 4);
@@ -794,10 +799,17 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       }
       __syncthreads();
       // every warp is past the values of the tile before: its stage is free
-      const unsigned told = tell[lane % L::kWarps];
-      fresh = __any_sync(0xffffffffu, told & 1);
-      // bit c: warp c of the row group holds its weights in float32
-      const uint32_t wide = __ballot_sync(0xffffffffu, told & 2) >> (wm * NB) & ((1u << NB) - 1);
+      const uint2 told = tell[lane % L::kWarps];
+      fresh = false;
+      uint32_t wide = 0;  // bit c: warp c of the row group holds its weights in float32
+      float apart = kApart;
+      if (__any_sync(0xffffffffu, told.y)) {
+        fresh = __any_sync(0xffffffffu, told.y & 1);
+        wide = __ballot_sync(0xffffffffu, told.y & 2) >> (wm * NB) & ((1u << NB) - 1);
+        // nor may one bring a weight of a row without enough that count below what counts
+        const uint32_t least = __reduce_min_sync(0xffffffffu, lane % L::kWarps / NB == wm ? told.x : 0x7f800000u);
+        apart = fmaxf(apart, __fdividef(kWeighty, __uint_as_float(least)));
+      }
       if (fresh) {
         __syncthreads();  // `tell` and the maxima are written again
         continue;
@@ -814,9 +826,7 @@ __global__ void __launch_bounds__(Plan<NB, WM>::kThreads, NB == 4 ? (WM == 1 ? 3
       const float new_unit = exp2i(min(max(15 - static_cast<int>(largest >> 10), -15), 15));
       const float moved = new_unit * (1.0f / unit);
       unit = new_unit;
-      // factors of the warp's columns that differ by more than 2^11 in a tile:
-      // float32, too
-      const bool slow = wide || !(half_value(largest) <= 2048.0f * half_value(smallest));
+      const bool slow = wide || !(half_value(largest) * apart <= half_value(smallest));  // float32, too
       const bool special = tile * kTile + kTile > it.len;
       // ------------------------------------------------------------ values
       // The tile's products go to accumulators of their own: the tensor cores

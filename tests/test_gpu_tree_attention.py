@@ -356,3 +356,29 @@ def test_missing_pages_leave_the_others(epq_lib, cuda_dev, P, low):
             list(range(last[1] - 3)),                                     # all but the last ones
             list(range(last[2])) + ([last[2]] if 700 % P else []), []]  # all
     _check_without(epq_lib, c, gone)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("n", [1, 5, 300])
+def test_small_weight_on_a_small_value(epq_lib, cuda_dev, n, D):
+    """One position has nearly all the weight and the largest value, but zeros among its elements: those elements are
+    made by the others' small weights on rows that are 2^5 to 2^10 smaller, and count by themselves."""
+    for ratio in (5, 8, 10):
+        c = Case(epq_lib, cuda_dev, [n], 4, 4, 1, D, 32, seed=ratio, spread=6.0)
+        a, k = (c.heads + c.kv) * D, c.heads * D
+        axis = c.rng.choice([-1.0, 1.0], D)
+        # the last committed position takes the weight: 2^-11 and less for the others
+        keys = 0.3 * c.rng.standard_normal((1, n, D))
+        keys[0, n - 1] = axis
+        c.K[0] = _rows(keys.astype(np.float32))
+        c.qkv[0, :, k:a] = 0.3 * c.rng.standard_normal((c.ntok, D))
+        c.qkv[0, :, :k] = np.tile(axis * 8.0 / math.sqrt(D), c.heads) + c.rng.standard_normal((c.ntok, k)) * 0.5
+        v = 2.0 ** -ratio * c.rng.standard_normal((1, n, D))
+        v[0, n - 1] = np.where(np.arange(D) % 3 == 0, 0.0, c.rng.standard_normal(D))
+        c.V[0] = _rows(v.astype(np.float32))
+        c.qkv[0, :, a:] = 2.0 ** -ratio * c.rng.standard_normal((c.ntok, D))
+        for p in range(n):
+            c.pool[0, c.table[0, p // 32], :, 0, p % 32] = c.K[0][:, p]
+            c.pool[0, c.table[0, p // 32], :, 1, p % 32] = c.V[0][:, p]
+        c.c.pool.copy_(torch.from_numpy(c.pool))
+        c.check()
