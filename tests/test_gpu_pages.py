@@ -266,3 +266,36 @@ def test_results_of_a_call_on_another_stream(epq_lib, cuda_dev):
             assert not again(like, side) & at
             torch.cuda.synchronize()
     assert epq_lib.epq_device_error() == 0
+
+
+def test_step_of_sequences_without_room(epq_lib, cuda_dev):
+    """The step of the usage text: two branches of one page and no free one, next to a sequence with room.  The branches
+    sit it out, their shared page keeps its bytes, and their next tokens are -1."""
+    cache = epq_lib.PagedKVCache(2, 3, 2, 128, 3, 4, 16, cuda_dev)
+    cache.pool.copy_(torch.randint(0, 64, cache.pool.shape, dtype=torch.uint8, device=cuda_dev))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda_dev)  # noqa: E731
+    epq_lib.epq_pages_reserve(cache, i32(20, 0, 10))  # all three pages
+    cache.length.copy_(i32(20, 0, 10))
+    epq_lib.epq_pages_fork(cache, i32(0), i32(1))
+    before = cache.pool.clone()
+    extra = i32(4, 4, 4)
+    parent = i32(-1, 0, 1, 2).repeat(3, 1)
+    q, k, v = (torch.randn((3, 4, n * 128), device=cuda_dev) for n in (4, 2, 2))
+    logits, u = torch.randn((3, 4, 50), device=cuda_dev), torch.zeros((3, 4), device=cuda_dev)
+    order = [2, 0, 1]  # the sequence with room first: later ones do not fit
+    cache.table.copy_(cache.table[order].clone())
+    cache.length.copy_(cache.length[order].clone())
+    status = epq_lib.epq_pages_reserve(cache, extra)
+    n_tok = extra * (status == 0)
+    mask = epq_lib.epq_tree_mask(parent)
+    for layer in range(2):
+        epq_lib.epq_attention_tree(q, k, v, cache, layer, 4, 0.1, mask=mask, n_tok=n_tok)
+    path, n, nxt, _ = epq_lib.epq_verify_tree(logits, parent.clamp(min=0), parent, u, n_tok=n_tok)
+    epq_lib.epq_pages_compact(cache, path, n)
+    assert status.tolist() == [0, 1, 1] and n_tok.tolist() == [4, 0, 0]
+    assert n.tolist()[1:] == [0, 0] and nxt.tolist()[1:] == [-1, -1] and n[0].item() >= 1
+    assert cache.length.tolist() == [10 + n[0].item(), 20, 20]
+    own = cache.table[0, 0].item()
+    others = [p for p in range(3) if p != own]
+    assert torch.equal(cache.pool[:, others], before[:, others]) and not torch.equal(cache.pool[:, own], before[:, own])
+    assert epq_lib.epq_device_error() == 0
