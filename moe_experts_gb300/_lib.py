@@ -10,6 +10,7 @@ a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -166,16 +167,20 @@ def _stream_object(stream):
     return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
-def _empty(shape, dtype, dev, stream) -> torch.Tensor:
-    """Memory that a call on `stream` (None: the current one) allocates for its results or scratch.  It comes from that
-    stream's memory, which nothing before the call can still be using, and is not given out again before the current
-    stream is done with it either."""
-    if stream is None or dev.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
+    """torch.empty for the results or scratch of a call on `stream`.  It comes from that stream's memory, which nothing
+    before the call can still be using, and is not given out again before the current stream is done with it either."""
+    if device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_stream_object(stream)):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream())
     return t
+
+
+def _allocator(stream):
+    """torch.empty, or its like for a call on a stream that is named."""
+    return torch.empty if stream is None else functools.partial(_empty_on, stream)
 
 
 def _check(fn: str, st: int):
@@ -411,26 +416,50 @@ def epq_attention_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tens
 
 # ------------------------------------------------------------------ paged cache
 # The calls of a speculative step are short next to what Python costs, so the
-# functions below compare shapes as tuples and pass addresses as integers.
-def _wrong(t, name, dtype, shape, dev):
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {dev}")
+# functions below compare shapes as tuples, GPUs by their index, and pass
+# addresses as integers.
+def _place(t):
+    """Where t lies: a GPU's index, or the torch.device that is none (argument checks work without a GPU)."""
+    return t.get_device() if t.is_cuda else t.device
+
+
+def _elsewhere(t, name, at):
+    if _place(t) != at:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {f'cuda:{at}' if type(at) is int else at}")
+
+
+def _refuse(t, name, dtype, shape, at):
+    _elsewhere(t, name, at)
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
-def _need(t, name, dtype, shape, dev):
-    """t is a contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        _wrong(t, name, dtype, shape, dev)
+def _need(t, name, dtype, shape, at):
+    """t is a contiguous tensor of this type and shape at this place (_place)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != at or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, at)
     return t.data_ptr()
 
 
-def _scratch(t, dev):
-    """A workspace that the caller holds: its address and bytes."""
-    if t.device != dev or not t.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
+def _result(t, name, dtype, shape, at, new, dev):
+    """A result tensor and its address: the caller's, or one made here (which needs no check)."""
+    if t is None:
+        t = new(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _need(t, name, dtype, shape, at)
+
+
+def _queue(stream, at):
+    """The handle of the stream to launch on: the one named, or the current one of the GPU that the tensors are on."""
+    return _raw_stream(at) if stream is None and type(at) is int and _raw_stream is not None else _stream(stream)
+
+
+def _scratch(t, at):
+    """A workspace: its address and bytes."""
+    if t.get_device() != at or not t.is_contiguous():
+        _refuse(t, "workspace", t.dtype, t.shape, at)
     return t.data_ptr(), t.numel()
 
 
@@ -461,23 +490,23 @@ class PagedKVCache:
     def _bind(self, pool, table, length, refs):
         if pool.dim() != 6 or pool.shape[3] != 2 or table.dim() != 2:
             raise ValueError("pool must be [layers, pages, heads, 2, page_size, row] and table [n_seq, max_pages]")
-        dev = pool.device
-        _need(pool, "pool", torch.uint8, pool.shape, dev)
-        _need(table, "table", torch.int32, table.shape, dev)
-        _need(length, "length", torch.int32, (table.shape[0],), dev)
-        _need(refs, "refs", torch.int32, (pool.shape[1],), dev)
+        self.device, self._at = pool.device, _place(pool)
+        _need(pool, "pool", torch.uint8, pool.shape, self._at)
+        _need(table, "table", torch.int32, table.shape, self._at)
+        _need(length, "length", torch.int32, (table.shape[0],), self._at)
+        _need(refs, "refs", torch.int32, (pool.shape[1],), self._at)
         self.n_layers, self.n_pages, self.n_kv_heads, _, self.page_size, rb = pool.shape
         self.head_dim = rb * 16 // 17
         if epq_kv_row_bytes(self.head_dim) != rb:
             raise ValueError(f"rows of {rb} bytes are no cache rows")
         self.n_seq, self.max_pages = table.shape
-        self.pool, self.table, self.length, self.refs, self.device = pool, table, length, refs, dev
+        self.pool, self.table, self.length, self.refs = pool, table, length, refs
         self._p = Pages(_addr(pool), _addr(table), _addr(length), _addr(refs), None, self.n_layers, self.n_pages,
                         self.n_kv_heads, self.head_dim, self.page_size, self.n_seq, self.max_pages)
         n = int(load().epq_pages_work_bytes(ctypes.byref(self._p)))
         if n == 0:
             raise ValueError("sizes of the paged cache not supported")
-        self.work = torch.zeros(n, dtype=torch.uint8, device=dev)
+        self.work = torch.zeros(n, dtype=torch.uint8, device=self.device)
         self._p.work = self.work.data_ptr()
         self._ref = ctypes.byref(self._p)
         self._per_seq = (self.n_seq,)
@@ -485,8 +514,9 @@ class PagedKVCache:
 
 def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=None) -> None:
     """new_length int32 [n_seq] (negative: leave): shorten sequences and give their pages back (0 frees one)."""
-    n = _need(new_length, "new_length", torch.int32, cache._per_seq, cache.device)
-    st = _lib.epq_pages_truncate(cache._ref, n, _stream(stream))
+    at = cache._at
+    n = _need(new_length, "new_length", torch.int32, cache._per_seq, at)
+    st = _lib.epq_pages_truncate(cache._ref, n, _queue(stream, at))
     if st:
         raise EpqError("epq_pages_truncate", st)
 
@@ -494,11 +524,11 @@ def epq_pages_truncate(cache: PagedKVCache, new_length: torch.Tensor, stream=Non
 def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, status: torch.Tensor | None = None,
                    stream=None) -> None:
     """Sequences dst (int32 [n], empty) become copies of src, sharing their pages; no entries: nothing happens."""
-    n, dev = dst.shape[0], cache.device
-    a, b = _need(src, "src", torch.int32, (n,), dev), _need(dst, "dst", torch.int32, (n,), dev)
-    c = None if status is None else _need(status, "status", torch.int32, (n,), dev)
+    n, at = dst.shape[0], cache._at
+    a, b = _need(src, "src", torch.int32, (n,), at), _need(dst, "dst", torch.int32, (n,), at)
+    c = None if status is None else _need(status, "status", torch.int32, (n,), at)
     if n:
-        st = _lib.epq_pages_fork(cache._ref, a, b, n, c, _stream(stream))
+        st = _lib.epq_pages_fork(cache._ref, a, b, n, c, _queue(stream, at))
         if st:
             raise EpqError("epq_pages_fork", st)
 
@@ -506,11 +536,10 @@ def epq_pages_fork(cache: PagedKVCache, src: torch.Tensor, dst: torch.Tensor, st
 def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """Make extra (int32 [n_seq]) more positions of every sequence writable -> status int32 [n_seq]."""
-    e = _need(extra, "extra", torch.int32, cache._per_seq, cache.device)
-    if status is None:
-        status = _empty(cache._per_seq, torch.int32, cache.device, stream)
-    st = _lib.epq_pages_reserve(cache._ref, e, _need(status, "status", torch.int32, cache._per_seq, cache.device),
-                                _stream(stream))
+    at = cache._at
+    e = _need(extra, "extra", torch.int32, cache._per_seq, at)
+    status, status_at = _result(status, "status", torch.int32, cache._per_seq, at, _allocator(stream), cache.device)
+    st = _lib.epq_pages_reserve(cache._ref, e, status_at, _queue(stream, at))
     if st:
         raise EpqError("epq_pages_reserve", st)
     return status
@@ -518,10 +547,10 @@ def epq_pages_reserve(cache: PagedKVCache, extra: torch.Tensor, status: torch.Te
 
 def epq_pages_compact(cache: PagedKVCache, path: torch.Tensor, n_keep: torch.Tensor, stream=None) -> None:
     """Commit the drafted rows path (int32 [n_seq, ntok], n_keep int32 [n_seq] of them) in every layer."""
-    ntok = path.shape[-1]
-    a = _need(path, "path", torch.int32, (cache.n_seq, ntok), cache.device)
-    st = _lib.epq_pages_compact(cache._ref, a, _need(n_keep, "n_keep", torch.int32, cache._per_seq, cache.device), ntok,
-                                _stream(stream))
+    ntok, at = path.shape[-1], cache._at
+    a = _need(path, "path", torch.int32, (cache.n_seq, ntok), at)
+    st = _lib.epq_pages_compact(cache._ref, a, _need(n_keep, "n_keep", torch.int32, cache._per_seq, at), ntok,
+                                _queue(stream, at))
     if st:
         raise EpqError("epq_pages_compact", st)
 
@@ -531,11 +560,10 @@ def epq_tree_mask(parent: torch.Tensor, mask: torch.Tensor | None = None, stream
     """parent int32 [n_seq, ntok] -> mask int64 [n_seq, ntok] (bit j: token j is i or an ancestor of i)."""
     if parent.dim() != 2:
         raise ValueError("parent must be [n_seq, ntok]")
-    a = _need(parent, "parent", torch.int32, parent.shape, parent.device)
-    if mask is None:
-        mask = _empty(parent.shape, torch.int64, parent.device, stream)
-    b = _need(mask, "mask", torch.int64, parent.shape, parent.device)
-    _check("epq_tree_mask", load().epq_tree_mask(a, parent.shape[0], parent.shape[1], b, _stream(stream)))
+    at = _place(parent)
+    a = _need(parent, "parent", torch.int32, parent.shape, at)
+    mask, b = _result(mask, "mask", torch.int64, parent.shape, at, _allocator(stream), parent.device)
+    _check("epq_tree_mask", load().epq_tree_mask(a, parent.shape[0], parent.shape[1], b, _queue(stream, at)))
     return mask
 
 
@@ -544,13 +572,15 @@ def epq_attention_tree_workspace(cache: PagedKVCache, n_heads: int, ntok: int, s
     n = int(load().epq_attention_tree_workspace_bytes(cache._ref, n_heads, ntok))
     if n == 0:
         raise ValueError("sizes of the tree attention not supported")
-    return _empty(n, torch.uint8, cache.device, stream)
+    return _allocator(stream)(n, dtype=torch.uint8, device=cache.device)
 
 
-def _token_strides(t, name, shape, dev):
+def _token_strides(t, name, shape, at):
     """Floats between sequences and tokens of t [n_seq, ntok, n] (0: a dimension of one entry says nothing)."""
-    if t.dtype is not torch.float32 or t.shape != shape or t.device != dev:
-        raise ValueError(f"{name}: expected float32 {list(shape)} on {dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != at:
+        _elsewhere(t, name, at)
+        if t.dtype is not torch.float32 or t.shape != shape:
+            raise ValueError(f"{name}: expected float32 {list(shape)}, got {t.dtype} {list(t.shape)}")
     a, b, c = t.stride()
     if c != 1 or (a == 0 and shape[0] > 1) or (b == 0 and shape[1] > 1):
         raise ValueError(f"{name}: rows must be contiguous and not broadcast")
@@ -563,23 +593,21 @@ def epq_attention_tree(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """q [n_seq, ntok, n_heads*D], k_new/v_new [n_seq, ntok, n_kv*D] (float32; views of one wider buffer are
     read in place) -> out [n_seq, ntok, n_heads*D]; the new rows are stored behind the committed positions."""
-    ntok, nseq, D, dev = q.shape[1], cache.n_seq, cache.head_dim, cache.device
+    ntok, nseq, D, at = q.shape[1], cache.n_seq, cache.head_dim, cache._at
     shape = (nseq, ntok, n_heads * D)
-    q_seq, q_tok = _token_strides(q, "q", shape, dev)
+    q_seq, q_tok = _token_strides(q, "q", shape, at)
     kv = (nseq, ntok, cache.n_kv_heads * D)
-    kv_seq, kv_tok = _token_strides(k_new, "k_new", kv, dev)
-    if _token_strides(v_new, "v_new", kv, dev) != (kv_seq, kv_tok):
+    kv_seq, kv_tok = _token_strides(k_new, "k_new", kv, at)
+    if _token_strides(v_new, "v_new", kv, at) != (kv_seq, kv_tok):
         raise ValueError("k_new and v_new must have the same strides")
-    if out is None:
-        out = _empty(shape, torch.float32, dev, stream)
+    out, out_at = _result(out, "out", torch.float32, shape, at, _allocator(stream), cache.device)
     if workspace is None:
         workspace = epq_attention_tree_workspace(cache, n_heads, ntok, stream)
-    o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), dev),
-                          None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, dev),
+    o = AttentionTreeOpts(None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
+                          None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at),
                           q_tok, q_seq, kv_tok, kv_seq)
     st = _lib.epq_attention_tree(cache._ref, layer, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), n_heads, ntok,
-                                 scale, ctypes.byref(o), _need(out, "out", torch.float32, shape, dev),
-                                 *_scratch(workspace, dev), _stream(stream))
+                                 scale, ctypes.byref(o), out_at, *_scratch(workspace, at), _queue(stream, at))
     if st:
         raise EpqError("epq_attention_tree", st)
     return out
@@ -590,7 +618,7 @@ def epq_verify_tree_workspace(logits: torch.Tensor, stream=None) -> torch.Tensor
     n = int(load().epq_verify_tree_workspace_bytes(logits.shape[0], logits.shape[1], logits.shape[2]))
     if n == 0:
         raise ValueError("sizes of the verification not supported")
-    return _empty(n, torch.uint8, logits.device, stream)
+    return _allocator(stream)(n, dtype=torch.uint8, device=logits.device)
 
 
 def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, u: torch.Tensor | None = None,
@@ -608,20 +636,19 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     full = logits.shape
     nseq, ntok, vocab = full
     tree, each = (nseq, ntok), (nseq,)
-    path = _empty(tree, i32, dev, stream) if path is None else path
-    n_accept = _empty(each, i32, dev, stream) if n_accept is None else n_accept
-    next_token = _empty(each, i32, dev, stream) if next_token is None else next_token
-    lse = _empty(tree, f32, dev, stream) if lse is None else lse
+    at, new = _place(logits), _allocator(stream)
+    path, path_at = _result(path, "path", i32, tree, at, new, dev)
+    n_accept, n_at = _result(n_accept, "n_accept", i32, each, at, new, dev)
+    next_token, next_at = _result(next_token, "next_token", i32, each, at, new, dev)
+    lse, lse_at = _result(lse, "lse", f32, tree, at, new, dev)
     if workspace is None:
         workspace = epq_verify_tree_workspace(logits, stream)
-    o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full, dev),
-                   None if n_tok is None else _need(n_tok, "n_tok", i32, each, dev), temperature, 0, 0)
+    o = VerifyOpts(None if draft is None else _need(draft, "draft", f32, full, at),
+                   None if n_tok is None else _need(n_tok, "n_tok", i32, each, at), temperature, 0, 0)
     st = lib.epq_verify_tree(
-        _need(logits, "logits", f32, full, dev), vocab, _need(tokens, "tokens", i32, tree, dev),
-        _need(parent, "parent", i32, tree, dev), None if u is None else _need(u, "u", f32, tree, dev), nseq, ntok,
-        ctypes.byref(o), _need(path, "path", i32, tree, dev), _need(n_accept, "n_accept", i32, each, dev),
-        _need(next_token, "next_token", i32, each, dev), _need(lse, "lse", f32, tree, dev), *_scratch(workspace, dev),
-        _stream(stream))
+        _need(logits, "logits", f32, full, at), vocab, _need(tokens, "tokens", i32, tree, at),
+        _need(parent, "parent", i32, tree, at), None if u is None else _need(u, "u", f32, tree, at), nseq, ntok,
+        ctypes.byref(o), path_at, n_at, next_at, lse_at, *_scratch(workspace, at), _queue(stream, at))
     if st:
         raise EpqError("epq_verify_tree", st)
     return path, n_accept, next_token, lse
