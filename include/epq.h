@@ -579,7 +579,8 @@ size_t epq_verify_tree_workspace_bytes(int n_seq, int ntok, int64_t vocab);
  *   next_token  int32 [n_seq]
  *   lse         NULL or float32 [n_seq][ntok]: log sum_v exp(l_v / temperature)
  *               (greedy: temperature 1), 0 for unused rows
- * Weights are held to 2^-44 of the largest and summed as integers, so the
+ * Weights are held in units of 2^-44 of the largest (below half a unit they are
+ * 0: such a token is neither accepted nor drawn) and summed as integers, so the
  * result does not depend on the order of summation; the lse is float32
  * arithmetic.  vocab 1..262144; ws 16-byte aligned (EPQ_ERR_ALIGN). */
 epq_status epq_verify_tree(const float *logits, int64_t vocab, const int32_t *tokens, const int32_t *parent,

@@ -45,8 +45,9 @@
 // one of row tile 0 also stores them in the cache).
 // Measured with 32 query and 8 key/value heads of 128 (both launches, from a
 // graph): 64 tokens over 8193 positions 107 us, four sequences of 8 tokens over
-// 32 k positions 173 us (280 MB of cache, 1.6 TB/s), 8 tokens over 1024
-// positions 17 us, one token over 37 positions 10 us.  The long ones are bound
+// 32 k positions 174 us (280 MB of cache, 1.6 TB/s), 8 tokens over 1024
+// positions 18 us, one token over 37 positions 10 us; heads of 256: 196, 344,
+// 19 and 10 us.  The long ones are bound
 // by instructions between the products, 0.52 issued per cycle of a scheduler
 // with 4 warps each (the MMA pipe is 31 % busy): a warp spends ~870 on a tile
 // of 16 rows, 64 of them MMAs.  Short ones are one chain of tile, parts and

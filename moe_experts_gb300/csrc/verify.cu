@@ -15,13 +15,14 @@
 // Measured (128256 tokens, both launches from a graph): one row 12.5 us, of
 // which the walk's dependent steps are the larger part (with 8 CTAs per
 // sequence that read the row again to draw: 25 us); 8 rows with draft
-// probabilities 22 us; 4 sequences of 64 rows 54 us, 131 MB.
+// probabilities 21 us; 4 sequences of 64 rows 52 us, 131 MB (51 to 55 with the
+// rejections that the inputs make).
 //
 // Drawing compares a partial sum of up to 2^18 weights with u times their
 // total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
 // 2^-29 of themselves (root mean square 2^-31.5) and summed as 64-bit integers
 // in units of 2^-44 (0 below half a unit): the sums do not depend on their
-// order, and a wrong neighbour needs u within 2e-9 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
+// order, and a wrong neighbour needs u within 4e-9 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
 // (n, j integers, |g| <= 1/64, everything that float32 loses of l - max and
 // of the product kept in a second float)
 //   w = 2^n 2^(j/32) (1 + (z + z^2/2 + z^3/6 + ...)),  z = g ln 2,
