@@ -111,7 +111,7 @@ constexpr float kUp = 9.0f;           // log2 of a weight at its row's reference
 constexpr float kPast = 32768.0f;     // largest weight as it is held: 2^6 at the reference
 constexpr float kWeighty = 0.03125f;  // a weight that counts, as it is held: 2^-14 at the reference
 constexpr float kWeightyMin = 12.0f;  // of them, among a warp's positions
-constexpr float kApart = 0.015625f;   // of a tile's largest factor: 2^-6, from which on fp16 parts do
+constexpr float kApart = 0.015625f;   // 2^-6: down to this share of its tile's largest a factor takes fp16 parts
 
 // What a work item is: row tile rt of head h of sequence s.
 struct Item {

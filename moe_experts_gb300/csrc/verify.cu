@@ -22,9 +22,10 @@
 // total.  The weights w(v) = exp((l_v - max) / T) are therefore formed to
 // 2^-29 of themselves (root mean square 2^-31.5) and summed as 64-bit integers
 // in units of 2^-44 (0 below half a unit): the sums do not depend on their
-// order, and a wrong neighbour needs u within 4e-9 of a boundary.  With t = (l - max) log2(e) / T = n + j / 32 + g
-// (n, j integers, |g| <= 1/64, everything that float32 loses of l - max and
-// of the product kept in a second float)
+// order, and a wrong neighbour needs u within 4e-9 of a boundary.  With t =
+// (l - max) log2(e) / T = n + j / 32 + g (n, j integers, |g| <= 1/64,
+// everything that float32 loses of l - max and of the product kept in a second
+// float)
 //   w = 2^n 2^(j/32) (1 + (z + z^2/2 + z^3/6 + ...)),  z = g ln 2,
 // a table entry of 62 bits plus a small float, shifted right by 18 - n.  (GB300
 // has two double-precision lanes per SM and clock; the same pass in double
