@@ -91,7 +91,8 @@ const char *epq_status_string(epq_status s);
 int epq_last_cuda_error(void);
 
 /* Reads and clears the device-side error record of the current device:
- * 0 = none; 5 = a position of a paged cache had no page (see epq_pages);
+ * 0 = none; 5 = a position of a paged cache had no page (see epq_pages); 6 =
+ * a token's position lies outside the rotation's table (see epq_rotation);
  * otherwise a code naming the pipeline wait that timed out.
  * Synchronizes the device. */
 int epq_device_error(void);
@@ -587,6 +588,109 @@ epq_status epq_verify_tree(const float *logits, int64_t vocab, const int32_t *to
                            const float *u, int n_seq, int ntok, const epq_verify_opts *opts, int32_t *path,
                            int32_t *n_accept, int32_t *next_token, float *lse, void *ws, size_t ws_bytes,
                            epq_stream_t stream);
+
+/* ---------------------------------------------------------------- rotary positions
+ * A token at position p turns the pairs of each head's rotated elements by
+ * the angles p f_j:
+ *   y0 = x0 c - x1 s,  y1 = x1 c + x0 s,  (c, s) = magnitude (cos, sin)(p f_j)
+ * each product and each sum rounded to float32.  (The pages' decode steps leave
+ * the positions out; the operators here are the usual rotary ones.)
+ *
+ * epq_rope_frequencies: f_j = base^(-2j/rot_dim) for j < rot_dim/2, changed by
+ * `scaling` (NULL: plain) for contexts longer than the trained one:
+ *   EPQ_ROPE_PLAIN   f
+ *   EPQ_ROPE_LINEAR  f / factor
+ *   EPQ_ROPE_PARTS   f/factor r_j + f (1 - r_j), r_j a ramp from 0 to 1 in j
+ *                    between floor(d(high)) and ceil(d(low)), where d(n) =
+ *                    rot_dim log(context / (2 pi n)) / (2 log base) is the
+ *                    (fractional) pair that turns n times over `context`
+ *                    positions; magnitude = 0.1 log(factor) + 1
+ *   EPQ_ROPE_BANDS   f/factor (1 - r_j) + f r_j, r_j a ramp from 0 to 1 in the
+ *                    turns of the pair over `context`, between low and high
+ * low and high are the numbers of turns (the usual values: parts 1 and 32,
+ * bands 1 and 4).  freq (double [rot_dim/2]) and magnitude are HOST memory.
+ * rot_dim even, 2..1024; base > 1; factor >= 1, context >= 1, 0 < low < high.
+ * Host-only. */
+enum { EPQ_ROPE_PLAIN = 0, EPQ_ROPE_LINEAR = 1, EPQ_ROPE_PARTS = 2, EPQ_ROPE_BANDS = 3 };
+typedef struct {
+  int kind;
+  double factor, context, low, high;
+} epq_rope_scaling;
+epq_status epq_rope_frequencies(int rot_dim, double base, const epq_rope_scaling *scaling, double *freq,
+                                double *magnitude);
+
+/* epq_rope_table: float32 table [n_pos][rot_dim/2][2] of (c, s) for positions
+ * 0..n_pos-1, from float64 frequencies (DEVICE, [rot_dim/2]): angles, cosines
+ * and sines in float64, rounded once.  n_pos 1..2^30. */
+epq_status epq_rope_table(const double *freq, int rot_dim, double magnitude, int64_t n_pos, float *table,
+                          epq_stream_t stream);
+
+/* A rotation: elements first .. first + rot_dim - 1 of every head, pairs
+ * (first + j, first + rot_dim/2 + j), or (first + 2j, first + 2j + 1) when
+ * `interleaved` is nonzero.  A token whose position is outside 0..n_pos-1 is
+ * recorded (epq_device_error code 6) and its rotated elements become NaN. */
+typedef struct {
+  const float *table;
+  int64_t n_pos;
+  int rot_dim, first, interleaved;
+} epq_rotation;
+
+/* Options of epq_rope (all-zero: contiguous tensors, token i of every sequence
+ * at position i).
+ *   position NULL or int32 [n_seq][ntok]: the tokens' positions
+ *   start    NULL or int32 [n_seq] (for instance epq_pages.length): without
+ *            `position`, token i is at start[s] + i (NULL: i) ...
+ *   mask     ... or, where mask (uint64 [n_seq][ntok] of epq_tree_mask; ntok
+ *            1..64) is given, at start[s] + the number of its ancestors
+ *   n_tok    NULL or int32 [n_seq]: tokens of each sequence (0..ntok); the
+ *            others' rows are copied unchanged
+ *   x_ld, x_seq_ld, y_ld, y_seq_ld  floats between tokens / sequences of x and
+ *            y (0 = contiguous) */
+typedef struct {
+  const int32_t *position, *start;
+  const uint64_t *mask;
+  const int32_t *n_tok;
+  int64_t x_ld, x_seq_ld, y_ld, y_seq_ld;
+} epq_rope_opts;
+
+/* epq_rope: x, y float32 [n_seq][ntok][n_heads][head_dim]; y may equal x (with
+ * the same strides), else they do not overlap.  Query and key heads that lie
+ * side by side in one buffer are one call.  n_seq, ntok, n_heads >= 1, n_seq *
+ * ntok < 2^31, n_heads <= 65535, head_dim 2..1024; any alignment of floats
+ * (16-byte aligned rows and multiples of 4 are moved 16 bytes at a time).
+ * One launch. */
+epq_status epq_rope(const epq_rotation *rotation, const float *x, float *y, int n_seq, int ntok, int n_heads,
+                    int head_dim, const epq_rope_opts *opts, epq_stream_t stream);
+
+/* ---------------------------------------------------------------- a prompt's rows
+ * Options of epq_pages_append (all-zero: contiguous tensors, nothing rotated).
+ *   rotation NULL or what turns the keys, at the positions of epq_rope_opts
+ *            with start = length
+ *   position, mask, n_tok  as there; the rows beyond n_tok are not stored
+ *   kv_ld, kv_seq_ld  floats between tokens / sequences of k and v (0 =
+ *            contiguous); multiples of 4 */
+typedef struct {
+  const epq_rotation *rotation;
+  const int32_t *position;
+  const uint64_t *mask;
+  const int32_t *n_tok;
+  int64_t kv_ld, kv_seq_ld;
+} epq_append_opts;
+
+/* epq_pages_append: k, v float32 [n_seq][ntok][n_kv_heads][head_dim], k rotated,
+ * quantized to Q8_0 (the packer's arithmetic) and stored in one layer at the
+ * positions length + i of their sequence; length itself stays (epq_pages_advance
+ * ends the step once every layer has its rows).  The positions must have been
+ * reserved; a row without a page is not stored and recorded (epq_device_error
+ * code 5).  A key whose position has no angle is stored with factors of NaN:
+ * what attends to it is NaN.  ntok >= 1, n_seq * ntok * n_kv_heads < 2^30.  One
+ * launch. */
+epq_status epq_pages_append(const epq_pages *pages, int layer, const float *k, const float *v, int ntok,
+                            const epq_append_opts *opts, epq_stream_t stream);
+
+/* epq_pages_advance: commits appended rows, length = min(length + max(n, 0),
+ * max_pages * page_size); n int32 [n_seq]. */
+epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n, epq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -83,7 +83,29 @@ class VerifyOpts(ctypes.Structure):
                 ("ld", ctypes.c_int64), ("draft_ld", ctypes.c_int64)]
 
 
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("context", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int),
+                ("first", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class RopeOpts(ctypes.Structure):
+    _fields_ = [("position", ctypes.c_void_p), ("start", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("n_tok", ctypes.c_void_p), ("x_ld", ctypes.c_int64), ("x_seq_ld", ctypes.c_int64),
+                ("y_ld", ctypes.c_int64), ("y_seq_ld", ctypes.c_int64)]
+
+
+class AppendOpts(ctypes.Structure):
+    _fields_ = [("rotation", ctypes.POINTER(Rotation)), ("position", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("n_tok", ctypes.c_void_p), ("kv_ld", ctypes.c_int64), ("kv_seq_ld", ctypes.c_int64)]
+
+
 EPQ_MOE_ROUTE, EPQ_MOE_GATE_UP, EPQ_MOE_DOWN = 1, 2, 4
+EPQ_ROPE_PLAIN, EPQ_ROPE_LINEAR, EPQ_ROPE_PARTS, EPQ_ROPE_BANDS = 0, 1, 2, 3
 
 
 def declared_symbols() -> list[str]:
@@ -137,6 +159,12 @@ def load(path: str | None = None):
         "epq_verify_tree_workspace_bytes": (ctypes.c_size_t, [i32, i32, i64]),
         "epq_verify_tree": (i32, [vp, i64, vp, vp, vp, i32, i32, ctypes.POINTER(VerifyOpts), vp, vp, vp, vp, vp,
                                   ctypes.c_size_t, vp]),
+        "epq_rope_frequencies": (i32, [i32, ctypes.c_double, ctypes.POINTER(RopeScaling),
+                                       ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+        "epq_rope_table": (i32, [vp, i32, ctypes.c_double, i64, vp, vp]),
+        "epq_rope": (i32, [ctypes.POINTER(Rotation), vp, vp, i32, i32, i32, i32, ctypes.POINTER(RopeOpts), vp]),
+        "epq_pages_append": (i32, [ctypes.POINTER(Pages), i32, vp, vp, i32, ctypes.POINTER(AppendOpts), vp]),
+        "epq_pages_advance": (i32, [ctypes.POINTER(Pages), vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -652,3 +680,111 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
     if st:
         raise EpqError("epq_verify_tree", st)
     return path, n_accept, next_token, lse
+
+
+# ------------------------------------------------------------------ rotary positions
+def epq_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = EPQ_ROPE_PLAIN, factor: float = 1.0,
+                         context: float = 1.0, low: float | None = None, high: float | None = None):
+    """(float64 [rot_dim / 2] on the host, magnitude): the angles per position and what the cosines and sines are
+    multiplied by; low, high: turns over `context` (None: the kind's usual ones)."""
+    usual = (1.0, 4.0) if kind == EPQ_ROPE_BANDS else (1.0, 32.0)
+    sc = RopeScaling(kind, factor, context, usual[0] if low is None else low, usual[1] if high is None else high)
+    freq, mag = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64), ctypes.c_double()
+    _check("epq_rope_frequencies", load().epq_rope_frequencies(
+        rot_dim, base, ctypes.byref(sc), ctypes.cast(freq.data_ptr(), ctypes.POINTER(ctypes.c_double)),
+        ctypes.byref(mag)))
+    return freq, mag.value
+
+
+class RopeTable:
+    """A rotation (epq_rotation): cosines and sines of positions 0..n_pos-1, float32 [n_pos, rot_dim / 2, 2], for
+    the elements first .. first + rot_dim - 1 of a head.  The further arguments are those of epq_rope_frequencies."""
+
+    def __init__(self, rot_dim: int, n_pos: int, base: float = 10000.0, first: int = 0, interleaved: bool = False,
+                 device="cuda", **scaling):
+        freq, magnitude = epq_rope_frequencies(rot_dim, base, **scaling)
+        freq = freq.to(device)
+        table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
+        _check("epq_rope_table", load().epq_rope_table(freq.data_ptr(), rot_dim, magnitude, n_pos, table.data_ptr(),
+                                                       _queue(None, _place(table))))
+        self._bind(table, first, interleaved)
+
+    @classmethod
+    def over(cls, table: torch.Tensor, first: int = 0, interleaved: bool = False) -> "RopeTable":
+        """A rotation by a table that the caller holds."""
+        self = cls.__new__(cls)
+        self._bind(table, first, interleaved)
+        return self
+
+    def _bind(self, table, first, interleaved):
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError("table must be [n_pos, rot_dim / 2, 2]")
+        self._at = _place(table)
+        _need(table, "table", torch.float32, table.shape, self._at)
+        load()
+        self.table, self.first, self.interleaved = table, first, bool(interleaved)
+        self.n_pos, self.rot_dim = table.shape[0], 2 * table.shape[1]
+        self._r = Rotation(table.data_ptr(), self.n_pos, self.rot_dim, first, int(self.interleaved))
+        self._ref = ctypes.byref(self._r)
+
+
+def epq_rope(x: torch.Tensor, rope: RopeTable, n_heads: int, position: torch.Tensor | None = None,
+             start: torch.Tensor | None = None, mask: torch.Tensor | None = None, n_tok: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x float32 [n_seq, ntok, n_heads*D] (a view of a wider buffer is read in place) -> out, the heads turned by
+    their tokens' positions; out may be x.  position int32 [n_seq, ntok], or start int32 [n_seq] plus the token's
+    index (mask int64 [n_seq, ntok]: plus its ancestors in the tree)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [n_seq, ntok, n_heads * head_dim]")
+    nseq, ntok, width = shape = x.shape
+    at = rope._at
+    if n_heads < 1 or width % n_heads:
+        raise ValueError(f"{width} elements are not {n_heads} heads")
+    x_seq, x_tok = _token_strides(x, "x", shape, at)
+    if out is None:
+        out, y_seq, y_tok = _allocator(stream)(shape, dtype=torch.float32, device=x.device), 0, 0
+    else:
+        y_seq, y_tok = _token_strides(out, "out", shape, at)
+    i32 = torch.int32
+    o = RopeOpts(None if position is None else _need(position, "position", i32, (nseq, ntok), at),
+                 None if start is None else _need(start, "start", i32, (nseq,), at),
+                 None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
+                 None if n_tok is None else _need(n_tok, "n_tok", i32, (nseq,), at), x_tok, x_seq, y_tok, y_seq)
+    st = _lib.epq_rope(rope._ref, x.data_ptr(), out.data_ptr(), nseq, ntok, n_heads, width // n_heads,
+                       ctypes.byref(o), _queue(stream, at))
+    if st:
+        raise EpqError("epq_rope", st)
+    return out
+
+
+# ------------------------------------------------------------------ a prompt's rows
+def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, layer: int, rope: RopeTable | None = None,
+                     position: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                     n_tok: torch.Tensor | None = None, stream=None) -> None:
+    """k, v float32 [n_seq, ntok, n_kv*D] (views of one wider buffer are read in place): the rows are stored behind
+    the committed positions of one layer, the keys turned by `rope` (positions as in epq_rope, start = the lengths)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [n_seq, ntok, n_kv * head_dim]")
+    ntok, nseq, at = k.shape[1], cache.n_seq, cache._at
+    kv = (nseq, ntok, cache.n_kv_heads * cache.head_dim)
+    kv_seq, kv_tok = _token_strides(k, "k", kv, at)
+    if _token_strides(v, "v", kv, at) != (kv_seq, kv_tok):
+        raise ValueError("k and v must have the same strides")
+    if rope is not None and rope._at != at:
+        _elsewhere(rope.table, "rope", at)
+    o = AppendOpts(None if rope is None else ctypes.pointer(rope._r),
+                   None if position is None else _need(position, "position", torch.int32, (nseq, ntok), at),
+                   None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
+                   None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at), kv_tok, kv_seq)
+    st = _lib.epq_pages_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), ntok, ctypes.byref(o),
+                               _queue(stream, at))
+    if st:
+        raise EpqError("epq_pages_append", st)
+
+
+def epq_pages_advance(cache: PagedKVCache, n: torch.Tensor, stream=None) -> None:
+    """Commit n (int32 [n_seq]) appended positions of every sequence."""
+    at = cache._at
+    st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _queue(stream, at))
+    if st:
+        raise EpqError("epq_pages_advance", st)

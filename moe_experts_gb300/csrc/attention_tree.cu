@@ -246,25 +246,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127), codes rint(x /
-// factor) in +-127, 0 for a zero factor) of 4 elements a lane, 8 lanes a block.
-__device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
-  const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
-  float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
-#pragma unroll
-  for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-  const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
-  const float d = __half2float(dh);
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
-    word |= (static_cast<uint32_t>(static_cast<int>(y)) & 0xffu) << (8 * j);
-  }
-  *factor = dh;
-  return word;
-}
-
 // Joins the parts of the items that more than one CTA holds: one warp per
 // (item, row), the parts in the order of their positions.
 template <int kD, int kRows>

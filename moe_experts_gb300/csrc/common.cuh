@@ -27,6 +27,7 @@ enum DeviceError : unsigned {
   DEVERR_DRAIN_WAIT = 3,   // copies still in flight at exit
   DEVERR_RED_WAIT = 4,     // waited too long for the cross-warp reduction
   DEVERR_NO_PAGE = 5,      // a position of a paged cache that has to be read or written has no page
+  DEVERR_NO_ANGLE = 6,     // a token stands at a position that the rotation table does not hold
 };
 
 // ------------------------------------------------------------------ PTX wrappers
