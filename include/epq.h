@@ -692,6 +692,56 @@ epq_status epq_pages_append(const epq_pages *pages, int layer, const float *k, c
  * max_pages * page_size); n int32 [n_seq]. */
 epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n, epq_stream_t stream);
 
+/* ---------------------------------------------------------------- logits
+ * Options of epq_logits_adjust (all-zero: nothing changes).
+ *   penalties   NULL or float32 [n_seq][3]: repetition r > 0, frequency f,
+ *               presence p
+ *   history     NULL or int32 [n_seq][max_history]: a sequence's tokens before
+ *               the drafted ones, of which history_len (NULL or int32 [n_seq];
+ *               NULL: all) are used, and the first prompt_len (NULL or int32
+ *               [n_seq]; NULL: none) are its prompt
+ *   tokens      NULL or int32 [n_seq][ntok]: the drafted tokens (token 0 is the
+ *               last committed one)
+ *   mask        NULL or uint64 [n_seq][ntok] (epq_tree_mask): of `tokens`, row i
+ *               comes after those that entry i names (NULL: 0..i); ntok 1..64
+ *               where tokens are given
+ *   n_tok       NULL or int32 [n_seq]: rows of each sequence (0..ntok); the
+ *               others are copied unchanged, and their tokens are not counted
+ *   bias_ids, bias  NULL or int32, float32 [n_seq][n_bias]: added to the logit
+ *               of a token (of entries for the same one the last counts)
+ *   allowed     NULL or uint32 [n_seq][ntok][ceil(vocab/32)]: bit v % 32 of word
+ *               v / 32 says whether row i may take token v
+ *   ld, out_ld  floats between rows of logits / out (0 = vocab)
+ * Ids outside the vocabulary are ignored. */
+typedef struct {
+  const float *penalties;
+  const int32_t *history, *history_len, *prompt_len;
+  int max_history;
+  const int32_t *tokens;
+  const uint64_t *mask;
+  const int32_t *n_tok;
+  const int32_t *bias_ids;
+  const float *bias;
+  int n_bias;
+  const uint32_t *allowed;
+  int64_t ld, out_ld;
+} epq_logits_opts;
+
+/* epq_logits_adjust: the target's logits before epq_verify_tree.  For token v
+ * of row i with n(v) = its occurrences among the row's generated tokens (the
+ * history behind the prompt, and the drafted tokens before the row):
+ *   l += bias(v)
+ *   where v occurs in the prompt or n > 0:  l = l > 0 ? l / r : l * r
+ *   where n > 0:                            l -= f * n + p
+ *   where v is not allowed:                 l = -inf   (NaN included)
+ * in float32, each operation rounded.  A row that allows nothing is all -inf
+ * (epq_verify_tree wants a finite logit: the caller ends such a branch).
+ *   logits, out  float32 [n_seq][ntok][vocab]; out may equal logits (with the
+ *                same stride), else they do not overlap
+ * vocab 1..2^24, n_seq * ntok < 2^24, max_history, n_bias 0..2^24.  One launch. */
+epq_status epq_logits_adjust(const float *logits, int64_t vocab, int n_seq, int ntok, const epq_logits_opts *opts,
+                             float *out, epq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -104,6 +104,14 @@ class AppendOpts(ctypes.Structure):
                 ("n_tok", ctypes.c_void_p), ("kv_ld", ctypes.c_int64), ("kv_seq_ld", ctypes.c_int64)]
 
 
+class LogitsOpts(ctypes.Structure):
+    _fields_ = [("penalties", ctypes.c_void_p), ("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("max_history", ctypes.c_int), ("tokens", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("n_tok", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("n_bias", ctypes.c_int), ("allowed", ctypes.c_void_p),
+                ("ld", ctypes.c_int64), ("out_ld", ctypes.c_int64)]
+
+
 EPQ_MOE_ROUTE, EPQ_MOE_GATE_UP, EPQ_MOE_DOWN = 1, 2, 4
 EPQ_ROPE_PLAIN, EPQ_ROPE_LINEAR, EPQ_ROPE_PARTS, EPQ_ROPE_BANDS = 0, 1, 2, 3
 
@@ -164,6 +172,7 @@ def load(path: str | None = None):
         "epq_rope_table": (i32, [vp, i32, ctypes.c_double, i64, vp, vp]),
         "epq_rope": (i32, [ctypes.POINTER(Rotation), vp, vp, i32, i32, i32, i32, ctypes.POINTER(RopeOpts), vp]),
         "epq_pages_append": (i32, [ctypes.POINTER(Pages), i32, vp, vp, i32, ctypes.POINTER(AppendOpts), vp]),
+        "epq_logits_adjust": (i32, [vp, i64, i32, i32, ctypes.POINTER(LogitsOpts), vp, vp]),
         "epq_pages_advance": (i32, [ctypes.POINTER(Pages), vp, vp]),
     }
     for name, (res, args) in sig.items():
@@ -788,3 +797,45 @@ def epq_pages_advance(cache: PagedKVCache, n: torch.Tensor, stream=None) -> None
     st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _queue(stream, at))
     if st:
         raise EpqError("epq_pages_advance", st)
+
+
+# ------------------------------------------------------------------ logits
+def epq_logits_adjust(logits: torch.Tensor, penalties: torch.Tensor | None = None, history: torch.Tensor | None = None,
+                      history_len: torch.Tensor | None = None, prompt_len: torch.Tensor | None = None,
+                      tokens: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                      n_tok: torch.Tensor | None = None, bias_ids: torch.Tensor | None = None,
+                      bias: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """logits float32 [n_seq, ntok, vocab] -> out (may be logits): biases (bias_ids int32, bias float32 [n_seq,
+    n_bias]), penalties (float32 [n_seq, 3]: repetition, frequency, presence) for the tokens of history (int32
+    [n_seq, max_history]; history_len, prompt_len int32 [n_seq]) and of tokens (int32 [n_seq, ntok]; mask int64
+    [n_seq, ntok]: a row's path in the tree), and -inf for what allowed (int32 [n_seq, ntok, ceil(vocab / 32)], bits)
+    leaves out."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [n_seq, ntok, vocab]")
+    full = logits.shape
+    nseq, ntok, vocab = full
+    at, i32, f32 = _place(logits), torch.int32, torch.float32
+    each, tree = (nseq,), (nseq, ntok)
+    if bias_ids is not None and (bias is None or bias_ids.dim() != 2) or bias_ids is None and bias is not None:
+        raise ValueError("bias_ids and bias must be [n_seq, n_bias] both")
+    if history is not None and history.dim() != 2:
+        raise ValueError("history must be [n_seq, max_history]")
+    nh, nb = 0 if history is None else history.shape[1], 0 if bias is None else bias_ids.shape[1]
+    src = _need(logits, "logits", f32, full, at)
+    out, dst = _result(out, "out", f32, full, at, _allocator(stream), logits.device)
+    o = LogitsOpts(None if penalties is None else _need(penalties, "penalties", f32, (nseq, 3), at),
+                   None if history is None else _need(history, "history", i32, (nseq, nh), at),
+                   None if history_len is None else _need(history_len, "history_len", i32, each, at),
+                   None if prompt_len is None else _need(prompt_len, "prompt_len", i32, each, at), nh,
+                   None if tokens is None else _need(tokens, "tokens", i32, tree, at),
+                   None if mask is None else _need(mask, "mask", torch.int64, tree, at),
+                   None if n_tok is None else _need(n_tok, "n_tok", i32, each, at),
+                   None if bias_ids is None else _need(bias_ids, "bias_ids", i32, (nseq, nb), at),
+                   None if bias is None else _need(bias, "bias", f32, (nseq, nb), at), nb,
+                   None if allowed is None else _need(allowed, "allowed", i32, (nseq, ntok, (vocab + 31) // 32), at),
+                   0, 0)
+    st = load().epq_logits_adjust(src, vocab, nseq, ntok, ctypes.byref(o), dst, _queue(stream, at))
+    if st:
+        raise EpqError("epq_logits_adjust", st)
+    return out

@@ -144,7 +144,9 @@ extern "C" epq_status epq_pages_append(const epq_pages *pages, int layer, const 
   p.ld = o.kv_ld ? o.kv_ld : static_cast<int64_t>(p.v.n_kv) * p.v.D;
   p.seq_ld = o.kv_seq_ld ? o.kv_seq_ld : ntok * p.ld;
   if (o.kv_ld < 0 || o.kv_seq_ld < 0) return EPQ_ERR_ARG;
-  if (!aligned16(k) || !aligned16(v) || p.ld % 4 || p.seq_ld % 4) return EPQ_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || p.ld % 4 || p.seq_ld % 4 || !aligned_to(4, o.position, o.n_tok) ||
+      !aligned_to(8, o.mask))
+    return EPQ_ERR_ALIGN;
   p.p = {o.position, p.v.length, o.mask, o.n_tok, ntok};
   p.k = k, p.x = v, p.layer = layer;
   p.rows = static_cast<int64_t>(p.v.n_seq) * ntok * p.v.n_kv;
@@ -165,6 +167,7 @@ extern "C" epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n
   const epq_status st = pages_view(pages, &v);
   if (st != EPQ_OK) return st;
   if (!n) return EPQ_ERR_ARG;
+  if (!aligned_to(4, n)) return EPQ_ERR_ALIGN;
   DeviceInfo dev;
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const cudaError_t e =

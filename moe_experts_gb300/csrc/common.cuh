@@ -280,6 +280,12 @@ inline epq_status check_launch() {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether all of the pointers (null ones too) are multiples of n, a power of two.
+template <typename... P>
+bool aligned_to(uintptr_t n, const P *...p) {
+  return (((... | reinterpret_cast<uintptr_t>(p))) & (n - 1)) == 0;
+}
+
 // Launch with the programmatic-stream-serialization attribute so that the
 // kernel may start while the previous kernel on the stream drains; the
 // kernel itself calls pdl_wait() before reading data produced upstream.

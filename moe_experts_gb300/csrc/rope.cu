@@ -220,7 +220,7 @@ extern "C" epq_status epq_rope(const epq_rotation *rotation, const float *x, flo
   if ((ntok > 1 && p.y_ld < width) || (n_seq > 1 && p.y_seq < width) || o.x_ld < 0 || o.y_ld < 0 || o.x_seq_ld < 0 || o.y_seq_ld < 0 ||
       (x == y && (p.x_ld != p.y_ld || p.x_seq != p.y_seq)))
     return EPQ_ERR_ARG;
-  if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 3) return EPQ_ERR_ALIGN;
+  if (!aligned_to(4, x, y, o.position, o.start, o.n_tok) || !aligned_to(8, o.mask)) return EPQ_ERR_ALIGN;
   p.p = {o.position, o.start, o.mask, o.n_tok, ntok};
   p.heads = n_heads, p.dim = head_dim;
   const bool four = aligned16(x) && aligned16(y) && head_dim % 4 == 0 && p.x_ld % 4 == 0 && p.y_ld % 4 == 0 &&
