@@ -692,6 +692,42 @@ epq_status epq_pages_append(const epq_pages *pages, int layer, const float *k, c
  * max_pages * page_size); n int32 [n_seq]. */
 epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n, epq_stream_t stream);
 
+/* Options of epq_attention_prompt (all-zero: contiguous q, ntok tokens in every
+ * sequence, no window).
+ *   n_tok    NULL or int32 [n_seq]: tokens of each sequence (0..ntok; the
+ *            others' output is 0)
+ *   window   0, or how many positions a token attends to, its own included
+ *   q_ld, q_seq_ld  floats between tokens / sequences of q (0 = contiguous);
+ *            multiples of 4 */
+typedef struct {
+  const int32_t *n_tok;
+  int window;
+  int64_t q_ld, q_seq_ld;
+} epq_attention_prompt_opts;
+
+/* Workspace bytes of epq_attention_prompt (0 on bad sizes).  Host-only. */
+size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads, int ntok);
+
+/* epq_attention_prompt: causal attention of any number of appended rows.
+ *   q    float32 [n_seq][ntok][n_heads][head_dim], rotated already
+ *   s_ij = scale * q_i . k_j over the positions j <= length + i (and j >
+ *   length + i - window) of the cache, which holds the tokens' own rows
+ *   (epq_pages_append) behind the committed ones; out_i = sum_j softmax(s_i)_j
+ *   v_j, 0 for a token that sees no position.  Query head h reads key/value
+ *   head h / (n_heads / n_kv_heads).  A position without a page is left out and
+ *   recorded (epq_device_error code 5).
+ *   out  float32 [n_seq][ntok][n_heads][head_dim]
+ *   ws, ws_bytes  device scratch of epq_attention_prompt_workspace_bytes(),
+ *        16-byte aligned, needs no initialisation; calls that share it must be
+ *        ordered on one stream.
+ * Requirements: n_seq * ntok < 2^24, n_heads a multiple of n_kv_heads, at most
+ * 16 heads per key/value head, scale > 0 and finite, finite q.  A key or value
+ * row with a factor that is not finite makes the outputs of the tokens that
+ * attend to it NaN, in the heads that read it, and changes no other output. */
+epq_status epq_attention_prompt(const epq_pages *pages, int layer, const float *q, int n_heads, int ntok, float scale,
+                                const epq_attention_prompt_opts *opts, float *out, void *ws, size_t ws_bytes,
+                                epq_stream_t stream);
+
 /* ---------------------------------------------------------------- logits
  * Options of epq_logits_adjust (all-zero: nothing changes).
  *   penalties   NULL or float32 [n_seq][3]: repetition r > 0, frequency f,

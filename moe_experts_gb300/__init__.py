@@ -12,6 +12,7 @@ from ._lib import (  # noqa: F401
     PagedKVCache, epq_pages_truncate, epq_pages_fork, epq_pages_reserve, epq_pages_compact,
     epq_tree_mask, epq_attention_tree, epq_attention_tree_workspace, epq_verify_tree, epq_verify_tree_workspace,
     EPQ_ROPE_PLAIN, EPQ_ROPE_LINEAR, EPQ_ROPE_PARTS, EPQ_ROPE_BANDS, epq_rope_frequencies, RopeTable, epq_rope,
-    epq_pages_append, epq_pages_advance, epq_logits_adjust,
+    epq_pages_append, epq_pages_advance, epq_attention_prompt, epq_attention_prompt_workspace,
+    epq_logits_adjust,
     MoELayer, epq_moe_workspace_bytes, epq_moe_forward, epq_moe_forward_noalloc, EPQ_MOE_ROUTE, EPQ_MOE_GATE_UP, EPQ_MOE_DOWN,
 )

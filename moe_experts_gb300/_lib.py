@@ -104,6 +104,11 @@ class AppendOpts(ctypes.Structure):
                 ("n_tok", ctypes.c_void_p), ("kv_ld", ctypes.c_int64), ("kv_seq_ld", ctypes.c_int64)]
 
 
+class PromptOpts(ctypes.Structure):
+    _fields_ = [("n_tok", ctypes.c_void_p), ("window", ctypes.c_int), ("q_ld", ctypes.c_int64),
+                ("q_seq_ld", ctypes.c_int64)]
+
+
 class LogitsOpts(ctypes.Structure):
     _fields_ = [("penalties", ctypes.c_void_p), ("history", ctypes.c_void_p), ("history_len", ctypes.c_void_p),
                 ("prompt_len", ctypes.c_void_p), ("max_history", ctypes.c_int), ("tokens", ctypes.c_void_p),
@@ -172,6 +177,9 @@ def load(path: str | None = None):
         "epq_rope_table": (i32, [vp, i32, ctypes.c_double, i64, vp, vp]),
         "epq_rope": (i32, [ctypes.POINTER(Rotation), vp, vp, i32, i32, i32, i32, ctypes.POINTER(RopeOpts), vp]),
         "epq_pages_append": (i32, [ctypes.POINTER(Pages), i32, vp, vp, i32, ctypes.POINTER(AppendOpts), vp]),
+        "epq_attention_prompt_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Pages), i32, i32]),
+        "epq_attention_prompt": (i32, [ctypes.POINTER(Pages), i32, vp, i32, i32, f32, ctypes.POINTER(PromptOpts), vp,
+                                       vp, ctypes.c_size_t, vp]),
         "epq_logits_adjust": (i32, [vp, i64, i32, i32, ctypes.POINTER(LogitsOpts), vp, vp]),
         "epq_pages_advance": (i32, [ctypes.POINTER(Pages), vp, vp]),
     }
@@ -797,6 +805,37 @@ def epq_pages_advance(cache: PagedKVCache, n: torch.Tensor, stream=None) -> None
     st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _queue(stream, at))
     if st:
         raise EpqError("epq_pages_advance", st)
+
+
+def epq_attention_prompt_workspace(cache: PagedKVCache, n_heads: int, ntok: int, stream=None) -> torch.Tensor:
+    """A workspace for epq_attention_prompt (on `stream`), to be kept between calls."""
+    n = int(load().epq_attention_prompt_workspace_bytes(cache._ref, n_heads, ntok))
+    if n == 0:
+        raise ValueError("sizes of the prompt attention not supported")
+    return _allocator(stream)(n, dtype=torch.uint8, device=cache.device)
+
+
+def epq_attention_prompt(q: torch.Tensor, cache: PagedKVCache, layer: int, n_heads: int, scale: float, window: int = 0,
+                         n_tok: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [n_seq, ntok, n_heads*D] (float32; a view of a wider buffer is read in place) -> out [n_seq, ntok, n_heads*D]:
+    token i of a sequence attends to its positions 0..length + i, the last `window` of them if that is not 0; the
+    tokens' own rows have been stored by epq_pages_append."""
+    if q.dim() != 3:
+        raise ValueError("q must be [n_seq, ntok, n_heads * head_dim]")
+    ntok, at = q.shape[1], cache._at
+    shape = (cache.n_seq, ntok, n_heads * cache.head_dim)
+    q_seq, q_tok = _token_strides(q, "q", shape, at)
+    out, out_at = _result(out, "out", torch.float32, shape, at, _allocator(stream), cache.device)
+    if workspace is None:
+        workspace = epq_attention_prompt_workspace(cache, n_heads, ntok, stream)
+    o = PromptOpts(None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at), window, q_tok,
+                   q_seq)
+    st = _lib.epq_attention_prompt(cache._ref, layer, q.data_ptr(), n_heads, ntok, scale, ctypes.byref(o), out_at,
+                                   *_scratch(workspace, at), _queue(stream, at))
+    if st:
+        raise EpqError("epq_attention_prompt", st)
+    return out
 
 
 # ------------------------------------------------------------------ logits
