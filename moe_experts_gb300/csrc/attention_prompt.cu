@@ -5,128 +5,824 @@
 //
 // over the positions j <= length + i.  The rows of one (sequence, key/value
 // head) are its tokens times its `group` query heads (row r: token r / group,
-// head r % group).  One pass over the positions in tiles of 32, dequantized
-// into shared memory, with a running maximum and sum per row; a warp has two
-// rows, a lane a position of the scores and D/32 columns of the output.
+// head r % group); an item is 128 of them and 128 columns of the output.
+//
+// One pass over the positions in tiles of 128 (64 for heads of 256), both
+// products on the tensor core (tcgen05, fp16 operands, float32 sums) without
+// giving up float32 accuracy: each operand is two fp16 parts, a = a1 + a2 with
+// a1 the 11 leading bits, and a product is a1 b1 + a1 b2 + a2 b1 (what is left
+// out is 2^-22 of it).  Powers of two keep the parts in fp16's range:
+//   queries  a row's largest element in [2^14, 2^15);
+//   keys     a tile's largest factor in [2^7, 2^8): code * factor < 2^15, its
+//            two parts exact;
+//   values   the same for each block of 32 columns of a tile;
+//   weights  2^15 at the row's maximum.
+// Halves are multiples of 2^-24, which is the floor: a weight is off by up to
+// 2^-39 of the one at the maximum, whatever it is, and a factor below 2^-21 of
+// its tile's largest by 2^-32 of that.
+// The sum of a tile is read from tensor memory and added to the output's
+// registers, scaled by the change of the row's maximum, so no sum in tensor
+// memory outlives a tile.
+//
+// Roles of a CTA's warps, each a step ahead of the next:
+//   scan     (2 warps) pages, factors' maxima, what is missing, 4 tiles ahead
+//   keys     (4) codes to two fp16 parts in swizzled shared memory, 2 tiles
+//   values   (4) the same, one tile
+//   products (1) issues them: scores of tile t + 1, then values of tile t, so
+//            that the tensor core works on one while the weights of the other
+//            are made
+//   weights  (4) one row a thread: maximum, exponentials, two parts, written
+//            over the scores in tensor memory
+//   output   (4) one row a thread: 128 columns in registers
+// Work: the tiles of all items in a row, cut into equal shares, one per CTA.
+// An item counts kExtra tiles more than it has.  A CTA's part of an item that
+// it does not hold whole goes to the workspace (maximum, sum, unnormalised
+// output), and a second launch joins the parts.
 #include <algorithm>
 #include <cmath>
 
 #include "pages.cuh"
+#include "tcgen05.cuh"
 
 namespace epq {
 namespace {
 
-constexpr int kTile = 32, kWarps = 8, kWarpRows = 2, kRows = kWarps * kWarpRows;
+constexpr int kRows = 128;     // rows of an item
+constexpr int kCols = 128;     // output columns of an item
+constexpr int kMaxCtas = 152;  // one per SM of a GB300
+constexpr int kMaxGroupPrompt = 16;
+constexpr int kExtra = 2;
+constexpr int kAhead = 4;  // tiles that the scan may be ahead of the output
+constexpr int kJoinWarps = 8;
+constexpr int kPartLd = kCols + 4;
+
+// Warps: 0-3 weights, 4-7 output, 8-11 keys, 12-15 values, 16 products, 17-18
+// scan, 19 unused rows.  Registers of each group of four warps: the launch has
+// 5 * 128 threads * 96, and 5 * 96 = 104 + 168 + 72 + 72 + 64.
+constexpr int kThreads = 640;
+constexpr int kRegsWeights = 104, kRegsOutput = 168, kRegsOperand = 72, kRegsRest = 64;
+constexpr int kRegsLaunch = 96;
+static_assert(kRegsWeights + kRegsOutput + 2 * kRegsOperand + kRegsRest <= 5 * kRegsLaunch,
+              "a split above the launch's total waits forever");
+
+struct Part {  // what a CTA left in the workspace: tiles a..b-1 of an item of `tiles` (0: nothing)
+  int s, rt, y, a, b, tiles, pad[2];
+};
 
 struct PromptParams {
   PagesView v;
   const float *q;
   const int32_t *n_tok;
   int64_t q_ld, q_seq_ld;
-  int layer, n_heads, group, ntok, window, tiles;
+  int layer, n_heads, group, ntok, window;
   float scale;
   float *out;
+  Part *notes;   // workspace: [2 per CTA]
+  float *parts;  // workspace: [2 per CTA][kRows][kPartLd]
   unsigned *err;
 };
 
+// Sizes that follow from the head.
 template <int kD>
-__global__ void __launch_bounds__(32 * kWarps) prompt_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int kLd = kD + 4;
-  extern __shared__ __align__(16) float smem[];
-  float *ks = smem, *vs = ks + kTile * kLd, *qs = vs + kTile * kLd;  // qs [kRows][kD]
-  __shared__ float lost[kTile];  // NaN: a factor of the position is not finite; -inf: it has no page
+struct Shape {
+  static constexpr int kPos = kD == 128 ? 128 : 64;  // positions of a tile
+  static constexpr int kSplit = kD / kCols;          // items that share a row tile's scores' rows
+  static constexpr uint32_t kKPart = kPos * kD * 2;  // bytes of one part of a tile's keys
+  static constexpr uint32_t kVPart = kPos * kCols * 2;  // and of its values
+  static constexpr uint32_t kKBytes = 2 * 2 * kKPart, kVBytes = 2 * kVPart;
+  // columns of tensor memory
+  static constexpr uint32_t kQ = 0, kS = kD, kT = kD + 2 * kPos;
+  static_assert(kT + kCols <= 512, "");
+};
+
+// What the scan says of a tile.
+struct Entry {
+  long long off[128];  // byte offset of a position's key row in the pool, -1: nothing to read
+  float lost[128];     // 0; NaN: a factor is not finite; -inf: no page
+  int kmax[2];         // largest factor of the keys (bits of the half), one per scanning warp
+  int vmax[2][4];      // of the values, by column block
+  int any[2];          // whether some `lost` matters
+};
+
+struct Control {
+  uint64_t k_full[2], v_full, s_full[2], p_full[2], t_full, t_free, q_full, c_full[kAhead], fin_full, fin_empty,
+      scan_full[kAhead], entry_free[kAhead];
+  uint32_t tmem;
+  long long begin, end;  // the CTA's share
+  int s, rt, y, tile;    // where it begins
+  long long sums[kThreads / 32];
+  int pair0[kMaxSeq + 1];  // row tiles of the sequences before each
+  int2 seq[kMaxSeq];       // length, tokens
+  Entry entry[kAhead];
+  float corr[kAhead][kRows];
+  float off[kRows], den[kRows];
+};
+
+__device__ __forceinline__ int row_tiles(const PromptParams &p, int n) { return (n * p.group + kRows - 1) / kRows; }
+
+// Row tile rt of a sequence: its tokens, and the positions that any of them sees.
+struct Span {
+  int t0, t1, end, first, tiles;  // first: the first tile's index; tiles: how many
+};
+
+template <int kD>
+__device__ __forceinline__ Span span_of(const PromptParams &p, int len, int n, int rt) {
+  constexpr int kPos = Shape<kD>::kPos;
+  Span x;
+  x.t0 = rt * kRows / p.group;
+  x.t1 = (min((rt + 1) * kRows, n * p.group) - 1) / p.group;
+  x.end = len + x.t1 + 1;
+  const int begin = p.window ? max(0, len + x.t0 - p.window + 1) : 0;
+  x.first = begin / kPos;
+  x.tiles = (x.end + kPos - 1) / kPos - x.first;
+  return x;
+}
+
+// Inclusive sum over the CTA.
+__device__ __forceinline__ long long scan_sum(long long x, long long *sums, long long *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  long long all = 0, base = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) base = all;
+    all += sums[w];
+  }
+  *total = all;
+  return base + x;
+}
+
+// The CTA's share of the tiles and where it begins; ends with a CTA barrier.
+template <int kD>
+__device__ __forceinline__ void find_work(const PromptParams &p, Control &c) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int s = tid; s < p.v.n_seq; s += kThreads)
+    c.seq[s] = make_int2(seq_length(p.v, s), p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok);
+  __syncthreads();
+  if (tid < 32) {
+    int run = 0;
+    for (int s0 = 0; s0 < p.v.n_seq; s0 += 32) {
+      int x = s0 + lane < p.v.n_seq ? row_tiles(p, c.seq[s0 + lane].y) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (s0 + lane < p.v.n_seq) c.pair0[s0 + lane + 1] = run + x;
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) c.pair0[0] = 0, c.begin = c.end = 0;
+  }
+  __syncthreads();
+  const int pairs = c.pair0[p.v.n_seq], heads = p.v.n_kv * Shape<kD>::kSplit;
+  const auto find = [&](int pair) {  // the last sequence with pair0 <= pair (empty ones are passed over)
+    int lo = 0, hi = p.v.n_seq - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (c.pair0[mid] <= pair) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  const auto units = [&](int pair, int s) {
+    return span_of<kD>(p, c.seq[s].x, c.seq[s].y, pair - c.pair0[s]).tiles + kExtra;
+  };
+  long long mine = 0, total;
+  for (int k = tid; k < pairs; k += kThreads) mine += units(k, find(k));
+  scan_sum(mine, c.sums, &total);
+  total *= heads;
+  const long long ctas = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x < ctas) {
+    const long long share = total / ctas, rest = total % ctas, b = blockIdx.x;
+    const long long begin = b * share + (b < rest ? b : rest), end = begin + share + (b < rest);
+    long long run = 0;
+    for (int k0 = 0; run <= begin; k0 += kThreads) {
+      const int k = k0 + tid, s = k < pairs ? find(k) : 0;
+      const long long each = k < pairs ? units(k, s) : 0;
+      long long all;
+      const long long upto = run + heads * scan_sum(each, c.sums, &all), from = upto - heads * each;
+      run += heads * all;
+      if (from <= begin && begin < upto) {
+        c.s = s, c.rt = k - c.pair0[s];
+        c.y = static_cast<int>((begin - from) / each);
+        c.tile = static_cast<int>((begin - from) % each);
+        c.begin = begin, c.end = end;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// The items of a CTA's share, one after the other; every role walks alone.
+template <int kD>
+struct Walk {
+  long long left;
+  int s, rt, y, tile;  // where the next item begins
+  // the item: tiles a..b-1 of its span; how many items and tiles came before it
+  int item_s, item_rt, item_y, len, n, a, b, items, before;
+  bool first;  // the share begins in it (or with it)
+  Span span;
+  __device__ explicit Walk(const Control &c)
+      : left(c.end - c.begin), s(c.s), rt(c.rt), y(c.y), tile(c.tile), a(0), b(0), items(-1), before(0), first(false) {}
+  __device__ bool next(const PromptParams &p, const Control &c) {
+    before += b - a;
+    bool begins = items < 0;
+    ++items;
+    while (left > 0) {
+      len = c.seq[s].x, n = c.seq[s].y;
+      if (rt >= row_tiles(p, n)) {
+        ++s, rt = 0;
+        continue;
+      }
+      span = span_of<kD>(p, len, n, rt);
+      const long long take = min(left, static_cast<long long>(span.tiles + kExtra - tile));
+      a = tile, b = min(tile + static_cast<int>(take), span.tiles);
+      item_s = s, item_rt = rt, item_y = y;
+      left -= take;
+      tile = 0;
+      if (++y == p.v.n_kv * Shape<kD>::kSplit) y = 0, ++rt;
+      if (a < b) {
+        first = begins;
+        return true;
+      }
+      begins = false;
+    }
+    return false;
+  }
+  __device__ int head() const { return item_y / Shape<kD>::kSplit; }
+  __device__ int split() const { return item_y % Shape<kD>::kSplit; }
+  __device__ bool whole() const { return a == 0 && b == span.tiles; }
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
+// x, y as two fp16 parts each: the 11 leading bits, and the rest rounded.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &first, uint32_t &rest) {
+  const float a = __uint_as_float(__float_as_uint(x) & 0xffffe000u);
+  const float b = __uint_as_float(__float_as_uint(y) & 0xffffe000u);
+  first = pack_half2(a, b);
+  rest = pack_half2(x - a, y - b);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Exponent of a finite half's bits (of 0: 0).
+__device__ __forceinline__ int half_exponent(int bits) {
+  return bits ? static_cast<int>(__float_as_uint(half_bits_to_float(bits)) >> 23) - 127 : 0;
+}
+
+// ------------------------------------------------------------------ scan
+template <int kD>
+__device__ void scan_role(const PromptParams &p, Control &c) {
+  constexpr int kPos = Shape<kD>::kPos, kMine = kPos / 64, kWords = kD / 128;
+  const int t = threadIdx.x - 17 * 32, lane = t & 31, warp = t >> 5;
+  Walk<kD> w(c);
+  while (w.next(p, c)) {
+    const int h = w.head(), split = w.split();
+    for (int k = w.a; k < w.b; ++k) {
+      const int g = w.before + k - w.a;
+      Entry &e = c.entry[g % kAhead];
+      const int p0 = (w.span.first + k) * kPos;
+      uint2 kf[kMine][kWords], vf[kMine][kWords];
+      long long off[kMine];
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int pos = p0 + t + 64 * m;
+        const int page = pos < w.span.end ? seq_page(p.v, w.item_s, pos / p.v.P) : -1;
+        off[m] = page < 0 ? -1 : page_row(p.v, p.layer, page, h, 0, pos % p.v.P) - p.v.pool;
+      }
+#pragma unroll
+      for (int m = 0; m < kMine; ++m)
+#pragma unroll
+        for (int x = 0; x < kWords; ++x) {
+          const uint8_t *row = p.v.pool + off[m];
+          kf[m][x] = off[m] < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(row + 8 * x);
+          vf[m][x] = off[m] < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(row + p.v.P * p.v.row + 8 * x);
+        }
+      if (g >= kAhead && !mbar_wait(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
+      unsigned kmax = 0, vmax[4] = {};
+      bool any = false;
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int row = t + 64 * m;
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < kWords; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned a = ((i & 2 ? kf[m][x].y : kf[m][x].x) >> (16 * (i & 1))) & 0x7fffu;
+            const unsigned b = ((i & 2 ? vf[m][x].y : vf[m][x].x) >> (16 * (i & 1))) & 0x7fffu;
+            bad |= a >= 0x7c00u || b >= 0x7c00u;
+            if (a < 0x7c00u) kmax = max(kmax, a);
+            if (b < 0x7c00u && (kWords == 1 || x == split)) vmax[i] = max(vmax[i], b);
+          }
+        const bool used = p0 + row < w.span.end;
+        if (used && off[m] < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(w.item_s));
+        e.off[row] = off[m];
+        e.lost[row] = off[m] < 0 ? -INFINITY : bad ? __int_as_float(0x7fffffff) : 0.0f;
+        any |= used && (off[m] < 0 || bad);
+      }
+      kmax = __reduce_max_sync(0xffffffffu, kmax);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vmax[i] = __reduce_max_sync(0xffffffffu, vmax[i]);
+      any = __any_sync(0xffffffffu, any);
+      if (lane == 0) {
+        e.kmax[warp] = kmax;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e.vmax[warp][i] = vmax[i];
+        e.any[warp] = any;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.scan_full[g % kAhead]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ operands
+// Eight codes times a factor as fp16: the rounded products, and what the
+// rounding lost (exact: a product has 18 bits).  A byte u = code + 128 under
+// the byte 0x64 is the half 1024 + u.
+__device__ __forceinline__ void convert8(uint2 x, __half factor, uint4 &first, uint4 &rest) {
+  const __half2 f = __half2half2(factor), bias = __half2half2(__ushort_as_half(0x6480));
+  uint32_t *a = &first.x, *b = &rest.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = (i < 2 ? x.x : x.y) ^ 0x80808080u;
+    const __half2 code = __hsub2(as_half2(__byte_perm(u, 0x64646464u, i & 1 ? 0x4342 : 0x4140)), bias);
+    const __half2 y = __hmul2(code, f);
+    a[i] = as_bits(y);
+    b[i] = as_bits(__hfma2(code, f, __hneg2(y)));
+  }
+}
+
+// A tile's rows to shared memory, by 128 threads: kWidth columns of `plane`
+// from column `col` on, block b's factors times mul[b].  `ready` is asked
+// before the first write.
+template <int kPos, int kWidth, int kBlocks, typename Ready>
+__device__ __forceinline__ bool operand(const PromptParams &p, const Entry &e, int plane, int col,
+                                        const float (&mul)[kBlocks], uint32_t part, uint32_t smem, Ready ready) {
+  constexpr int kChunks = kWidth / 8, kStep = 128 / kChunks, kSteps = kPos / kStep, kBatch = 8;
+  static_assert(kSteps % kBatch == 0, "");
+  const int t = threadIdx.x & 127, chunk = t % kChunks, r0 = t / kChunks;
+  const uint8_t *base = p.v.pool + static_cast<int64_t>(plane) * p.v.P * p.v.row;
+  const int codes = p.v.D / 16 + col + 8 * chunk, factor = 2 * (col / 32 + chunk / 4);
+  float m = mul[0];
+#pragma unroll
+  for (int b = 1; b < kBlocks; ++b) m = chunk / 4 == b ? mul[b] : m;
+  const uint32_t at = smem + (chunk / 8) * (kPos * 128);
+  uint2 x[kBatch];
+  unsigned short f[kBatch];
+  const auto load = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long off = e.off[r0 + kStep * (k + i)];
+      x[i] = off < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(base + off + codes);
+      f[i] = off < 0 ? 0 : *reinterpret_cast<const unsigned short *>(base + off + factor);
+    }
+  };
+  load(0);
+  if (!ready()) return false;
+#pragma unroll
+  for (int k = 0; k < kSteps; k += kBatch) {
+    uint2 y[kBatch];
+    __half g[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      y[i] = x[i];
+      const unsigned short h = (f[i] & 0x7fffu) < 0x7c00u ? f[i] : 0;  // `lost` tells of the others
+      g[i] = __float2half_rn(__half2float(__ushort_as_half(h)) * m);
+    }
+    if (k + kBatch < kSteps) load(k + kBatch);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = r0 + kStep * (k + i);
+      uint4 a, b;
+      convert8(y[i], g[i], a, b);
+      const uint32_t to = at + row * 128 + (((chunk % 8) ^ (row % 8)) * 16);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w)
+                   : "memory");
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + part), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                   : "memory");
+    }
+  }
+  fence_shared_async();
+  return true;
+}
+
+template <int kD>
+__device__ void keys_role(const PromptParams &p, Control &c, uint32_t smem) {
+  using S = Shape<kD>;
+  Walk<kD> w(c);
+  while (w.next(p, c))
+    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
+      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      const Entry &e = c.entry[g % kAhead];
+      const float mul[1] = {exp2i(7 - half_exponent(max(e.kmax[0], e.kmax[1])))};
+      // the scores of two tiles before have been computed: their keys' place is free
+      const bool ok = operand<S::kPos, kD, 1>(p, e, 0, 0, mul, S::kKPart, smem + (g & 1) * 2 * S::kKPart, [&] {
+        return g < 2 || mbar_wait(&c.s_full[g & 1], ((g - 2) >> 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
+      });
+      if (!ok) return;
+      mbar_arrive(&c.k_full[g & 1]);
+    }
+}
+
+template <int kD>
+__device__ void values_role(const PromptParams &p, Control &c, uint32_t smem) {
+  using S = Shape<kD>;
+  Walk<kD> w(c);
+  while (w.next(p, c)) {
+    const int col = w.split() * kCols;
+    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
+      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      const Entry &e = c.entry[g % kAhead];
+      float mul[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) mul[b] = exp2i(7 - half_exponent(max(e.vmax[0][b], e.vmax[1][b])));
+      const bool ok = operand<S::kPos, kCols, 4>(p, e, 1, col, mul, S::kVPart, smem + S::kKBytes, [&] {
+        return g < 1 || mbar_wait(&c.t_full, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
+      });
+      if (!ok) return;
+      mbar_arrive(&c.v_full);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ products
+// One thread.  8 columns of tensor memory are 16 elements of a query's first
+// parts, D/2 columns on are the second ones; of the weights the first and
+// second parts of 16 positions follow one another.
+template <int kD>
+__device__ void products_role(const PromptParams &p, Control &c, uint32_t smem) {
+  using S = Shape<kD>;
+  constexpr int kPos = S::kPos;
+  constexpr uint32_t kScores = mma_f16_shape<kPos, false>(), kValues = mma_f16_shape<kCols, true>();
+  const uint32_t tm = c.tmem;
+  Walk<kD> w(c);
+  while (w.next(p, c)) {
+    const int n = w.b - w.a;
+    if (!mbar_wait(&c.q_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {
+        const int g = w.before + i;
+        if (!mbar_wait(&c.k_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+        tmem_fence_after();
+        const uint32_t d = tm + S::kS + (g & 1) * kPos, k0 = smem + (g & 1) * 2 * S::kKPart;
+        // the small products first
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k)
+            mma_f16(d, tm + S::kQ + (x == 0 ? kD / 2 : 0) + 8 * k,
+                    mma_b_descriptor(k0 + (x == 1 ? S::kKPart : 0) + (k / 4) * (kPos * 128) + (k % 4) * 32, 16), kScores,
+                    x + k > 0);
+        mma_commit(&c.s_full[g & 1]);
+      }
+      if (i > 0) {
+        const int g = w.before + i - 1;
+        if (!mbar_wait(&c.v_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+        if (!mbar_wait(&c.p_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+        if (g > 0 && !mbar_wait(&c.t_free, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
+        tmem_fence_after();
+        const uint32_t a = tm + S::kS + (g & 1) * kPos, v0 = smem + S::kKBytes;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int k = 0; k < kPos / 16; ++k)
+            mma_f16(tm + S::kT, a + 16 * k + (x == 0 ? 8 : 0),
+                    mma_b_descriptor(v0 + (x == 1 ? S::kVPart : 0) + k * 2048, kPos * 128), kValues, x + k > 0);
+        mma_commit(&c.t_full);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ weights
+template <int kD>
+__device__ void weights_role(const PromptParams &p, Control &c) {
+  using S = Shape<kD>;
+  constexpr int kPos = S::kPos;
+  const int row = threadIdx.x;
+  const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16);
+  Walk<kD> w(c);
+  while (w.next(p, c)) {
+    const int h = w.head(), r = w.item_rt * kRows + row;
+    const bool used = r < w.n * p.group;
+    const int tok = used ? r / p.group : w.span.t1;
+    // the row's query, in two parts.  All scores of the item before have been
+    // seen, so nothing reads its queries any more.
+    const float *q = p.q + w.item_s * p.q_seq_ld + tok * p.q_ld + (h * p.group + (used ? r % p.group : 0)) * kD;
+    float big = 0.0f;
+    if (used)
+      for (int x = 0; x < kD; x += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(q + x);
+        big = fmaxf(fmaxf(big, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
+      }
+    const int up = big > 0.0f ? 14 - max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126) : 0;
+    const float row_mul = scale_pow2(p.scale, -up) * 1.44269504088896f;
+#pragma unroll
+    for (int x = 0; x < kD; x += 32) {
+      uint32_t first[16], rest[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float4 a = used ? *reinterpret_cast<const float4 *>(q + x + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        split2(scale_pow2(a.x, up), scale_pow2(a.y, up), first[2 * k], rest[2 * k]);
+        split2(scale_pow2(a.z, up), scale_pow2(a.w, up), first[2 * k + 1], rest[2 * k + 1]);
+      }
+      tmem_store16(tm + S::kQ + x / 2, first);
+      tmem_store16(tm + S::kQ + kD / 2 + x / 2, rest);
+    }
+    tmem_wait_stores();
+    tmem_fence_before();
+    mbar_arrive(&c.q_full);
+
+    const int at = w.len + tok, low = p.window ? at - p.window + 1 : 0;
+    float top = -INFINITY, off = 0.0f, den = 0.0f;  // weights are exp2(x - off): 2^15 at the maximum
+    for (int k = w.a; k < w.b; ++k) {
+      const int g = w.before + k - w.a, p0 = (w.span.first + k) * kPos;
+      const uint32_t s = tm + S::kS + (g & 1) * kPos;
+      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      const Entry &e = c.entry[g % kAhead];
+      const float mul = row_mul * exp2i(half_exponent(max(e.kmax[0], e.kmax[1])) - 7);
+      // some position of the tile is not for all rows
+      const bool masked = p0 + kPos - 1 > w.len + w.span.t0 || (p.window && p0 <= w.len + w.span.t1 - p.window) ||
+                          (e.any[0] | e.any[1]);
+      if (!mbar_wait(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      tmem_fence_after();
+      const auto score = [&](float x, int j) {
+        return p0 + j >= low && p0 + j <= at ? fmaf(x, mul, e.lost[j]) : -INFINITY;
+      };
+      float up_to = -INFINITY;
+      uint32_t x[32];
+      if (masked) {
+        for (int j0 = 0; j0 < kPos; j0 += 32) {
+          tmem_load32(s + j0, x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) up_to = fmaxf(up_to, score(__uint_as_float(x[j]), j0 + j));
+        }
+      } else {
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int j0 = 0; j0 < kPos; j0 += 32) {
+          tmem_load32(s + j0, x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
+        }
+        // rounded up, so that no weight passes 2^15
+        up_to = __fmul_ru(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul);
+      }
+      float keep = 1.0f;
+      if (up_to > top) {
+        const float now = __fadd_ru(up_to, -15.0f);
+        keep = top == -INFINITY ? 0.0f : exp2_approx(off - now);
+        top = up_to, off = now;
+      }
+      c.corr[g % kAhead][row] = keep;
+      float sum4[4] = {};
+      for (int j0 = 0; j0 < kPos; j0 += 32) {
+        tmem_load32(s + j0, x);
+        uint32_t y[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float a, b;
+          if (masked) {
+            a = exp2_approx(score(__uint_as_float(x[j]), j0 + j) - off);
+            b = exp2_approx(score(__uint_as_float(x[j + 1]), j0 + j + 1) - off);
+          } else {
+            a = exp2_approx(fmaf(__uint_as_float(x[j]), mul, -off));
+            b = exp2_approx(fmaf(__uint_as_float(x[j + 1]), mul, -off));
+          }
+          sum4[(j >> 1) & 1] += a;
+          sum4[2 + ((j >> 1) & 1)] += b;
+          const int to = (j / 16) * 16 + (j % 16) / 2;
+          split2(a, b, y[to], y[to + 8]);
+        }
+        tmem_store32(s + j0, y);
+      }
+      den = fmaf(den, keep, (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+      tmem_wait_stores();
+      tmem_fence_before();
+      mbar_arrive(&c.c_full[g % kAhead]);
+      mbar_arrive(&c.p_full[g & 1]);
+    }
+    if (w.items > 0 && !mbar_wait(&c.fin_empty, (w.items - 1) & 1, p.err, DEVERR_EMPTY_WAIT, w.items)) return;
+    c.off[row] = top == -INFINITY ? -INFINITY : off;
+    c.den[row] = den;
+    mbar_arrive(&c.fin_full);
+  }
+}
+
+// ------------------------------------------------------------------ output
+template <int kD>
+__device__ void output_role(const PromptParams &p, Control &c) {
+  using S = Shape<kD>;
+  const int row = threadIdx.x & 127;
+  const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16) + S::kT;
+  Walk<kD> w(c);
+  while (w.next(p, c)) {
+    float o[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
+    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
+      if (!mbar_wait(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      const float keep = c.corr[g % kAhead][row];
+      const Entry &e = c.entry[g % kAhead];
+      float mul[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) mul[b] = exp2i(half_exponent(max(e.vmax[0][b], e.vmax[1][b])) - 7);
+      if (!mbar_wait(&c.t_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      tmem_fence_after();
+      if (!__all_sync(0xffffffffu, keep == 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) o[i] *= keep;
+      }
+#pragma unroll
+      for (int j = 0; j < kCols; j += 16) {
+        uint32_t x[16];
+        tmem_load16(tm + j, x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[j + i] = fmaf(__uint_as_float(x[i]), mul[j / 32], o[j + i]);
+      }
+      tmem_fence_before();
+      mbar_arrive(&c.t_free);
+      mbar_arrive(&c.entry_free[g % kAhead]);
+    }
+    if (!mbar_wait(&c.fin_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
+    const float off = c.off[row], den = c.den[row];
+    mbar_arrive(&c.fin_empty);
+    const int r = w.item_rt * kRows + row;
+    if (w.whole()) {
+      if (r < w.n * p.group) {
+        float4 *to = reinterpret_cast<float4 *>(
+            p.out + (static_cast<int64_t>(w.item_s) * p.ntok + r / p.group) * p.n_heads * kD +
+            (w.head() * p.group + r % p.group) * kD + w.split() * kCols);
+        const float inv = den != 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kCols / 4; ++i)
+          to[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+      }
+    } else {
+      const int slot = 2 * blockIdx.x + (w.first ? 0 : 1);
+      float4 *to = reinterpret_cast<float4 *>(p.parts + (static_cast<int64_t>(slot) * kRows + row) * kPartLd);
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      to[kCols / 4] = make_float4(off, den, 0.0f, 0.0f);
+    }
+  }
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+  using S = Shape<kD>;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const uint32_t pad = (1024 - (smem_addr(smem_raw) & 1023)) & 1023;
+  const uint32_t operands = smem_addr(smem_raw) + pad;
+  Control &c = *reinterpret_cast<Control *>(smem_raw + pad + S::kKBytes + S::kVBytes);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.k_full[i], 128);
+      mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_full[i], 128);
+    }
+    mbar_init(&c.v_full, 128);
+    mbar_init(&c.t_full, 1);
+    mbar_init(&c.t_free, 128);
+    mbar_init(&c.q_full, 128);
+    mbar_init(&c.fin_full, 128);
+    mbar_init(&c.fin_empty, 128);
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&c.c_full[i], 128);
+      mbar_init(&c.scan_full[i], 2);
+      mbar_init(&c.entry_free[i], 128);
+    }
+    fence_mbar_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tile = blockIdx.x % p.tiles, sh = blockIdx.x / p.tiles;
-  const int h = sh % p.v.n_kv, s = sh / p.v.n_kv;
-  const int n = p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
-  const int len = seq_length(p.v, s);
-  const int r0 = tile * kRows, rows = n * p.group;
-  const auto out_row = [&](int r) {
-    return p.out + (static_cast<int64_t>(s) * p.ntok + r / p.group) * p.n_heads * kD + (h * p.group + r % p.group) * kD;
-  };
-  for (int x = tid; x < kRows * kD; x += 32 * kWarps) {
-    const int r = r0 + x / kD, e = x % kD;
-    qs[x] = r < rows ? p.q[s * p.q_seq_ld + (r / p.group) * p.q_ld + (h * p.group + r % p.group) * kD + e] * p.scale : 0.0f;
-    if (r >= rows && r < p.ntok * p.group) out_row(r)[e] = 0.0f;
-  }
-  if (r0 >= rows) return;
-  const int t0 = r0 / p.group, t1 = (min(r0 + kRows, rows) - 1) / p.group;
-  const int begin = p.window ? max(0, len + t0 - p.window + 1) : 0, end = len + t1 + 1;
-  float top[kWarpRows], den[kWarpRows], o[kWarpRows][kD / 32];
-#pragma unroll
-  for (int k = 0; k < kWarpRows; ++k) {
-    top[k] = -INFINITY, den[k] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kD / 32; ++e) o[k][e] = 0.0f;
-  }
-  for (int j0 = begin; j0 < end; j0 += kTile) {
-    __syncthreads();
-    for (int j = warp; j < kTile; j += kWarps) {
-      const int pos = j0 + j;
-      const int page = pos < end ? seq_page(p.v, s, pos / p.v.P) : -1;
-      const uint8_t *kr = page >= 0 ? page_row(p.v, p.layer, page, h, 0, pos % p.v.P) : nullptr;
-      const uint8_t *vr = page >= 0 ? page_row(p.v, p.layer, page, h, 1, pos % p.v.P) : nullptr;
-      if (!kr && pos < end && lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(s));
-      bool bad = false;
-#pragma unroll
-      for (int e = 0; e < kD / 32; ++e) {
-        float a = 0.0f, b = 0.0f;
-        if (kr) {
-          const float fk = __half2float(reinterpret_cast<const __half *>(kr)[e]);
-          const float fv = __half2float(reinterpret_cast<const __half *>(vr)[e]);
-          bad |= !isfinite(fk) || !isfinite(fv);
-          a = isfinite(fk) ? fk * reinterpret_cast<const int8_t *>(kr + kD / 16)[32 * e + lane] : 0.0f;
-          b = isfinite(fv) ? fv * reinterpret_cast<const int8_t *>(vr + kD / 16)[32 * e + lane] : 0.0f;
+  find_work<kD>(p, c);  // with CTA barriers
+  const bool work = c.begin < c.end;
+  if (work && warp == 16) tmem_alloc(&c.tmem);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  if (warp < 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWeights));
+    if (work) weights_role<kD>(p, c);
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOutput));
+    if (work) output_role<kD>(p, c);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOperand));
+    if (work) keys_role<kD>(p, c, operands);
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOperand));
+    if (work) values_role<kD>(p, c, operands);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 16) {
+      if (work && (tid & 31) == 0) products_role<kD>(p, c, operands);
+      __syncwarp();
+    } else if (warp < 19) {
+      if (work) scan_role<kD>(p, c);
+    } else {
+      // the parts that the CTA leaves, for the join
+      Walk<kD> w(c);
+      Part note[2] = {};
+      while (work && w.next(p, c))
+        if (!w.whole()) note[w.first ? 0 : 1] = Part{w.item_s, w.item_rt, w.item_y, w.a, w.b, w.span.tiles, {0, 0}};
+      if ((tid & 31) < 2) p.notes[2 * blockIdx.x + (tid & 31)] = note[tid & 1];
+      // tokens beyond a sequence's have an output of 0
+      if (p.n_tok) {
+        const int width = p.n_heads * kD;
+        for (int64_t r = blockIdx.x; r < static_cast<int64_t>(p.v.n_seq) * p.ntok; r += gridDim.x) {
+          if (r % p.ntok < c.seq[r / p.ntok].y) continue;
+          float4 *o = reinterpret_cast<float4 *>(p.out + r * width);
+          for (int i = tid & 31; i < width / 4; i += 32) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        ks[j * kLd + 32 * e + lane] = a;
-        vs[j * kLd + 32 * e + lane] = b;
-      }
-      if (lane == 0) lost[j] = !kr ? -INFINITY : bad ? __int_as_float(0x7fffffff) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarpRows; ++k) {
-      const int row = warp * kWarpRows + k, at = len + (r0 + row) / p.group, pos = j0 + lane;
-      const bool sees = r0 + row < rows && pos <= at && (!p.window || pos > at - p.window);
-      float sc = 0.0f;
-      for (int e = 0; e < kD; e += 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(qs + row * kD + e);
-        const float4 b = *reinterpret_cast<const float4 *>(ks + lane * kLd + e);
-        sc = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, sc))));
-      }
-      sc = sees ? sc + lost[lane] : -INFINITY;
-      const bool nan = __any_sync(0xffffffffu, isnan(sc));
-      const float up = nan ? __int_as_float(0x7fffffff) : fmaxf(top[k], warp_max_all(sc));
-      const float ref = up == -INFINITY ? 0.0f : up;
-      const float keep = expf(top[k] - ref), w = expf(sc - ref);
-      top[k] = isnan(top[k]) ? top[k] : up;
-      den[k] = den[k] * keep + warp_sum_xor<32>(w);
-#pragma unroll
-      for (int e = 0; e < kD / 32; ++e) o[k][e] *= keep;
-      for (int j = 0; j < kTile; ++j) {
-        const float wj = __shfl_sync(0xffffffffu, w, j);
-#pragma unroll
-        for (int e = 0; e < kD / 32; ++e) o[k][e] = fmaf(wj, vs[j * kLd + 32 * e + lane], o[k][e]);
       }
     }
   }
-#pragma unroll
-  for (int k = 0; k < kWarpRows; ++k) {
-    const int r = r0 + warp * kWarpRows + k;
-    if (r >= rows) continue;
-#pragma unroll
-    for (int e = 0; e < kD / 32; ++e) out_row(r)[32 * e + lane] = den[k] != 0.0f ? o[k][e] / den[k] : 0.0f;
+  // the products of all tiles have been waited for by the roles that use them
+  tmem_fence_before();
+  __syncthreads();
+  if (work && warp == 16) {
+    tmem_fence_after();
+    tmem_free(c.tmem);
   }
+}
+
+// The parts of an item, joined in the order of their positions: block x is the
+// CTA that holds an item's first part, block y a group of rows, a warp a row.
+template <int kD>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ PromptParams p, int ctas) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const auto heads = [](const Part &x) { return x.tiles > 0 && x.a == 0 && x.b < x.tiles; };
+  int slot = 2 * c0;
+  Part x = p.notes[slot];
+  if (!heads(x)) x = p.notes[++slot];
+  if (!heads(x)) return;
+  const int r = x.rt * kRows + row, n = p.n_tok ? min(max(p.n_tok[x.s], 0), p.ntok) : p.ntok;
+  if (r >= n * p.group) return;
+  float top = -INFINITY, den = 0.0f;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  int upto = x.b;
+  for (int c = c0;; slot = 2 * ++c) {
+    if (c > c0) {  // the item goes on at the start of the next CTA's share
+      if (c >= ctas || upto >= x.tiles) break;
+      upto = p.notes[slot].b;
+    }
+    const float *from = p.parts + (static_cast<int64_t>(slot) * kRows + row) * kPartLd;
+    const float2 ml = *reinterpret_cast<const float2 *>(from + kCols);
+    const float4 a = reinterpret_cast<const float4 *>(from)[lane];
+    const float up = fmaxf(top, ml.x), ref = up == -INFINITY ? 0.0f : up;
+    const float keep = exp2f(top - ref), f = exp2f(ml.x - ref);  // 0 for a part that saw nothing
+    top = up;
+    den = fmaf(den, keep, f * ml.y);
+    y = make_float4(fmaf(f, a.x, y.x * keep), fmaf(f, a.y, y.y * keep), fmaf(f, a.z, y.z * keep), fmaf(f, a.w, y.w * keep));
+  }
+  const int h = x.y / Shape<kD>::kSplit, split = x.y % Shape<kD>::kSplit;
+  float4 *to = reinterpret_cast<float4 *>(p.out + (static_cast<int64_t>(x.s) * p.ntok + r / p.group) * p.n_heads * kD +
+                                          (h * p.group + r % p.group) * kD + split * kCols);
+  to[lane] = den != 0.0f ? make_float4(y.x / den, y.y / den, y.z / den, y.w / den) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 bool sizes_ok(const epq_pages *pages, int n_heads, int ntok) {
-  return pages_sizes_ok(pages) && n_heads >= 1 && n_heads % pages->n_kv_heads == 0 && n_heads / pages->n_kv_heads <= 16 &&
-         ntok >= 1 && static_cast<int64_t>(pages->n_seq) * ntok < (1 << 24);
+  return pages_sizes_ok(pages) && n_heads >= 1 && n_heads % pages->n_kv_heads == 0 &&
+         n_heads / pages->n_kv_heads <= kMaxGroupPrompt && ntok >= 1 &&
+         static_cast<int64_t>(pages->n_seq) * ntok < (1 << 24);
 }
 
-LaunchOnce g_launch[2];
+template <int kD>
+cudaError_t launch(const PromptParams &p, const DeviceInfo &dev, cudaStream_t s) {
+  static LaunchOnce once;
+  const size_t smem = 1024 + Shape<kD>::kKBytes + Shape<kD>::kVBytes + sizeof(Control);
+  cudaError_t e = once.prepare(dev.device, prompt_kernel<kD>, kThreads, smem, false, nullptr);
+  const int ctas = std::min(dev.sm_count, kMaxCtas);
+  if (e == cudaSuccess) e = launch_pdl(prompt_kernel<kD>, dim3(ctas), dim3(kThreads), smem, s, p);
+  if (e == cudaSuccess)
+    e = launch_pdl(join_kernel<kD>, dim3(ctas, kRows / kJoinWarps), dim3(32 * kJoinWarps), 0, s, p, ctas);
+  return e;
+}
 
 }  // namespace
 }  // namespace epq
@@ -134,7 +830,7 @@ LaunchOnce g_launch[2];
 using namespace epq;
 
 extern "C" size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads, int ntok) {
-  return sizes_ok(pages, n_heads, ntok) ? 16 : 0;
+  return sizes_ok(pages, n_heads, ntok) ? 2 * kMaxCtas * (sizeof(Part) + 4 * kRows * kPartLd) : 0;
 }
 
 extern "C" epq_status epq_attention_prompt(const epq_pages *pages, int layer, const float *q, int n_heads, int ntok,
@@ -156,16 +852,13 @@ extern "C" epq_status epq_attention_prompt(const epq_pages *pages, int layer, co
   if (!aligned16(ws)) return EPQ_ERR_ALIGN;
   p.q = q, p.n_tok = o.n_tok, p.layer = layer, p.n_heads = n_heads, p.group = n_heads / p.v.n_kv, p.ntok = ntok;
   p.window = o.window, p.scale = scale, p.out = out;
-  p.tiles = (ntok * p.group + kRows - 1) / kRows;
+  p.notes = static_cast<Part *>(ws);
+  p.parts = reinterpret_cast<float *>(p.notes + 2 * kMaxCtas);
   DeviceInfo dev;
-  if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
+  if (!current_device(&dev) || dev.major * 10 + dev.minor != 103) return EPQ_ERR_DEVICE;
   p.err = device_error_slot();
   if (!p.err) return EPQ_ERR_DEVICE;
-  void (*kernel)(PromptParams) = p.v.D == 128 ? prompt_kernel<128> : prompt_kernel<256>;
-  const size_t smem = 4 * (2 * kTile * (p.v.D + 4) + kRows * p.v.D);
-  cudaError_t e = g_launch[p.v.D == 256].prepare(dev.device, kernel, 32 * kWarps, smem, false, nullptr);
-  if (e == cudaSuccess)
-    e = launch_pdl(kernel, dim3(static_cast<unsigned>(p.tiles * p.v.n_kv * p.v.n_seq)), dim3(32 * kWarps), smem,
-                   reinterpret_cast<cudaStream_t>(stream), p);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = p.v.D == 128 ? launch<128>(p, dev, s) : launch<256>(p, dev, s);
   return e == cudaSuccess ? EPQ_OK : cuda_fail(e);
 }

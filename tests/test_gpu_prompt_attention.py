@@ -3,7 +3,14 @@ bounds that count float32 roundings: a score is off by at most ds = (32 + D/4)
 2^-24 scale sum |q||k| (D/4 additions of a dot product that pass through one
 accumulator, 32 for the rest: the parts of an operand, the scale, the
 exponential's argument), which changes a weight by a factor within exp(+-2 ds);
-a sum over T positions is off by (32 + T/4) 2^-24 of the sum of magnitudes."""
+a sum over T positions is off by (32 + T/4) 2^-24 of the sum of magnitudes.
+
+Weights have a floor besides.  The kernel holds a weight w (1 at the row's
+maximum) as two halves of w' = 2^15 w: the 11 leading bits, and the rest
+rounded.  A half is a multiple of 2^-24, so where w' is small each of the two
+roundings is off by up to 2^-25, whatever w' is: 2^-24 of w', 2^-39 of w.  An
+output is off by up to 2^-39 sum_j |v_j| for it, which shows where every larger
+weight meets a value of 0."""
 import math
 
 import pytest
@@ -94,7 +101,8 @@ class Case:
                 smag = (q.abs() @ K.abs().T * self.scale).masked_fill(~see[:, None], 0.0).amax(-1)
                 w = torch.softmax(sc, -1).nan_to_num(0.0)
                 ds = (32 + D / 4) * 2.0 ** -24 * smag[..., None]
-                bound = (w @ V.abs()) * (torch.expm1(2 * ds) + 2 * (32 + (n + t) / 4) * 2.0 ** -24) + 1e-30
+                bound = (w @ V.abs()) * (torch.expm1(2 * ds) + 2 * (32 + (n + t) / 4) * 2.0 ** -24)
+                bound = bound + 2.0 ** -39 * V.abs().sum(0) + 1e-30
                 out_h = got[s, :t, h * G:(h + 1) * G]
                 nan = (see & lost[:, h]).any(1)
                 assert torch.isnan(out_h[nan]).all()
