@@ -25,9 +25,11 @@
 // memory outlives a tile.
 //
 // Roles of a CTA's warps, each a step ahead of the next:
-//   scan     (2 warps) pages, factors' maxima, what is missing, 4 tiles ahead
-//   keys     (4) codes to two fp16 parts in swizzled shared memory, 2 tiles
-//   values   (4) the same, one tile
+//   copies   (1 warp) a tile's rows, page by page, into shared memory as the
+//            cache holds them
+//   scan     (2) their factors' maxima and scaled factors, what is missing
+//   operands (8) keys of tile t + 1, then values of tile t: codes times
+//            factors, two fp16 parts in swizzled shared memory
 //   products (1) issues them: scores of tile t + 1, then values of tile t, so
 //            that the tensor core works on one while the weights of the other
 //            are made
@@ -53,11 +55,12 @@ constexpr int kMaxCtas = 152;  // one per SM of a GB300
 constexpr int kMaxGroupPrompt = 16;
 constexpr int kExtra = 2;
 constexpr int kAhead = 4;  // tiles that the scan may be ahead of the output
+constexpr int kRaw = 2;    // tiles of keys, and of values, as the cache holds them
 constexpr int kJoinWarps = 8;
 constexpr int kPartLd = kCols + 4;
 
-// Warps: 0-3 weights, 4-7 output, 8-11 keys, 12-15 values, 16 products, 17-18
-// scan, 19 unused rows.  Registers of each group of four warps: the launch has
+// Warps: 0-3 weights, 4-7 output, 8-15 operands, 16 products, 17 copies, 18-19
+// scan.  Registers of each group of four warps: the launch has
 // 5 * 128 threads * 96, and 5 * 96 = 104 + 168 + 72 + 72 + 64.
 constexpr int kThreads = 640;
 constexpr int kRegsWeights = 104, kRegsOutput = 168, kRegsOperand = 72, kRegsRest = 64;
@@ -89,24 +92,26 @@ struct Shape {
   static constexpr int kSplit = kD / kCols;          // items that share a row tile's scores' rows
   static constexpr uint32_t kKPart = kPos * kD * 2;  // bytes of one part of a tile's keys
   static constexpr uint32_t kVPart = kPos * kCols * 2;  // and of its values
-  static constexpr uint32_t kKBytes = 2 * 2 * kKPart, kVBytes = 2 * kVPart;
+  static constexpr uint32_t kRow = kD + kD / 16;        // bytes of a row
+  static constexpr uint32_t kPlane = kPos * kRow;       // of a tile's rows
+  // shared memory: keys, values, rows
+  static constexpr uint32_t kV = 2 * kKPart, kRows = kV + 2 * kVPart, kBytes = kRows + kRaw * 2 * kPlane;
   // columns of tensor memory
   static constexpr uint32_t kQ = 0, kS = kD, kT = kD + 2 * kPos;
   static_assert(kT + kCols <= 512, "");
 };
 
 // What the scan says of a tile.
-struct Entry {
-  long long off[128];  // byte offset of a position's key row in the pool, -1: nothing to read
-  float lost[128];     // 0; NaN: a factor is not finite; -inf: no page
-  int kmax[2];         // largest factor of the keys (bits of the half), one per scanning warp
-  int vmax[2][4];      // of the values, by column block
-  int any[2];          // whether some `lost` matters
+struct alignas(16) Entry {
+  __half kf[512], vf[512];  // scaled factors [position][block], 0 where there is nothing to read
+  float lost[128];          // 0; NaN: a factor is not finite; -inf: no page
+  float kmul, vmul[4];      // what undoes the factors' scales
+  int any;                  // whether some `lost` matters
 };
 
 struct Control {
-  uint64_t k_full[2], v_full, s_full[2], p_full[2], t_full, t_free, q_full, c_full[kAhead], fin_full, fin_empty,
-      scan_full[kAhead], entry_free[kAhead];
+  uint64_t raw_full[2][kRaw], raw_free[2][kRaw], k_full, v_full, s_full[2], p_full[2], t_full, t_free, q_full, c_full[kAhead],
+      fin_full, fin_empty, scan_full[kAhead], entry_free[kAhead], drain;
   uint32_t tmem;
   long long begin, end;  // the CTA's share
   int s, rt, y, tile;    // where it begins
@@ -114,9 +119,34 @@ struct Control {
   int pair0[kMaxSeq + 1];  // row tiles of the sequences before each
   int2 seq[kMaxSeq];       // length, tokens
   Entry entry[kAhead];
+  uint32_t scan[2][2][6];  // what the two scanning warps tell each other
   float corr[kAhead][kRows];
   float off[kRows], den[kRows];
 };
+
+// The code of all roles together has to fit the SM's instruction cache (a first
+// version, unrolled further, waited for instructions half of the time): loops
+// are unrolled only as far as registers or latencies ask for, and what a wait
+// does when it gives up is out of line.  (No other call: a role's registers are
+// fewer than the launch's.)
+__device__ __noinline__ void gave_up(unsigned *err, unsigned code, unsigned where) { record_error(err, code, where); }
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err, unsigned code, unsigned where = 0) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      gave_up(err, code, where);
+      return false;
+    }
+  return true;
+}
+
+// All lanes of the warp wait; the same answer for all.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, unsigned *err, unsigned code, unsigned where) {
+  return __all_sync(0xffffffffu, wait(bar, parity, err, code, where));
+}
 
 __device__ __forceinline__ int row_tiles(const PromptParams &p, int n) { return (n * p.group + kRows - 1) / kRows; }
 
@@ -288,66 +318,142 @@ __device__ __forceinline__ int half_exponent(int bits) {
   return bits ? static_cast<int>(__float_as_uint(half_bits_to_float(bits)) >> 23) - 127 : 0;
 }
 
+// ------------------------------------------------------------------ copies
+// One warp.  A tile's rows lie in runs, each within a page; lane r brings run r
+// of the keys and of the values.
+template <int kD>
+__device__ void copies_role(const PromptParams &p, Control &c, uint8_t *smem) {
+  using S = Shape<kD>;
+  const int lane = threadIdx.x & 31, run = min(p.v.P, S::kPos);
+  const uint32_t bytes = run * S::kRow;
+  Walk<kD> w(c);
+  int issued[2] = {};
+  bool ok = true;
+  while (ok && w.next(p, c)) {
+    for (int k = w.a; ok && k < w.b; ++k) {
+      const int g = w.before + k - w.a, stage = g % kRaw;
+      const int pos = (w.span.first + k) * S::kPos + lane * run;
+      const bool used = lane * run < S::kPos && pos < w.span.end;
+      const int page = used ? seq_page(p.v, w.item_s, pos / p.v.P) : -1;
+      if (used && page < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(w.item_s));
+      const uint32_t all = __popc(__ballot_sync(0xffffffffu, page >= 0)) * bytes;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (ok && g >= kRaw) ok = wait_warp(&c.raw_free[x][stage], (g / kRaw - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[x][stage], all);
+        __syncwarp();
+        if (page >= 0)
+          bulk_g2s(smem + S::kRows + (2 * stage + x) * S::kPlane + lane * bytes,
+                   page_row(p.v, p.layer, page, w.head(), x, pos % p.v.P), bytes, &c.raw_full[x][stage]);
+        issued[x] = g + 1;
+      }
+    }
+  }
+  for (int x = 0; x < 2; ++x)  // no copy is in flight when the CTA ends
+    for (int g = max(0, issued[x] - kRaw); g < issued[x]; ++g)
+      wait_warp(&c.raw_full[x][g % kRaw], (g / kRaw) & 1, p.err, DEVERR_DRAIN_WAIT, g);
+}
+
 // ------------------------------------------------------------------ scan
+// Four halves times a power of two (one that is not finite: 0).
+__device__ __forceinline__ uint2 scale4(uint2 f, const float (&mul)[4]) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = ((i & 2 ? f.y : f.x) >> (16 * (i & 1))) & 0xffffu;
+    y[i] = (h & 0x7fffu) < 0x7c00u ? half_bits_to_float(h) * mul[i] : 0.0f;
+  }
+  return make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
+}
+
+// Largest of two pairs of halves, as bits without the sign (an element that is
+// not finite counts as 0).
+__device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
+  b &= 0x7fff7fffu;
+  if ((b & 0x7fffu) >= 0x7c00u) b &= 0xffff0000u;
+  if (b >= 0x7c000000u) b &= 0xffffu;
+  return __vmaxu2(a, b);
+}
+
+// Two warps, kPos / 64 positions a lane.
 template <int kD>
 __device__ void scan_role(const PromptParams &p, Control &c) {
-  constexpr int kPos = Shape<kD>::kPos, kMine = kPos / 64, kWords = kD / 128;
-  const int t = threadIdx.x - 17 * 32, lane = t & 31, warp = t >> 5;
+  using S = Shape<kD>;
+  constexpr int kPos = S::kPos, kWords = kD / 128, kMine = kPos / 64;
+  const int t = threadIdx.x - 18 * 32, lane = t & 31;
   Walk<kD> w(c);
   while (w.next(p, c)) {
-    const int h = w.head(), split = w.split();
+    const int split = w.split();
+#pragma unroll 1
     for (int k = w.a; k < w.b; ++k) {
-      const int g = w.before + k - w.a;
+      const int g = w.before + k - w.a, p0 = (w.span.first + k) * kPos;
       Entry &e = c.entry[g % kAhead];
-      const int p0 = (w.span.first + k) * kPos;
       uint2 kf[kMine][kWords], vf[kMine][kWords];
-      long long off[kMine];
+      bool read[kMine];
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int pos = p0 + t + 64 * m;
         const int page = pos < w.span.end ? seq_page(p.v, w.item_s, pos / p.v.P) : -1;
-        off[m] = page < 0 ? -1 : page_row(p.v, p.layer, page, h, 0, pos % p.v.P) - p.v.pool;
-      }
-#pragma unroll
-      for (int m = 0; m < kMine; ++m)
+        read[m] = page >= 0;
+        const uint8_t *row = page_row(p.v, p.layer, max(page, 0), w.head(), 0, pos % p.v.P);
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
-          const uint8_t *row = p.v.pool + off[m];
-          kf[m][x] = off[m] < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(row + 8 * x);
-          vf[m][x] = off[m] < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(row + p.v.P * p.v.row + 8 * x);
+          kf[m][x] = read[m] ? *reinterpret_cast<const uint2 *>(row + 8 * x) : make_uint2(0, 0);
+          vf[m][x] = read[m] ? *reinterpret_cast<const uint2 *>(row + p.v.P * S::kRow + 8 * x) : make_uint2(0, 0);
         }
-      if (g >= kAhead && !mbar_wait(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
-      unsigned kmax = 0, vmax[4] = {};
-      bool any = false;
+      }
+      uint32_t kmax = 0, vmax[2] = {};
+      bool bad[kMine], any = false;
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        bad[m] = false;
+#pragma unroll
+        for (int x = 0; x < kWords; ++x) {
+          const uint32_t four[4] = {kf[m][x].x, kf[m][x].y, vf[m][x].x, vf[m][x].y};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            bad[m] |= (four[i] & 0x7c00u) == 0x7c00u || (four[i] & 0x7c000000u) == 0x7c000000u;
+          kmax = larger2(larger2(kmax, kf[m][x].x), kf[m][x].y);
+          if (kWords == 1 || x == split) vmax[0] = larger2(vmax[0], vf[m][x].x), vmax[1] = larger2(vmax[1], vf[m][x].y);
+        }
+        any |= p0 + t + 64 * m < w.span.end && (!read[m] || bad[m]);
+      }
+      if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
+      // the largest of both warps: of the keys, and of the values by block
+      uint32_t most[5];
+      most[4] = max(kmax & 0xffffu, kmax >> 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most[i] = (vmax[i / 2] >> (16 * (i & 1))) & 0xffffu;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) most[i] = __reduce_max_sync(0xffffffffu, most[i]);
+      any = __any_sync(0xffffffffu, any);
+      uint32_t *mine = c.scan[g & 1][t >> 5];
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) mine[i] = most[i];
+        mine[5] = any;
+      }
+      named_sync(1, 64);
+      const uint32_t *other = c.scan[g & 1][1 - (t >> 5)];
+      float mul[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) mul[i] = exp2i(7 - half_exponent(max(most[i], other[i])));
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int row = t + 64 * m;
-        bool bad = false;
+        e.lost[row] = !read[m] ? -INFINITY : bad[m] ? __int_as_float(0x7fffffff) : 0.0f;
+        const float kmul[4] = {mul[4], mul[4], mul[4], mul[4]}, vmul[4] = {mul[0], mul[1], mul[2], mul[3]};
 #pragma unroll
         for (int x = 0; x < kWords; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const unsigned a = ((i & 2 ? kf[m][x].y : kf[m][x].x) >> (16 * (i & 1))) & 0x7fffu;
-            const unsigned b = ((i & 2 ? vf[m][x].y : vf[m][x].x) >> (16 * (i & 1))) & 0x7fffu;
-            bad |= a >= 0x7c00u || b >= 0x7c00u;
-            if (a < 0x7c00u) kmax = max(kmax, a);
-            if (b < 0x7c00u && (kWords == 1 || x == split)) vmax[i] = max(vmax[i], b);
-          }
-        const bool used = p0 + row < w.span.end;
-        if (used && off[m] < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(w.item_s));
-        e.off[row] = off[m];
-        e.lost[row] = off[m] < 0 ? -INFINITY : bad ? __int_as_float(0x7fffffff) : 0.0f;
-        any |= used && (off[m] < 0 || bad);
+          *reinterpret_cast<uint2 *>(e.kf + row * (kD / 32) + 4 * x) = scale4(kf[m][x], kmul);
+        *reinterpret_cast<uint2 *>(e.vf + row * 4) = scale4(kWords == 1 || split == 0 ? vf[m][0] : vf[m][kWords - 1], vmul);
       }
-      kmax = __reduce_max_sync(0xffffffffu, kmax);
+      if (t == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vmax[i] = __reduce_max_sync(0xffffffffu, vmax[i]);
-      any = __any_sync(0xffffffffu, any);
-      if (lane == 0) {
-        e.kmax[warp] = kmax;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e.vmax[warp][i] = vmax[i];
-        e.any[warp] = any;
+        for (int i = 0; i < 4; ++i) e.vmul[i] = __frcp_rn(mul[i]);  // exact: powers of two
+        e.kmul = __frcp_rn(mul[4]);
+        e.any = any | other[5];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.scan_full[g % kAhead]);
@@ -372,95 +478,72 @@ __device__ __forceinline__ void convert8(uint2 x, __half factor, uint4 &first, u
   }
 }
 
-// A tile's rows to shared memory, by 128 threads: kWidth columns of `plane`
-// from column `col` on, block b's factors times mul[b].  `ready` is asked
-// before the first write.
-template <int kPos, int kWidth, int kBlocks, typename Ready>
-__device__ __forceinline__ bool operand(const PromptParams &p, const Entry &e, int plane, int col,
-                                        const float (&mul)[kBlocks], uint32_t part, uint32_t smem, Ready ready) {
-  constexpr int kChunks = kWidth / 8, kStep = 128 / kChunks, kSteps = kPos / kStep, kBatch = 8;
-  static_assert(kSteps % kBatch == 0, "");
-  const int t = threadIdx.x & 127, chunk = t % kChunks, r0 = t / kChunks;
-  const uint8_t *base = p.v.pool + static_cast<int64_t>(plane) * p.v.P * p.v.row;
-  const int codes = p.v.D / 16 + col + 8 * chunk, factor = 2 * (col / 32 + chunk / 4);
-  float m = mul[0];
-#pragma unroll
-  for (int b = 1; b < kBlocks; ++b) m = chunk / 4 == b ? mul[b] : m;
-  const uint32_t at = smem + (chunk / 8) * (kPos * 128);
-  uint2 x[kBatch];
-  unsigned short f[kBatch];
-  const auto load = [&](int k) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const long long off = e.off[r0 + kStep * (k + i)];
-      x[i] = off < 0 ? make_uint2(0, 0) : *reinterpret_cast<const uint2 *>(base + off + codes);
-      f[i] = off < 0 ? 0 : *reinterpret_cast<const unsigned short *>(base + off + factor);
-    }
-  };
-  load(0);
-  if (!ready()) return false;
-#pragma unroll
-  for (int k = 0; k < kSteps; k += kBatch) {
-    uint2 y[kBatch];
-    __half g[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      y[i] = x[i];
-      const unsigned short h = (f[i] & 0x7fffu) < 0x7c00u ? f[i] : 0;  // `lost` tells of the others
-      g[i] = __float2half_rn(__half2float(__ushort_as_half(h)) * m);
-    }
-    if (k + kBatch < kSteps) load(k + kBatch);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int row = r0 + kStep * (k + i);
-      uint4 a, b;
-      convert8(y[i], g[i], a, b);
-      const uint32_t to = at + row * 128 + (((chunk % 8) ^ (row % 8)) * 16);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w)
-                   : "memory");
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + part), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
-                   : "memory");
-    }
+// What a thread does of a tile's keys or values: every `step` positions from
+// its first one on, eight codes of a row.  Position r's row of 64 columns is 128
+// bytes, its 16-byte pieces permuted by r % 8; a step is a multiple of 8
+// positions, so that the permutation is the thread's own.
+struct Piece {
+  uint32_t codes, factor, to;  // bytes from the tile's rows, factors and operand
+  uint32_t step, blocks;
+  template <int kPos, int kWidth, int kRowBytes>
+  __device__ void set() {
+    constexpr int kChunks = kWidth / 8;
+    const int t = threadIdx.x & 255, chunk = t % kChunks, r0 = t / kChunks;
+    step = 256 / kChunks, blocks = kWidth / 32;
+    codes = r0 * kRowBytes + 8 * chunk;
+    factor = 2 * (r0 * blocks + chunk / 4);
+    to = (chunk / 8) * (kPos * 128) + r0 * 128 + (((chunk % 8) ^ (r0 % 8)) * 16);
   }
-  fence_shared_async();
-  return true;
-}
+};
 
 template <int kD>
-__device__ void keys_role(const PromptParams &p, Control &c, uint32_t smem) {
+__device__ void operands_role(const PromptParams &p, Control &c, uint8_t *smem) {
   using S = Shape<kD>;
+  const bool one = (threadIdx.x & 31) == 0;
+  Piece piece[2];
+  piece[0].set<S::kPos, kD, S::kRow>();
+  piece[1].set<S::kPos, kCols, S::kRow>();
   Walk<kD> w(c);
-  while (w.next(p, c))
-    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
-      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-      const Entry &e = c.entry[g % kAhead];
-      const float mul[1] = {exp2i(7 - half_exponent(max(e.kmax[0], e.kmax[1])))};
-      // the scores of two tiles before have been computed: their keys' place is free
-      const bool ok = operand<S::kPos, kD, 1>(p, e, 0, 0, mul, S::kKPart, smem + (g & 1) * 2 * S::kKPart, [&] {
-        return g < 2 || mbar_wait(&c.s_full[g & 1], ((g - 2) >> 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
-      });
-      if (!ok) return;
-      mbar_arrive(&c.k_full[g & 1]);
-    }
-}
-
-template <int kD>
-__device__ void values_role(const PromptParams &p, Control &c, uint32_t smem) {
-  using S = Shape<kD>;
-  Walk<kD> w(c);
-  while (w.next(p, c)) {
-    const int col = w.split() * kCols;
-    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
-      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-      const Entry &e = c.entry[g % kAhead];
-      float mul[4];
+  int last = -1, col = 0;  // the tile whose values come next, and their first column
+  for (bool more = true; more;) {
+    more = w.next(p, c);
+    const int begin = more ? w.before : last + 1, end = more ? begin + w.b - w.a : begin + 1;  // (once more for the last values)
+#pragma unroll 1
+    for (int g = begin; g < end; ++g) {
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {  // keys of tile g, then values of the tile before
+        const int t = x ? last : g;
+        if (x ? last < 0 : !more) continue;
+        if (!x && !wait(&c.scan_full[t % kAhead], (t / kAhead) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
+        if (!wait(&c.raw_full[x][t % kRaw], (t / kRaw) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
+        // the tile before t has its scores (its products with the values are done): its place is free
+        if (t > 0 && !wait(x ? &c.t_full : &c.s_full[(t - 1) & 1], (x ? t - 1 : (t - 1) >> 1) & 1, p.err, DEVERR_EMPTY_WAIT, t))
+          return;
+        const Piece &m = piece[x];
+        const Entry &e = c.entry[t % kAhead];
+        const uint8_t *codes = smem + S::kRows + (2 * (t % kRaw) + x) * S::kPlane + kD / 16 + (x ? col : 0) + m.codes;
+        const uint8_t *factors = reinterpret_cast<const uint8_t *>(x ? e.vf : e.kf) + m.factor;
+        uint8_t *to = smem + (x ? S::kV : 0) + m.to, *rest = to + (x ? S::kVPart : S::kKPart);
+        const uint32_t step = m.step, blocks = m.blocks;
+#pragma unroll 1
+        for (uint32_t i = 0; i < S::kPos; i += 4 * step)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) mul[b] = exp2i(7 - half_exponent(max(e.vmax[0][b], e.vmax[1][b])));
-      const bool ok = operand<S::kPos, kCols, 4>(p, e, 1, col, mul, S::kVPart, smem + S::kKBytes, [&] {
-        return g < 1 || mbar_wait(&c.t_full, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
-      });
-      if (!ok) return;
-      mbar_arrive(&c.v_full);
+          for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t r = i + k * step;
+            uint4 a, b;
+            convert8(*reinterpret_cast<const uint2 *>(codes + r * S::kRow),
+                     *reinterpret_cast<const __half *>(factors + 2 * r * blocks), a, b);
+            *reinterpret_cast<uint4 *>(to + r * 128) = a;
+            *reinterpret_cast<uint4 *>(rest + r * 128) = b;
+          }
+        fence_shared_async();
+        __syncwarp();
+        if (one) {
+          mbar_arrive(x ? &c.v_full : &c.k_full);
+          mbar_arrive(&c.raw_free[x][t % kRaw]);
+        }
+      }
+      last = g, col = w.split() * kCols;
     }
   }
 }
@@ -470,7 +553,7 @@ __device__ void values_role(const PromptParams &p, Control &c, uint32_t smem) {
 // parts, D/2 columns on are the second ones; of the weights the first and
 // second parts of 16 positions follow one another.
 template <int kD>
-__device__ void products_role(const PromptParams &p, Control &c, uint32_t smem) {
+__device__ bool products(const PromptParams &p, Control &c, uint32_t smem) {
   using S = Shape<kD>;
   constexpr int kPos = S::kPos;
   constexpr uint32_t kScores = mma_f16_shape<kPos, false>(), kValues = mma_f16_shape<kCols, true>();
@@ -478,43 +561,75 @@ __device__ void products_role(const PromptParams &p, Control &c, uint32_t smem) 
   Walk<kD> w(c);
   while (w.next(p, c)) {
     const int n = w.b - w.a;
-    if (!mbar_wait(&c.q_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
+    if (!wait(&c.q_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return false;
+#pragma unroll 1
     for (int i = 0; i <= n; ++i) {
       if (i < n) {
         const int g = w.before + i;
-        if (!mbar_wait(&c.k_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+        if (!wait(&c.k_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
         tmem_fence_after();
-        const uint32_t d = tm + S::kS + (g & 1) * kPos, k0 = smem + (g & 1) * 2 * S::kKPart;
+        const uint32_t d = tm + S::kS + (g & 1) * kPos;
         // the small products first
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
+#pragma unroll 1
+        for (int x = 0; x < 3; ++x) {
+          const uint32_t a = tm + S::kQ + (x == 0 ? kD / 2 : 0);
+          const uint64_t b = mma_b_descriptor(smem + (x == 1 ? S::kKPart : 0), 16);
 #pragma unroll
           for (int k = 0; k < kD / 16; ++k)
-            mma_f16(d, tm + S::kQ + (x == 0 ? kD / 2 : 0) + 8 * k,
-                    mma_b_descriptor(k0 + (x == 1 ? S::kKPart : 0) + (k / 4) * (kPos * 128) + (k % 4) * 32, 16), kScores,
-                    x + k > 0);
+            mma_f16(d, a + 8 * k, b + ((k / 4) * (kPos * 128) + (k % 4) * 32) / 16, kScores, x + k > 0);
+        }
         mma_commit(&c.s_full[g & 1]);
       }
       if (i > 0) {
         const int g = w.before + i - 1;
-        if (!mbar_wait(&c.v_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-        if (!mbar_wait(&c.p_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-        if (g > 0 && !mbar_wait(&c.t_free, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
+        if (!wait(&c.v_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
+        if (!wait(&c.p_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
+        if (g > 0 && !wait(&c.t_free, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return false;
         tmem_fence_after();
-        const uint32_t a = tm + S::kS + (g & 1) * kPos, v0 = smem + S::kKBytes;
+#pragma unroll 1
+        for (int x = 0; x < 3; ++x) {
+          const uint32_t a = tm + S::kS + (g & 1) * kPos + (x == 0 ? 8 : 0);
+          const uint64_t b = mma_b_descriptor(smem + S::kV + (x == 1 ? S::kVPart : 0), kPos * 128);
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
-#pragma unroll
-          for (int k = 0; k < kPos / 16; ++k)
-            mma_f16(tm + S::kT, a + 16 * k + (x == 0 ? 8 : 0),
-                    mma_b_descriptor(v0 + (x == 1 ? S::kVPart : 0) + k * 2048, kPos * 128), kValues, x + k > 0);
+          for (int k = 0; k < kPos / 16; ++k) mma_f16(tm + S::kT, a + 16 * k, b + k * 2048 / 16, kValues, x + k > 0);
+        }
         mma_commit(&c.t_full);
       }
     }
   }
+  return true;
+}
+
+template <int kD>
+__device__ void products_role(const PromptParams &p, Control &c, uint32_t smem) {
+  products<kD>(p, c, smem);
+  // no product is in flight when the tensor memory is given back
+  mma_commit(&c.drain);
+  wait(&c.drain, 0, p.err, DEVERR_DRAIN_WAIT);
 }
 
 // ------------------------------------------------------------------ weights
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z;
+  float2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(y), "l"(z));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+// A pair of weights as two fp16 parts each: the 11 leading bits, and the rest rounded.
+__device__ __forceinline__ void split_weights(float2 w, uint32_t &first, uint32_t &rest) {
+  const float2 a = make_float2(__uint_as_float(__float_as_uint(w.x) & 0xffffe000u),
+                               __uint_as_float(__float_as_uint(w.y) & 0xffffe000u));
+  const float2 b = fma2(a, make_float2(-1.0f, -1.0f), w);
+  first = pack_half2(a.x, a.y);
+  rest = pack_half2(b.x, b.y);
+}
+
 template <int kD>
 __device__ void weights_role(const PromptParams &p, Control &c) {
   using S = Shape<kD>;
@@ -530,14 +645,16 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
     // seen, so nothing reads its queries any more.
     const float *q = p.q + w.item_s * p.q_seq_ld + tok * p.q_ld + (h * p.group + (used ? r % p.group : 0)) * kD;
     float big = 0.0f;
-    if (used)
+    if (used) {
+#pragma unroll 8
       for (int x = 0; x < kD; x += 4) {
         const float4 a = *reinterpret_cast<const float4 *>(q + x);
         big = fmaxf(fmaxf(big, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
       }
+    }
     const int up = big > 0.0f ? 14 - max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126) : 0;
     const float row_mul = scale_pow2(p.scale, -up) * 1.44269504088896f;
-#pragma unroll
+#pragma unroll 1
     for (int x = 0; x < kD; x += 32) {
       uint32_t first[16], rest[16];
 #pragma unroll
@@ -555,37 +672,47 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
 
     const int at = w.len + tok, low = p.window ? at - p.window + 1 : 0;
     float top = -INFINITY, off = 0.0f, den = 0.0f;  // weights are exp2(x - off): 2^15 at the maximum
+#pragma unroll 1
     for (int k = w.a; k < w.b; ++k) {
       const int g = w.before + k - w.a, p0 = (w.span.first + k) * kPos;
       const uint32_t s = tm + S::kS + (g & 1) * kPos;
-      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const Entry &e = c.entry[g % kAhead];
-      const float mul = row_mul * exp2i(half_exponent(max(e.kmax[0], e.kmax[1])) - 7);
+      float mul = row_mul * e.kmul;
       // some position of the tile is not for all rows
-      const bool masked = p0 + kPos - 1 > w.len + w.span.t0 || (p.window && p0 <= w.len + w.span.t1 - p.window) ||
-                          (e.any[0] | e.any[1]);
-      if (!mbar_wait(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      const bool masked =
+          p0 + kPos - 1 > w.len + w.span.t0 || (p.window && p0 <= w.len + w.span.t1 - p.window) || e.any;
+      if (!wait(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       tmem_fence_after();
-      const auto score = [&](float x, int j) {
-        return p0 + j >= low && p0 + j <= at ? fmaf(x, mul, e.lost[j]) : -INFINITY;
-      };
       float up_to = -INFINITY;
-      uint32_t x[32];
       if (masked) {
-        for (int j0 = 0; j0 < kPos; j0 += 32) {
-          tmem_load32(s + j0, x);
+        // the scores as they count, over the products
+#pragma unroll 1
+        for (int j0 = 0; j0 < kPos; j0 += 16) {
+          uint32_t x[16];
+          tmem_load16(s + j0, x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) up_to = fmaxf(up_to, score(__uint_as_float(x[j]), j0 + j));
+          for (int j = 0; j < 16; ++j) {
+            const int pos = p0 + j0 + j;
+            const float y = pos >= low && pos <= at ? fmaf(__uint_as_float(x[j]), mul, e.lost[j0 + j]) : -INFINITY;
+            up_to = fmaxf(up_to, y);
+            x[j] = __float_as_uint(y);
+          }
+          tmem_store16(s + j0, x);
         }
+        tmem_wait_stores();
+        mul = 1.0f;
       } else {
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
         for (int j0 = 0; j0 < kPos; j0 += 32) {
+          uint32_t x[32];
           tmem_load32(s + j0, x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
+          for (int j = 0; j < 32; j += 2)
+            m2[(j >> 1) & 1] = fmaxf(fmaxf(m2[(j >> 1) & 1], __uint_as_float(x[j])), __uint_as_float(x[j + 1]));
         }
-        // rounded up, so that no weight passes 2^15
-        up_to = __fmul_ru(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), mul);
+        up_to = __fmul_ru(fmaxf(m2[0], m2[1]), mul);  // rounded up, so that no weight passes 2^15
       }
       float keep = 1.0f;
       if (up_to > top) {
@@ -594,34 +721,30 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
         top = up_to, off = now;
       }
       c.corr[g % kAhead][row] = keep;
-      float sum4[4] = {};
+      const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-off, -off);
+      float2 sum2[2] = {};
+#pragma unroll 1
       for (int j0 = 0; j0 < kPos; j0 += 32) {
+        uint32_t x[32], y[32];
         tmem_load32(s + j0, x);
-        uint32_t y[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          float a, b;
-          if (masked) {
-            a = exp2_approx(score(__uint_as_float(x[j]), j0 + j) - off);
-            b = exp2_approx(score(__uint_as_float(x[j + 1]), j0 + j + 1) - off);
-          } else {
-            a = exp2_approx(fmaf(__uint_as_float(x[j]), mul, -off));
-            b = exp2_approx(fmaf(__uint_as_float(x[j + 1]), mul, -off));
-          }
-          sum4[(j >> 1) & 1] += a;
-          sum4[2 + ((j >> 1) & 1)] += b;
+          float2 v = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), mul2, off2);
+          v.x = exp2_approx(v.x), v.y = exp2_approx(v.y);
+          sum2[(j >> 1) & 1] = fma2(v, make_float2(1.0f, 1.0f), sum2[(j >> 1) & 1]);
           const int to = (j / 16) * 16 + (j % 16) / 2;
-          split2(a, b, y[to], y[to + 8]);
+          split_weights(v, y[to], y[to + 8]);
         }
         tmem_store32(s + j0, y);
       }
-      den = fmaf(den, keep, (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+      const float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      den = fmaf(den, keep, sum);
       tmem_wait_stores();
       tmem_fence_before();
       mbar_arrive(&c.c_full[g % kAhead]);
       mbar_arrive(&c.p_full[g & 1]);
     }
-    if (w.items > 0 && !mbar_wait(&c.fin_empty, (w.items - 1) & 1, p.err, DEVERR_EMPTY_WAIT, w.items)) return;
+    if (w.items > 0 && !wait(&c.fin_empty, (w.items - 1) & 1, p.err, DEVERR_EMPTY_WAIT, w.items)) return;
     c.off[row] = top == -INFINITY ? -INFINITY : off;
     c.den[row] = den;
     mbar_arrive(&c.fin_full);
@@ -636,35 +759,39 @@ __device__ void output_role(const PromptParams &p, Control &c) {
   const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16) + S::kT;
   Walk<kD> w(c);
   while (w.next(p, c)) {
-    float o[kCols];
+    float2 o[kCols / 2];
 #pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = 0.0f;
+    for (int i = 0; i < kCols / 2; ++i) o[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
     for (int g = w.before; g < w.before + w.b - w.a; ++g) {
-      if (!mbar_wait(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-      if (!mbar_wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const float keep = c.corr[g % kAhead][row];
       const Entry &e = c.entry[g % kAhead];
       float mul[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) mul[b] = exp2i(half_exponent(max(e.vmax[0][b], e.vmax[1][b])) - 7);
-      if (!mbar_wait(&c.t_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      for (int b = 0; b < 4; ++b) mul[b] = e.vmul[b];
+      if (!wait(&c.t_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       tmem_fence_after();
       if (!__all_sync(0xffffffffu, keep == 1.0f)) {
+        const float2 keep2 = make_float2(keep, keep), none = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) o[i] *= keep;
+        for (int i = 0; i < kCols / 2; ++i) o[i] = fma2(o[i], keep2, none);
       }
 #pragma unroll
       for (int j = 0; j < kCols; j += 16) {
         uint32_t x[16];
         tmem_load16(tm + j, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[j + i] = fmaf(__uint_as_float(x[i]), mul[j / 32], o[j + i]);
+        for (int i = 0; i < 8; ++i)
+          o[j / 2 + i] = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                              make_float2(mul[j / 32], mul[j / 32]), o[j / 2 + i]);
       }
       tmem_fence_before();
       mbar_arrive(&c.t_free);
       mbar_arrive(&c.entry_free[g % kAhead]);
     }
-    if (!mbar_wait(&c.fin_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
+    if (!wait(&c.fin_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
     const float off = c.off[row], den = c.den[row];
     mbar_arrive(&c.fin_empty);
     const int r = w.item_rt * kRows + row;
@@ -676,13 +803,13 @@ __device__ void output_role(const PromptParams &p, Control &c) {
         const float inv = den != 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
 #pragma unroll
         for (int i = 0; i < kCols / 4; ++i)
-          to[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
+          to[i] = make_float4(o[2 * i].x * inv, o[2 * i].y * inv, o[2 * i + 1].x * inv, o[2 * i + 1].y * inv);
       }
     } else {
       const int slot = 2 * blockIdx.x + (w.first ? 0 : 1);
       float4 *to = reinterpret_cast<float4 *>(p.parts + (static_cast<int64_t>(slot) * kRows + row) * kPartLd);
 #pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+      for (int i = 0; i < kCols / 4; ++i) to[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
       to[kCols / 4] = make_float4(off, den, 0.0f, 0.0f);
     }
   }
@@ -693,16 +820,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   using S = Shape<kD>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t pad = (1024 - (smem_addr(smem_raw) & 1023)) & 1023;
-  const uint32_t operands = smem_addr(smem_raw) + pad;
-  Control &c = *reinterpret_cast<Control *>(smem_raw + pad + S::kKBytes + S::kVBytes);
+  uint8_t *smem = smem_raw + pad;
+  Control &c = *reinterpret_cast<Control *>(smem + S::kBytes);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&c.k_full[i], 128);
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.p_full[i], 128);
     }
-    mbar_init(&c.v_full, 128);
+    for (int i = 0; i < 2 * kRaw; ++i) {
+      mbar_init(&c.raw_full[i / kRaw][i % kRaw], 1);
+      mbar_init(&c.raw_free[i / kRaw][i % kRaw], 8);
+    }
+    mbar_init(&c.k_full, 8);
+    mbar_init(&c.v_full, 8);
+    mbar_init(&c.drain, 1);
     mbar_init(&c.t_full, 1);
     mbar_init(&c.t_free, 128);
     mbar_init(&c.q_full, 128);
@@ -729,20 +861,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsOutput));
     if (work) output_role<kD>(p, c);
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOperand));
-    if (work) keys_role<kD>(p, c, operands);
   } else if (warp < 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOperand));
-    if (work) values_role<kD>(p, c, operands);
+    if (work) operands_role<kD>(p, c, smem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == 16) {
-      if (work && (tid & 31) == 0) products_role<kD>(p, c, operands);
+      if (work && (tid & 31) == 0) products_role<kD>(p, c, smem_addr(smem));
       __syncwarp();
-    } else if (warp < 19) {
-      if (work) scan_role<kD>(p, c);
-    } else {
+    } else if (warp == 17) {
+      if (work) copies_role<kD>(p, c, smem);
       // the parts that the CTA leaves, for the join
       Walk<kD> w(c);
       Part note[2] = {};
@@ -758,9 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           for (int i = tid & 31; i < width / 4; i += 32) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
+    } else {
+      if (work) scan_role<kD>(p, c);
     }
   }
-  // the products of all tiles have been waited for by the roles that use them
   tmem_fence_before();
   __syncthreads();
   if (work && warp == 16) {
@@ -815,7 +944,7 @@ bool sizes_ok(const epq_pages *pages, int n_heads, int ntok) {
 template <int kD>
 cudaError_t launch(const PromptParams &p, const DeviceInfo &dev, cudaStream_t s) {
   static LaunchOnce once;
-  const size_t smem = 1024 + Shape<kD>::kKBytes + Shape<kD>::kVBytes + sizeof(Control);
+  const size_t smem = 1024 + Shape<kD>::kBytes + sizeof(Control);
   cudaError_t e = once.prepare(dev.device, prompt_kernel<kD>, kThreads, smem, false, nullptr);
   const int ctas = std::min(dev.sm_count, kMaxCtas);
   if (e == cudaSuccess) e = launch_pdl(prompt_kernel<kD>, dim3(ctas), dim3(kThreads), smem, s, p);
