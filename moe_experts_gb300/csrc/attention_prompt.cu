@@ -53,7 +53,7 @@ constexpr int kRows = 128;     // rows of an item
 constexpr int kCols = 128;     // output columns of an item
 constexpr int kMaxCtas = 152;  // one per SM of a GB300
 constexpr int kMaxGroupPrompt = 16;
-constexpr int kExtra = 2;
+constexpr int kExtra = 4;
 constexpr int kAhead = 4;  // tiles that the scan may be ahead of the output
 constexpr int kRaw = 2;    // tiles of keys, and of values, as the cache holds them
 constexpr int kJoinWarps = 8;
@@ -109,7 +109,21 @@ struct alignas(16) Entry {
   int any;                  // whether some `lost` matters
 };
 
+// An item of the CTA's share, in the order of the work.
+struct Item {
+  int s, h, col, rt;   // sequence, head, first output column, row tile
+  int len, rows;       // the sequence's committed length and rows
+  int t0, t1;          // tokens of the row tile
+  int end;             // positions that any of its rows sees
+  int p0, tiles;       // first position and tiles of the CTA's part of it; no tiles: there is no further item
+  int before;          // tiles of the items before
+  int slot;            // where a part of an item goes, -1: the item is whole
+};
+constexpr int kItems = 8;
+
 struct Control {
+  uint64_t item_full[kItems], item_free[kItems];
+  Item item[kItems];
   uint64_t raw_full[2][kRaw], raw_free[2][kRaw], k_full, v_full, s_full[2], p_full[2], t_full, t_free, q_full, c_full[kAhead],
       fin_full, fin_empty, scan_full[kAhead], entry_free[kAhead], drain;
   uint32_t tmem;
@@ -121,7 +135,7 @@ struct Control {
   Entry entry[kAhead];
   uint32_t scan[2][2][6];  // what the two scanning warps tell each other
   float corr[kAhead][kRows];
-  float off[kRows], den[kRows];
+  float off[kRows], den[kRows], row_mul[kRows];
 };
 
 // The code of all roles together has to fit the SM's instruction cache (a first
@@ -249,46 +263,58 @@ __device__ __forceinline__ void find_work(const PromptParams &p, Control &c) {
   __syncthreads();
 }
 
-// The items of a CTA's share, one after the other; every role walks alone.
+// The items of a CTA's share, one after the other.  The copies' warp walks and
+// tells the other roles.
 template <int kD>
 struct Walk {
   long long left;
-  int s, rt, y, tile;  // where the next item begins
-  // the item: tiles a..b-1 of its span; how many items and tiles came before it
-  int item_s, item_rt, item_y, len, n, a, b, items, before;
-  bool first;  // the share begins in it (or with it)
-  Span span;
+  int s, rt, y, tile, before;  // where the next item begins; tiles before it
+  bool begins;                 // whether the share begins with it (or in it)
   __device__ explicit Walk(const Control &c)
-      : left(c.end - c.begin), s(c.s), rt(c.rt), y(c.y), tile(c.tile), a(0), b(0), items(-1), before(0), first(false) {}
-  __device__ bool next(const PromptParams &p, const Control &c) {
-    before += b - a;
-    bool begins = items < 0;
-    ++items;
+      : left(c.end - c.begin), s(c.s), rt(c.rt), y(c.y), tile(c.tile), before(0), begins(true) {}
+  // The next item; its part's note for the join is written, where it is one.
+  __device__ Item next(const PromptParams &p, const Control &c) {
+    Item x = {};
     while (left > 0) {
-      len = c.seq[s].x, n = c.seq[s].y;
+      const int len = c.seq[s].x, n = c.seq[s].y;
       if (rt >= row_tiles(p, n)) {
         ++s, rt = 0;
         continue;
       }
-      span = span_of<kD>(p, len, n, rt);
+      const Span span = span_of<kD>(p, len, n, rt);
       const long long take = min(left, static_cast<long long>(span.tiles + kExtra - tile));
-      a = tile, b = min(tile + static_cast<int>(take), span.tiles);
-      item_s = s, item_rt = rt, item_y = y;
+      const int a = tile, b = min(tile + static_cast<int>(take), span.tiles);
+      if (a < b) {
+        x = {s, y / Shape<kD>::kSplit, y % Shape<kD>::kSplit * kCols, rt, len, n * p.group, span.t0, span.t1, span.end,
+             (span.first + a) * Shape<kD>::kPos, b - a, before, -1};
+        if (a > 0 || b < span.tiles) {
+          x.slot = begins ? 0 : 1;
+          if ((threadIdx.x & 31) == 0) p.notes[2 * blockIdx.x + x.slot] = Part{s, rt, y, a, b, span.tiles, {0, 0}};
+        }
+        before += b - a;
+      }
       left -= take;
       tile = 0;
-      if (++y == p.v.n_kv * Shape<kD>::kSplit) y = 0, ++rt;
-      if (a < b) {
-        first = begins;
-        return true;
-      }
       begins = false;
+      if (++y == p.v.n_kv * Shape<kD>::kSplit) y = 0, ++rt;
+      if (a < b) break;
     }
-    return false;
+    return x;
   }
-  __device__ int head() const { return item_y / Shape<kD>::kSplit; }
-  __device__ int split() const { return item_y % Shape<kD>::kSplit; }
-  __device__ bool whole() const { return a == 0 && b == span.tiles; }
 };
+
+// Item n of the walk, once it is known.  A role that has what it needs of it
+// gives the place back (one arrival a warp).
+__device__ __forceinline__ bool item_at(const PromptParams &p, Control &c, int n, Item &x) {
+  if (!wait(&c.item_full[n % kItems], (n / kItems) & 1, p.err, DEVERR_FULL_WAIT, n)) return false;
+  x = c.item[n % kItems];
+  return x.tiles > 0;
+}
+
+__device__ __forceinline__ void item_done(Control &c, int n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&c.item_free[n % kItems]);
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
@@ -329,26 +355,43 @@ __device__ void copies_role(const PromptParams &p, Control &c, uint8_t *smem) {
   Walk<kD> w(c);
   int issued[2] = {};
   bool ok = true;
-  while (ok && w.next(p, c)) {
-    for (int k = w.a; ok && k < w.b; ++k) {
-      const int g = w.before + k - w.a, stage = g % kRaw;
-      const int pos = (w.span.first + k) * S::kPos + lane * run;
-      const bool used = lane * run < S::kPos && pos < w.span.end;
-      const int page = used ? seq_page(p.v, w.item_s, pos / p.v.P) : -1;
-      if (used && page < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(w.item_s));
+  int told = 0;  // items that the other roles know of: one more than the copies are at
+  const auto tell = [&]() {
+    if (told >= kItems) ok = wait_warp(&c.item_free[told % kItems], (told / kItems - 1) & 1, p.err, DEVERR_EMPTY_WAIT, told);
+    if (!ok) return;
+    const Item x = w.next(p, c);
+    if (lane == 0) {
+      c.item[told % kItems] = x;
+      mbar_arrive(&c.item_full[told % kItems]);
+    }
+    __syncwarp();
+    ++told;
+  };
+  tell();
+  for (int n = 0; ok; ++n) {
+    const Item x = c.item[n % kItems];
+    if (x.tiles == 0) break;
+    tell();
+    for (int k = 0; ok && k < x.tiles; ++k) {
+      const int g = x.before + k, stage = g % kRaw;
+      const int pos = x.p0 + k * S::kPos + lane * run;
+      const bool used = lane * run < S::kPos && pos < x.end;
+      const int page = used ? seq_page(p.v, x.s, pos / p.v.P) : -1;
+      if (used && page < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(x.s));
       const uint32_t all = __popc(__ballot_sync(0xffffffffu, page >= 0)) * bytes;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (ok && g >= kRaw) ok = wait_warp(&c.raw_free[x][stage], (g / kRaw - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
+      for (int v = 0; v < 2; ++v) {
+        if (ok && g >= kRaw) ok = wait_warp(&c.raw_free[v][stage], (g / kRaw - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[x][stage], all);
+        if (lane == 0) mbar_arrive_expect_tx(&c.raw_full[v][stage], all);
         __syncwarp();
         if (page >= 0)
-          bulk_g2s(smem + S::kRows + (2 * stage + x) * S::kPlane + lane * bytes,
-                   page_row(p.v, p.layer, page, w.head(), x, pos % p.v.P), bytes, &c.raw_full[x][stage]);
-        issued[x] = g + 1;
+          bulk_g2s(smem + S::kRows + (2 * stage + v) * S::kPlane + lane * bytes,
+                   page_row(p.v, p.layer, page, x.h, v, pos % p.v.P), bytes, &c.raw_full[v][stage]);
+        issued[v] = g + 1;
       }
     }
+    item_done(c, n);
   }
   for (int x = 0; x < 2; ++x)  // no copy is in flight when the CTA ends
     for (int g = max(0, issued[x] - kRaw); g < issued[x]; ++g)
@@ -382,21 +425,22 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
   using S = Shape<kD>;
   constexpr int kPos = S::kPos, kWords = kD / 128, kMine = kPos / 64;
   const int t = threadIdx.x - 18 * 32, lane = t & 31;
-  Walk<kD> w(c);
-  while (w.next(p, c)) {
-    const int split = w.split();
+  Item it;
+  for (int n = 0; item_at(p, c, n, it); ++n) {
+    item_done(c, n);
+    const int split = it.col / kCols;
 #pragma unroll 1
-    for (int k = w.a; k < w.b; ++k) {
-      const int g = w.before + k - w.a, p0 = (w.span.first + k) * kPos;
+    for (int k = 0; k < it.tiles; ++k) {
+      const int g = it.before + k, p0 = it.p0 + k * kPos;
       Entry &e = c.entry[g % kAhead];
       uint2 kf[kMine][kWords], vf[kMine][kWords];
       bool read[kMine];
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int pos = p0 + t + 64 * m;
-        const int page = pos < w.span.end ? seq_page(p.v, w.item_s, pos / p.v.P) : -1;
+        const int page = pos < it.end ? seq_page(p.v, it.s, pos / p.v.P) : -1;
         read[m] = page >= 0;
-        const uint8_t *row = page_row(p.v, p.layer, max(page, 0), w.head(), 0, pos % p.v.P);
+        const uint8_t *row = page_row(p.v, p.layer, max(page, 0), it.h, 0, pos % p.v.P);
 #pragma unroll
         for (int x = 0; x < kWords; ++x) {
           kf[m][x] = read[m] ? *reinterpret_cast<const uint2 *>(row + 8 * x) : make_uint2(0, 0);
@@ -417,7 +461,7 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
           kmax = larger2(larger2(kmax, kf[m][x].x), kf[m][x].y);
           if (kWords == 1 || x == split) vmax[0] = larger2(vmax[0], vf[m][x].x), vmax[1] = larger2(vmax[1], vf[m][x].y);
         }
-        any |= p0 + t + 64 * m < w.span.end && (!read[m] || bad[m]);
+        any |= p0 + t + 64 * m < it.end && (!read[m] || bad[m]);
       }
       if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
       // the largest of both warps: of the keys, and of the values by block
@@ -503,11 +547,13 @@ __device__ void operands_role(const PromptParams &p, Control &c, uint8_t *smem) 
   Piece piece[2];
   piece[0].set<S::kPos, kD, S::kRow>();
   piece[1].set<S::kPos, kCols, S::kRow>();
-  Walk<kD> w(c);
   int last = -1, col = 0;  // the tile whose values come next, and their first column
-  for (bool more = true; more;) {
-    more = w.next(p, c);
-    const int begin = more ? w.before : last + 1, end = more ? begin + w.b - w.a : begin + 1;  // (once more for the last values)
+  bool more = true;
+  for (int n = 0; more; ++n) {
+    Item it;
+    more = item_at(p, c, n, it);
+    item_done(c, n);
+    const int begin = more ? it.before : last + 1, end = more ? begin + it.tiles : begin + 1;  // (once more for the last values)
 #pragma unroll 1
     for (int g = begin; g < end; ++g) {
 #pragma unroll 1
@@ -543,7 +589,7 @@ __device__ void operands_role(const PromptParams &p, Control &c, uint8_t *smem) 
           mbar_arrive(&c.raw_free[x][t % kRaw]);
         }
       }
-      last = g, col = w.split() * kCols;
+      last = g, col = it.col;
     }
   }
 }
@@ -558,14 +604,15 @@ __device__ bool products(const PromptParams &p, Control &c, uint32_t smem) {
   constexpr int kPos = S::kPos;
   constexpr uint32_t kScores = mma_f16_shape<kPos, false>(), kValues = mma_f16_shape<kCols, true>();
   const uint32_t tm = c.tmem;
-  Walk<kD> w(c);
-  while (w.next(p, c)) {
-    const int n = w.b - w.a;
-    if (!wait(&c.q_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return false;
+  Item it;
+  for (int m = 0; item_at(p, c, m, it); ++m) {
+    mbar_arrive(&c.item_free[m % kItems]);
+    const int n = it.tiles;
+    if (!wait(&c.q_full, m & 1, p.err, DEVERR_FULL_WAIT, m)) return false;
 #pragma unroll 1
     for (int i = 0; i <= n; ++i) {
       if (i < n) {
-        const int g = w.before + i;
+        const int g = it.before + i;
         if (!wait(&c.k_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
         tmem_fence_after();
         const uint32_t d = tm + S::kS + (g & 1) * kPos;
@@ -581,7 +628,7 @@ __device__ bool products(const PromptParams &p, Control &c, uint32_t smem) {
         mma_commit(&c.s_full[g & 1]);
       }
       if (i > 0) {
-        const int g = w.before + i - 1;
+        const int g = it.before + i - 1;
         if (!wait(&c.v_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
         if (!wait(&c.p_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return false;
         if (g > 0 && !wait(&c.t_free, (g - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return false;
@@ -630,58 +677,99 @@ __device__ __forceinline__ void split_weights(float2 w, uint32_t &first, uint32_
   rest = pack_half2(b.x, b.y);
 }
 
+// The queries of an item's rows in two parts; what undoes a row's scale goes to
+// c.row_mul.  Four threads share a row: a thread for each row would touch 32
+// lines with every read.
+template <int kD>
+__device__ __forceinline__ void queries(const PromptParams &p, Control &c, const Item &it) {
+  using S = Shape<kD>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = 4 * (lane & 3);
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    const int row0 = 32 * warp + 16 * half + (lane >> 2);  // and 8 rows on
+    const float *q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = it.rt * kRows + row0 + 8 * i;
+      q[i] = r < it.rows ? p.q + it.s * p.q_seq_ld + r / p.group * p.q_ld + (it.h * p.group + r % p.group) * kD + mine : nullptr;
+    }
+    float4 x[2][8];
+    const auto load = [&](int col) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          x[i][k] = q[i] ? *reinterpret_cast<const float4 *>(q[i] + col + 16 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float big[2] = {};
+#pragma unroll 1
+    for (int col = 0; col < kD; col += 128) {
+      load(col);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          big[i] = fmaxf(fmaxf(big[i], fmaxf(fabsf(x[i][k].x), fabsf(x[i][k].y))), fmaxf(fabsf(x[i][k].z), fabsf(x[i][k].w)));
+    }
+    int up[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 1));
+      big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], 2));
+      up[i] = big[i] > 0.0f ? 14 - max(static_cast<int>(__float_as_uint(big[i]) >> 23) - 127, -126) : 0;
+      if (mine == 0) c.row_mul[row0 + 8 * i] = scale_pow2(p.scale, -up[i]) * 1.44269504088896f;
+    }
+    const uint32_t to = c.tmem + S::kQ + (static_cast<uint32_t>(32 * warp + 16 * half) << 16);
+#pragma unroll 1
+    for (int col = 0; col < kD; col += 128) {
+      if (kD > 128) load(col);
+#pragma unroll
+      for (int k0 = 0; k0 < 8; k0 += 4) {
+        uint32_t first[16], rest[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4 a = x[i][k0 + k];
+            const int u = 4 * k + 2 * i;
+            split2(scale_pow2(a.x, up[i]), scale_pow2(a.y, up[i]), first[u], rest[u]);
+            split2(scale_pow2(a.z, up[i]), scale_pow2(a.w, up[i]), first[u + 1], rest[u + 1]);
+          }
+        tmem_store_quads(to + col / 2 + 8 * k0, first);
+        tmem_store_quads(to + kD / 2 + col / 2 + 8 * k0, rest);
+      }
+    }
+  }
+}
+
 template <int kD>
 __device__ void weights_role(const PromptParams &p, Control &c) {
   using S = Shape<kD>;
   constexpr int kPos = S::kPos;
   const int row = threadIdx.x;
   const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16);
-  Walk<kD> w(c);
-  while (w.next(p, c)) {
-    const int h = w.head(), r = w.item_rt * kRows + row;
-    const bool used = r < w.n * p.group;
-    const int tok = used ? r / p.group : w.span.t1;
-    // the row's query, in two parts.  All scores of the item before have been
-    // seen, so nothing reads its queries any more.
-    const float *q = p.q + w.item_s * p.q_seq_ld + tok * p.q_ld + (h * p.group + (used ? r % p.group : 0)) * kD;
-    float big = 0.0f;
-    if (used) {
-#pragma unroll 8
-      for (int x = 0; x < kD; x += 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(q + x);
-        big = fmaxf(fmaxf(big, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(a.z), fabsf(a.w)));
-      }
-    }
-    const int up = big > 0.0f ? 14 - max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -126) : 0;
-    const float row_mul = scale_pow2(p.scale, -up) * 1.44269504088896f;
-#pragma unroll 1
-    for (int x = 0; x < kD; x += 32) {
-      uint32_t first[16], rest[16];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float4 a = used ? *reinterpret_cast<const float4 *>(q + x + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
-        split2(scale_pow2(a.x, up), scale_pow2(a.y, up), first[2 * k], rest[2 * k]);
-        split2(scale_pow2(a.z, up), scale_pow2(a.w, up), first[2 * k + 1], rest[2 * k + 1]);
-      }
-      tmem_store16(tm + S::kQ + x / 2, first);
-      tmem_store16(tm + S::kQ + kD / 2 + x / 2, rest);
-    }
+  Item it;
+  for (int n = 0; item_at(p, c, n, it); ++n) {
+    item_done(c, n);
+    // All scores of the item before have been seen: nothing reads its queries any more.
+    queries<kD>(p, c, it);
     tmem_wait_stores();
     tmem_fence_before();
     mbar_arrive(&c.q_full);
-
-    const int at = w.len + tok, low = p.window ? at - p.window + 1 : 0;
+    __syncwarp();
+    const float row_mul = c.row_mul[row];
+    const int at = it.len + min((it.rt * kRows + row) / p.group, it.t1), low = p.window ? at - p.window + 1 : 0;
     float top = -INFINITY, off = 0.0f, den = 0.0f;  // weights are exp2(x - off): 2^15 at the maximum
 #pragma unroll 1
-    for (int k = w.a; k < w.b; ++k) {
-      const int g = w.before + k - w.a, p0 = (w.span.first + k) * kPos;
+    for (int k = 0; k < it.tiles; ++k) {
+      const int g = it.before + k, p0 = it.p0 + k * kPos;
       const uint32_t s = tm + S::kS + (g & 1) * kPos;
       if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const Entry &e = c.entry[g % kAhead];
       float mul = row_mul * e.kmul;
       // some position of the tile is not for all rows
       const bool masked =
-          p0 + kPos - 1 > w.len + w.span.t0 || (p.window && p0 <= w.len + w.span.t1 - p.window) || e.any;
+          p0 + kPos - 1 > it.len + it.t0 || (p.window && p0 <= it.len + it.t1 - p.window) || e.any;
       if (!wait(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       tmem_fence_after();
       float up_to = -INFINITY;
@@ -722,29 +810,28 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
       }
       c.corr[g % kAhead][row] = keep;
       const float2 mul2 = make_float2(mul, mul), off2 = make_float2(-off, -off);
-      float2 sum2[2] = {};
+      float2 sum2 = {};
 #pragma unroll 1
-      for (int j0 = 0; j0 < kPos; j0 += 32) {
-        uint32_t x[32], y[32];
-        tmem_load32(s + j0, x);
+      for (int j0 = 0; j0 < kPos; j0 += 16) {
+        uint32_t x[16], y[16];
+        tmem_load16(s + j0, x);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float2 v = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), mul2, off2);
+        for (int j = 0; j < 8; ++j) {
+          float2 v = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), mul2, off2);
           v.x = exp2_approx(v.x), v.y = exp2_approx(v.y);
-          sum2[(j >> 1) & 1] = fma2(v, make_float2(1.0f, 1.0f), sum2[(j >> 1) & 1]);
-          const int to = (j / 16) * 16 + (j % 16) / 2;
-          split_weights(v, y[to], y[to + 8]);
+          sum2 = fma2(v, make_float2(1.0f, 1.0f), sum2);
+          split_weights(v, y[j], y[8 + j]);
         }
-        tmem_store32(s + j0, y);
+        tmem_store16(s + j0, y);
       }
-      const float sum = (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+      const float sum = sum2.x + sum2.y;
       den = fmaf(den, keep, sum);
       tmem_wait_stores();
       tmem_fence_before();
       mbar_arrive(&c.c_full[g % kAhead]);
       mbar_arrive(&c.p_full[g & 1]);
     }
-    if (w.items > 0 && !wait(&c.fin_empty, (w.items - 1) & 1, p.err, DEVERR_EMPTY_WAIT, w.items)) return;
+    if (n > 0 && !wait(&c.fin_empty, (n - 1) & 1, p.err, DEVERR_EMPTY_WAIT, n)) return;
     c.off[row] = top == -INFINITY ? -INFINITY : off;
     c.den[row] = den;
     mbar_arrive(&c.fin_full);
@@ -757,13 +844,16 @@ __device__ void output_role(const PromptParams &p, Control &c) {
   using S = Shape<kD>;
   const int row = threadIdx.x & 127;
   const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16) + S::kT;
-  Walk<kD> w(c);
-  while (w.next(p, c)) {
+  for (int n = 0;; ++n) {
+    if (!wait(&c.item_full[n % kItems], (n / kItems) & 1, p.err, DEVERR_FULL_WAIT, n)) return;
+    const Item &it = c.item[n % kItems];  // kept until the end
+    const int tiles = it.tiles, begin = it.before;
+    if (tiles == 0) return;
     float2 o[kCols / 2];
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) o[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-    for (int g = w.before; g < w.before + w.b - w.a; ++g) {
+    for (int g = begin; g < begin + tiles; ++g) {
       if (!wait(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const float keep = c.corr[g % kAhead][row];
@@ -791,27 +881,26 @@ __device__ void output_role(const PromptParams &p, Control &c) {
       mbar_arrive(&c.t_free);
       mbar_arrive(&c.entry_free[g % kAhead]);
     }
-    if (!wait(&c.fin_full, w.items & 1, p.err, DEVERR_FULL_WAIT, w.items)) return;
+    if (!wait(&c.fin_full, n & 1, p.err, DEVERR_FULL_WAIT, n)) return;
     const float off = c.off[row], den = c.den[row];
     mbar_arrive(&c.fin_empty);
-    const int r = w.item_rt * kRows + row;
-    if (w.whole()) {
-      if (r < w.n * p.group) {
-        float4 *to = reinterpret_cast<float4 *>(
-            p.out + (static_cast<int64_t>(w.item_s) * p.ntok + r / p.group) * p.n_heads * kD +
-            (w.head() * p.group + r % p.group) * kD + w.split() * kCols);
-        const float inv = den != 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kCols / 4; ++i)
-          to[i] = make_float4(o[2 * i].x * inv, o[2 * i].y * inv, o[2 * i + 1].x * inv, o[2 * i + 1].y * inv);
-      }
-    } else {
-      const int slot = 2 * blockIdx.x + (w.first ? 0 : 1);
-      float4 *to = reinterpret_cast<float4 *>(p.parts + (static_cast<int64_t>(slot) * kRows + row) * kPartLd);
-#pragma unroll
-      for (int i = 0; i < kCols / 4; ++i) to[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+    const int r = it.rt * kRows + row;
+    float scale = 1.0f;
+    float4 *to = nullptr;
+    if (it.slot >= 0) {
+      to = reinterpret_cast<float4 *>(p.parts + (static_cast<int64_t>(2 * blockIdx.x + it.slot) * kRows + row) * kPartLd);
       to[kCols / 4] = make_float4(off, den, 0.0f, 0.0f);
+    } else if (r < it.rows) {
+      to = reinterpret_cast<float4 *>(p.out + (static_cast<int64_t>(it.s) * p.ntok + r / p.group) * p.n_heads * kD +
+                                      (it.h * p.group + r % p.group) * kD + it.col);
+      scale = den != 0.0f ? __fdiv_rn(1.0f, den) : 0.0f;
     }
+    if (to) {
+#pragma unroll
+      for (int i = 0; i < kCols / 4; ++i)
+        to[i] = make_float4(o[2 * i].x * scale, o[2 * i].y * scale, o[2 * i + 1].x * scale, o[2 * i + 1].y * scale);
+    }
+    item_done(c, n);
   }
 }
 
@@ -840,6 +929,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     mbar_init(&c.q_full, 128);
     mbar_init(&c.fin_full, 128);
     mbar_init(&c.fin_empty, 128);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&c.item_full[i], 1);
+      mbar_init(&c.item_free[i], kThreads / 32);
+    }
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&c.c_full[i], 128);
       mbar_init(&c.scan_full[i], 2);
@@ -870,13 +963,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (work && (tid & 31) == 0) products_role<kD>(p, c, smem_addr(smem));
       __syncwarp();
     } else if (warp == 17) {
+      if ((tid & 31) == 0) p.notes[2 * blockIdx.x] = p.notes[2 * blockIdx.x + 1] = Part{};
       if (work) copies_role<kD>(p, c, smem);
-      // the parts that the CTA leaves, for the join
-      Walk<kD> w(c);
-      Part note[2] = {};
-      while (work && w.next(p, c))
-        if (!w.whole()) note[w.first ? 0 : 1] = Part{w.item_s, w.item_rt, w.item_y, w.a, w.b, w.span.tiles, {0, 0}};
-      if ((tid & 31) < 2) p.notes[2 * blockIdx.x + (tid & 31)] = note[tid & 1];
       // tokens beyond a sequence's have an output of 0
       if (p.n_tok) {
         const int width = p.n_heads * kD;

@@ -105,6 +105,18 @@ __device__ __forceinline__ void tmem_store16(uint32_t address, const uint32_t (&
       : "memory");
 }
 
+// 32 columns of 16 lanes, four threads to a lane: of columns 8 n .. 8 n + 7
+// thread t has 2 (t % 4) and the next one, x[4 n] and x[4 n + 1] for the lane
+// t / 4, x[4 n + 2] and x[4 n + 3] for the lane 8 further on.
+__device__ __forceinline__ void tmem_store_quads(uint32_t address, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(x[0]),
+      "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]),
+      "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(address)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 }  // namespace epq
