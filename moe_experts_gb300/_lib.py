@@ -100,7 +100,7 @@ class RopeOpts(ctypes.Structure):
 
 
 class AppendOpts(ctypes.Structure):
-    _fields_ = [("rotation", ctypes.POINTER(Rotation)), ("position", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+    _fields_ = [("rotation", ctypes.c_void_p), ("position", ctypes.c_void_p), ("mask", ctypes.c_void_p),
                 ("n_tok", ctypes.c_void_p), ("kv_ld", ctypes.c_int64), ("kv_seq_ld", ctypes.c_int64)]
 
 
@@ -742,7 +742,7 @@ class RopeTable:
         self.table, self.first, self.interleaved = table, first, bool(interleaved)
         self.n_pos, self.rot_dim = table.shape[0], 2 * table.shape[1]
         self._r = Rotation(table.data_ptr(), self.n_pos, self.rot_dim, first, int(self.interleaved))
-        self._ref = ctypes.byref(self._r)
+        self._ref, self._address = ctypes.byref(self._r), ctypes.addressof(self._r)
 
 
 def epq_rope(x: torch.Tensor, rope: RopeTable, n_heads: int, position: torch.Tensor | None = None,
@@ -759,7 +759,7 @@ def epq_rope(x: torch.Tensor, rope: RopeTable, n_heads: int, position: torch.Ten
         raise ValueError(f"{width} elements are not {n_heads} heads")
     x_seq, x_tok = _token_strides(x, "x", shape, at)
     if out is None:
-        out, y_seq, y_tok = _allocator(stream)(shape, dtype=torch.float32, device=x.device), 0, 0
+        out, y_seq, y_tok = x.new_empty(shape) if stream is None else _empty_on(stream, shape, x.dtype, x.device), 0, 0
     else:
         y_seq, y_tok = _token_strides(out, "out", shape, at)
     i32 = torch.int32
@@ -789,7 +789,7 @@ def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, laye
         raise ValueError("k and v must have the same strides")
     if rope is not None and rope._at != at:
         _elsewhere(rope.table, "rope", at)
-    o = AppendOpts(None if rope is None else ctypes.pointer(rope._r),
+    o = AppendOpts(None if rope is None else rope._address,
                    None if position is None else _need(position, "position", torch.int32, (nseq, ntok), at),
                    None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
                    None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at), kv_tok, kv_seq)

@@ -19,7 +19,7 @@ namespace epq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;  // tokens of a CTA: 16 a thread
+constexpr int kChunk = 2048;  // tokens of a CTA: 8 a thread
 constexpr int kMaxTokens = 64;
 
 struct LogitsParams {
@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
         if (place(k) < nv) x[k] = row[place(k)];
     }
   };
-  __align__(16) float x[kEach];
-  load(r0, x);
+  __align__(16) float x[kEach], ahead[kEach];  // a row, and the next one while the row is worked on
+  load(r0, ahead);
   const int live = p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
   float pen[3] = {1.0f, 0.0f, 0.0f};
   if (p.penalties) {
@@ -137,7 +137,9 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
   for (int r = r0; r < r1; ++r) {
     const int64_t row = static_cast<int64_t>(s) * p.ntok + r;
     float *y = p.y + row * p.out_ld + v0;
-    if (r > r0) load(r, x);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) x[k] = ahead[k];
+    if (r + 1 < r1) load(r + 1, ahead);
     if (r < live) {
       uint64_t path = 0;
       if (mine) {
@@ -222,7 +224,7 @@ extern "C" epq_status epq_logits_adjust(const float *logits, int64_t vocab, int 
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int chunks = (p.vocab + kChunk - 1) / kChunk;
   // rows share the pass over the history; but all SMs have CTAs
-  const int64_t want = std::max<int64_t>(1, 6ll * dev.sm_count / chunks);  // CTAs of a chunk
+  const int64_t want = std::max<int64_t>(1, 5ll * dev.sm_count / chunks);  // CTAs of a chunk
   const int groups = static_cast<int>(std::min<int64_t>(ntok, std::max<int64_t>(1, want / n_seq)));
   p.rows_per_cta = (ntok + groups - 1) / groups;
   p.row_groups = (ntok + p.rows_per_cta - 1) / p.rows_per_cta;
