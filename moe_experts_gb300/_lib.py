@@ -759,7 +759,7 @@ def epq_rope(x: torch.Tensor, rope: RopeTable, n_heads: int, position: torch.Ten
         raise ValueError(f"{width} elements are not {n_heads} heads")
     x_seq, x_tok = _token_strides(x, "x", shape, at)
     if out is None:
-        out, y_seq, y_tok = x.new_empty(shape) if stream is None else _empty_on(stream, shape, x.dtype, x.device), 0, 0
+        out, y_seq, y_tok = _allocator(stream)(shape, dtype=torch.float32, device=x.device), 0, 0
     else:
         y_seq, y_tok = _token_strides(out, "out", shape, at)
     i32 = torch.int32

@@ -21,7 +21,8 @@ struct AppendParams {
   const float *k, *x;  // keys and values
   int64_t ld, seq_ld;
   int layer;
-  int64_t rows;  // sequences * tokens * heads
+  unsigned warps, groups, each;  // groups of `each` heads that a token has, and of all tokens
+  unsigned page_bits, plane_bytes;
   unsigned *err;
 };
 
@@ -59,57 +60,68 @@ __device__ __forceinline__ void rotate4(const RotationView &r, const float *x, i
   }
 }
 
-// One warp per (token, key/value head): its key row and its value row, four
-// elements a lane.
+// One warp per token and `each` of its key/value heads, one after the other:
+// their key rows and value rows, four elements a lane.
 template <int kD, bool kFour>
 __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int N = kD / 128;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (w >= p.rows) return;
-  const int head = static_cast<int>(w % p.v.n_kv), tok = static_cast<int>(w / p.v.n_kv);
-  const int s = tok / p.p.ntok, i = tok - s * p.p.ntok;
-  const int64_t from = s * p.seq_ld + i * p.ld + head * kD;
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (w >= p.warps) return;
+  const unsigned tok = w / p.groups, h0 = (w - tok * p.groups) * p.each;
+  const unsigned s = tok / p.p.ntok, i = tok - s * p.p.ntok;
+  const int64_t from = s * p.seq_ld + i * p.ld + h0 * kD + 4 * lane;
+  const float *k = p.k + from, *v = p.x + from;
   float4 x[2][N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    x[0][n] = *reinterpret_cast<const float4 *>(p.k + from + 128 * n + 4 * lane);
-    x[1][n] = *reinterpret_cast<const float4 *>(p.x + from + 128 * n + 4 * lane);
+    x[0][n] = *reinterpret_cast<const float4 *>(k + 128 * n);
+    x[1][n] = *reinterpret_cast<const float4 *>(v + 128 * n);
   }
   if (i >= tokens_of(p.p, s)) return;
   const int pos = seq_length(p.v, s) + i;
-  const int page = seq_page(p.v, s, pos / p.v.P);
+  const int page = seq_page(p.v, s, pos >> p.page_bits);
   if (page < 0) {
-    if (lane == 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(s));
+    if (lane == 0) record_error(p.err, DEVERR_NO_PAGE, s);
     return;
   }
-  bool lost = false;  // the key's position has no angle
+  const float *angles = nullptr;
   if (p.r.table) {
-    const float *angles = angles_at(p.r, place_of(p.p, s, i));
-    lost = angles == nullptr;
-    if (!lost) {
-#pragma unroll
-      for (int n = 0; n < N; ++n) rotate4<kFour>(p.r, p.k + from, 128 * n + 4 * lane, angles, x[0][n]);
-    } else if (lane == 0) {
-      record_error(p.err, DEVERR_NO_ANGLE, static_cast<unsigned>(s));
-    }
+    angles = angles_at(p.r, place_of(p.p, s, i));
+    if (!angles && lane == 0) record_error(p.err, DEVERR_NO_ANGLE, s);
   }
+  const bool lost = p.r.table && !angles;  // the keys' position has no angle
+  uint8_t *row = page_row(p.v, p.layer, page, h0, 0, pos & (p.v.P - 1));
+  for (unsigned h = h0; h < h0 + p.each; ++h, k += kD, v += kD, row += p.v.head_bytes) {
+    float4 next[2][N] = {};  // the next head's rows, while these are worked on
+    if (h + 1 < h0 + p.each) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint8_t *row = page_row(p.v, p.layer, page, head, c, pos % p.v.P);
+      for (int n = 0; n < N; ++n) {
+        next[0][n] = *reinterpret_cast<const float4 *>(k + kD + 128 * n);
+        next[1][n] = *reinterpret_cast<const float4 *>(v + kD + 128 * n);
+      }
+    }
+    if (angles) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      __half d;
-      const uint32_t word = quantize4(x[c][n], &d);
-      // the factors of four blocks, joined in lane 0
-      uint32_t f = __half_as_ushort(d);
-      if (c == 0 && lost) f = 0x7fffu;
-      f |= __shfl_down_sync(0xffffffffu, f, 8) << 16;
-      const uint32_t g = __shfl_down_sync(0xffffffffu, f, 16);
-      if (lane == 0) *reinterpret_cast<uint2 *>(row + 8 * n) = make_uint2(f, g);
-      *reinterpret_cast<uint32_t *>(row + kD / 16 + 128 * n + 4 * lane) = word;
+      for (int n = 0; n < N; ++n) rotate4<kFour>(p.r, k - 4 * lane, 128 * n + 4 * lane, angles, x[0][n]);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint8_t *to = row + c * p.plane_bytes;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        __half d;
+        const uint32_t word = quantize4(x[c][n], &d);
+        // the factors of four blocks, joined in lane 0
+        uint32_t f = c == 0 && lost ? 0x7fffu : __half_as_ushort(d);
+        f |= __shfl_down_sync(0xffffffffu, f, 8) << 16;
+        const uint32_t g = __shfl_down_sync(0xffffffffu, f, 16);
+        if (lane == 0) *reinterpret_cast<uint2 *>(to + 8 * n) = make_uint2(f, g);
+        *reinterpret_cast<uint32_t *>(to + kD / 16 + 128 * n + 4 * lane) = word;
+        x[c][n] = next[c][n];
+      }
     }
   }
 }
@@ -149,15 +161,23 @@ extern "C" epq_status epq_pages_append(const epq_pages *pages, int layer, const 
     return EPQ_ERR_ALIGN;
   p.p = {o.position, p.v.length, o.mask, o.n_tok, ntok};
   p.k = k, p.x = v, p.layer = layer;
-  p.rows = static_cast<int64_t>(p.v.n_seq) * ntok * p.v.n_kv;
   DeviceInfo dev;
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   p.err = device_error_slot();
   if (!p.err) return EPQ_ERR_DEVICE;
+  // what a token's heads share is worked out once for as many of them as leave
+  // every SM 64 warps
+  const int64_t tokens = static_cast<int64_t>(p.v.n_seq) * ntok;
+  p.each = p.v.n_kv;
+  while (p.each % 2 == 0 && tokens * (p.v.n_kv / p.each) < 64ll * dev.sm_count) p.each /= 2;
+  p.groups = p.v.n_kv / p.each;
+  p.warps = static_cast<unsigned>(tokens * p.groups);
+  p.page_bits = p.v.P == 16 ? 4 : p.v.P == 32 ? 5 : p.v.P == 64 ? 6 : 7;
+  p.plane_bytes = p.v.P * p.v.row;
   const bool four = rotates_by_four(p.r);
   void (*kernel)(AppendParams) = p.v.D == 128 ? (four ? append_kernel<128, true> : append_kernel<128, false>)
                                               : (four ? append_kernel<256, true> : append_kernel<256, false>);
-  const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>((p.rows + kWarps - 1) / kWarps)),
+  const cudaError_t e = launch_pdl(kernel, dim3((p.warps + kWarps - 1) / kWarps),
                                    dim3(32 * kWarps), 0, reinterpret_cast<cudaStream_t>(stream), p);
   return e == cudaSuccess ? EPQ_OK : cuda_fail(e);
 }

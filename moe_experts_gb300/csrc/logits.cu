@@ -6,11 +6,16 @@
 // n(v) counts the row's generated tokens v: the history behind the prompt, and
 // the drafted tokens on the row's path.  A CTA takes kChunk tokens of the
 // vocabulary for some rows of one sequence.  It goes through the history and
-// the biases once and keeps a note for each of its tokens in shared memory; only
-// the path differs between the rows, and the thread that owns a drafted token
-// adds it to its note for the row and takes it away again, so the rows need no
-// barrier.  Integer counts and a maximum of indices do not depend on the order
-// in which threads come, so the result does not either.
+// the biases once, keeps a note for each of its tokens in shared memory, and
+// lists the tokens with a note and the drafted ones.  A row is then two things
+// side by side: the tokens that are not listed, of which a thread has eight and
+// only the mask asks, and the list, a token a thread, with the penalties' division
+// and what the path adds.  (Where each thread makes up the notes of its own
+// tokens, a few of them keep all lanes of most warps dividing.)  A CTA whose
+// notes are more than its threads does that all the same, and lists the drafted
+// tokens alone: its lanes all have notes.  Integer counts and a maximum of
+// indices do not depend on the order in which threads come, and listed tokens
+// not on one another, so the result does not either.
 #include <algorithm>
 
 #include "common.cuh"
@@ -41,13 +46,13 @@ struct LogitsParams {
   int words;  // of a row of `allowed`
 };
 
-// A token's note: its count, whether the prompt has it, whether it has a bias.
-// Most are 0: the token's logit changes by the mask alone.
-constexpr uint32_t kRead = 0x80000000u, kBiased = 0x40000000u, kCount = 0x3fffffffu;
+// A token's note: its count, whether the prompt has it, whether it has a bias,
+// whether it is drafted.
+constexpr uint32_t kRead = 0x80000000u, kBiased = 0x40000000u, kDrafted = 0x20000000u, kCount = 0x1fffffffu;
 
 __device__ __forceinline__ float adjusted(float l, uint32_t w, float bias, const float (&pen)[3]) {
   if (w & kBiased) l = __fadd_rn(l, bias);
-  if (w & ~kBiased) l = l > 0.0f ? __fdiv_rn(l, pen[0]) : __fmul_rn(l, pen[0]);
+  if (w & (kRead | kCount)) l = l > 0.0f ? __fdiv_rn(l, pen[0]) : __fmul_rn(l, pen[0]);
   if (w & kCount) l = __fsub_rn(l, __fadd_rn(__fmul_rn(pen[1], static_cast<float>(w & kCount)), pen[2]));
   return l;
 }
@@ -55,11 +60,12 @@ __device__ __forceinline__ float adjusted(float l, uint32_t w, float bias, const
 // kFour: a thread has four tokens next to one another, in 16-byte words (rows
 // that begin at 16 bytes); else every 256th.
 template <bool kFour>
-__global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant__ LogitsParams p) {
-  constexpr int kEach = kChunk / kThreads;
+__global__ void __launch_bounds__(kThreads, 4) adjust_kernel(const __grid_constant__ LogitsParams p) {
+  constexpr int kEach = kChunk / kThreads, kRun = kFour ? 4 : 1;
   __shared__ __align__(16) uint32_t note[kChunk];
   __shared__ __align__(16) float added[kChunk];  // first 1 + the last bias entry (0: none), then that bias
-  __shared__ int drafted[kMaxTokens];            // the drafted tokens' places in the chunk, or -1
+  __shared__ unsigned short list[kThreads];      // places in the chunk, the drafted tokens' first
+  __shared__ int drafted[kMaxTokens], many[2];   // places of the drafted tokens, or -1; listed of them, and others
   pdl_launch_dependents();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -67,44 +73,76 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
   const int v0 = blockIdx.y * kChunk, nv = min(kChunk, p.vocab - v0);
   const int r1 = min(r0 + p.rows_per_cta, p.ntok);
   const auto place = [&](int k) { return kFour ? 4 * (tid + kThreads * (k / 4)) + k % 4 : tid + kThreads * k; };
-  const auto load = [&](int r, float (&x)[kEach]) {
-    const float *row = p.x + (static_cast<int64_t>(s) * p.ntok + r) * p.ld + v0;
-    if constexpr (kFour) {
+  const float *from = p.x + (static_cast<int64_t>(s) * p.ntok + r0) * p.ld + v0;
+  float *to = p.y + (static_cast<int64_t>(s) * p.ntok + r0) * p.out_ld + v0;
+  const uint32_t *allowed = p.allowed ? p.allowed + (static_cast<int64_t>(s) * p.ntok + r0) * p.words + v0 / 32 : nullptr;
+  const uint64_t *mask = p.mask ? p.mask + static_cast<int64_t>(s) * p.ntok + r0 : nullptr;
+  // What a thread reads of a row: its tokens' logits and words of the mask; the
+  // same of its first listed token, and the path.  The next row is read while
+  // one is worked on.
+  struct Row {
+    __align__(16) float x[kEach];
+    uint32_t in[kEach / kRun];
+    float l;
+    uint32_t l_in;
+    uint64_t path;
+  } now, ahead;
+  int at0 = -1;  // the thread's first listed token
+  const auto load = [&](Row &row, const float *from, const uint32_t *allowed) {
 #pragma unroll
-      for (int k = 0; k < kEach; k += 4)
-        if (place(k) < nv) *reinterpret_cast<float4 *>(x + k) = *reinterpret_cast<const float4 *>(row + place(k));
-    } else {
-#pragma unroll
-      for (int k = 0; k < kEach; ++k)
-        if (place(k) < nv) x[k] = row[place(k)];
+    for (int k = 0; k < kEach; k += kRun) {
+      row.in[k / kRun] = ~0u;
+      if (place(k) >= nv) continue;
+      if constexpr (kFour) *reinterpret_cast<float4 *>(row.x + k) = *reinterpret_cast<const float4 *>(from + place(k));
+      else row.x[k] = from[place(k)];
+      if (allowed) row.in[k / kRun] = allowed[place(k) >> 5];
     }
   };
-  __align__(16) float x[kEach], ahead[kEach];  // a row, and the next one while the row is worked on
-  load(r0, ahead);
+  const auto load_listed = [&](Row &row, const float *from, const uint32_t *allowed, const uint64_t *mask, int r) {
+    row.l = 0.0f, row.l_in = ~0u, row.path = ~0ull >> (63 - (r & 63));
+    if (at0 < 0) return;
+    row.l = from[at0];
+    if (allowed) row.l_in = allowed[at0 >> 5];
+    if (mask) row.path = *mask;
+  };
+  load(now, from, allowed);
   const int live = p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
   float pen[3] = {1.0f, 0.0f, 0.0f};
   if (p.penalties) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) pen[k] = p.penalties[3 * s + k];
   }
-  uint64_t mine = 0;  // the drafted tokens that this thread has
+  unsigned noted = 0, listed = 0;  // of the thread's tokens, those with a note, and those that the list has
+  uint64_t mine = 0;  // the drafted tokens that are the thread's first listed one
+  uint32_t w0 = 0;    // its note and its bias
+  float b0 = 0.0f;
   if (r0 < live) {
     int *entry = reinterpret_cast<int *>(added);
     for (int i = 4 * tid; i < kChunk; i += 4 * kThreads) {
       *reinterpret_cast<uint4 *>(note + i) = make_uint4(0, 0, 0, 0);
       *reinterpret_cast<uint4 *>(entry + i) = make_uint4(0, 0, 0, 0);
     }
+    if (tid < 2) many[tid] = 0;
+    if (tid < kMaxTokens) {
+      unsigned at = 0xffffffffu;
+      if (p.tokens && tid < live) at = static_cast<unsigned>(p.tokens[static_cast<int64_t>(s) * p.ntok + tid]) - v0;
+      drafted[tid] = at < static_cast<unsigned>(nv) ? static_cast<int>(at) : -1;
+    }
     __syncthreads();
     if (p.history) {
       const int n = p.history_len ? min(max(p.history_len[s], 0), p.max_history) : p.max_history;
       const int given = p.prompt_len ? min(max(p.prompt_len[s], 0), n) : 0;
       const int32_t *h = p.history + static_cast<int64_t>(s) * p.max_history;
-#pragma unroll 8
-      for (int i = tid; i < n; i += kThreads) {
-        const unsigned at = static_cast<unsigned>(h[i]) - v0;
-        if (at >= static_cast<unsigned>(nv)) continue;
-        if (i < given) atomicOr(&note[at], kRead);
-        else atomicAdd(&note[at], 1u);
+      for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
+        unsigned at[8];  // eight at a time on their way
+#pragma unroll
+        for (int k = 0; k < 8; ++k) at[k] = i0 + k * kThreads < n ? static_cast<unsigned>(h[i0 + k * kThreads]) - v0 : ~0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (at[k] >= static_cast<unsigned>(nv)) continue;
+          if (i0 + k * kThreads < given) atomicOr(&note[at[k]], kRead);
+          else atomicAdd(&note[at[k]], 1u);
+        }
       }
     }
     for (int i = tid; i < p.n_bias; i += kThreads) {
@@ -113,78 +151,83 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
       atomicOr(&note[at], kBiased);
       atomicMax(&entry[at], i + 1);
     }
-    if (tid < kMaxTokens) {
-      unsigned at = 0xffffffffu;
-      if (p.tokens && tid < live) at = static_cast<unsigned>(p.tokens[static_cast<int64_t>(s) * p.ntok + tid]) - v0;
-      drafted[tid] = at < static_cast<unsigned>(nv) ? static_cast<int>(at) : -1;
+    if (p.tokens && tid < kMaxTokens && drafted[tid] >= 0) {
+      bool first = true;
+      for (int j = 0; j < tid; ++j) first = first && drafted[j] != drafted[tid];
+      if (first) {
+        atomicOr(&note[drafted[tid]], kDrafted);
+        list[atomicAdd(&many[0], 1)] = static_cast<unsigned short>(drafted[tid]);
+      }
     }
     __syncthreads();
-    if (p.n_bias) {
+    const int first = many[0];
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        const int e = entry[place(k)];
-        if (e) added[place(k)] = p.bias[static_cast<int64_t>(s) * p.n_bias + e - 1];
-      }
+    for (int k = 0; k < kEach; ++k) {
+      const uint32_t w = note[place(k)];
+      if (w & ~kDrafted) noted |= 1u << k;
+      if (w & kDrafted) listed |= 1u << k;
+      if (w & kBiased) added[place(k)] = p.bias[static_cast<int64_t>(s) * p.n_bias + entry[place(k)] - 1];
     }
-    if (p.tokens) {
-#pragma unroll 8
-      for (int j = 0; j < kMaxTokens; ++j) {
-        const int at = drafted[j];
-        if (at >= 0 && (kFour ? at / 4 : at) % kThreads == tid) mine |= 1ull << j;
-      }
-    }
-  }
-  for (int r = r0; r < r1; ++r) {
-    const int64_t row = static_cast<int64_t>(s) * p.ntok + r;
-    float *y = p.y + row * p.out_ld + v0;
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) x[k] = ahead[k];
-    if (r + 1 < r1) load(r + 1, ahead);
-    if (r < live) {
-      uint64_t path = 0;
-      if (mine) {
-        path = mine & (p.mask ? p.mask[row] : ~0ull >> (63 - r));
-        for (uint64_t b = path; b; b &= b - 1) ++note[drafted[__ffsll(b) - 1]];
-      }
-      const uint32_t *allowed = p.allowed ? p.allowed + row * p.words + v0 / 32 : nullptr;
-#pragma unroll
-      for (int k = 0; k < kEach; k += 4) {
-        uint32_t w[4], in[4];
-        if constexpr (kFour) {
-          *reinterpret_cast<uint4 *>(w) = *reinterpret_cast<const uint4 *>(note + place(k));
-          const uint32_t bits = allowed && place(k) < nv ? allowed[place(k) >> 5] >> (place(k) & 31) : ~0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) in[i] = bits >> i & 1;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = place(k + i);
-            w[i] = note[at];
-            in[i] = allowed && at < nv ? allowed[at >> 5] >> (at & 31) & 1 : 1;
-          }
-        }
-        if (w[0] | w[1] | w[2] | w[3]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (w[i]) x[k + i] = adjusted(x[k + i], w[i], added[place(k + i)], pen);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!in[i]) x[k + i] = -INFINITY;
-      }
-      for (uint64_t b = path; b; b &= b - 1) --note[drafted[__ffsll(b) - 1]];
-    } else if (p.x == p.y) {
-      continue;
-    }
-    if constexpr (kFour) {
-#pragma unroll
-      for (int k = 0; k < kEach; k += 4)
-        if (place(k) < nv) *reinterpret_cast<float4 *>(y + place(k)) = *reinterpret_cast<const float4 *>(x + k);
-    } else {
+    noted &= ~listed;
+    if (noted) atomicAdd(&many[1], __popc(noted));
+    __syncthreads();
+    const bool fits = first + many[1] <= kThreads;
+    int end = first;
+    if (fits) {
+      end = first + many[1];
+      __syncthreads();  // every thread has read what is counted down here
 #pragma unroll
       for (int k = 0; k < kEach; ++k)
-        if (place(k) < nv) y[place(k)] = x[k];
+        if (noted >> k & 1) list[first - 1 + atomicSub(&many[1], 1)] = static_cast<unsigned short>(place(k));
+      listed |= noted, noted = 0;
+      __syncthreads();
     }
+    if (tid < end) at0 = list[tid], w0 = note[at0], b0 = added[at0];
+    if (tid < first)
+      for (int j = 0; j < kMaxTokens; ++j) mine |= static_cast<uint64_t>(drafted[j] == at0) << j;
+    load_listed(now, from, allowed, mask, r0);
+  }
+  const auto work = [&](int r, Row &now, Row &ahead) {
+    if (r + 1 < r1) {
+      const uint32_t *next = allowed ? allowed + p.words : nullptr;
+      load(ahead, from + p.ld, next);
+      load_listed(ahead, from + p.ld, next, mask ? mask + 1 : nullptr, r + 1);
+    }
+    if (r < live) {
+      if (at0 >= 0) {
+        const float l = adjusted(now.l, w0 + __popcll(now.path & mine), b0, pen);
+        to[at0] = now.l_in >> (at0 & 31) & 1 ? l : -INFINITY;
+      }
+      if (noted) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          if (noted >> k & 1) now.x[k] = adjusted(now.x[k], note[place(k)], added[place(k)], pen);
+      }
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (!(now.in[k / kRun] >> (place(k) & 31) & 1)) now.x[k] = -INFINITY;
+    }
+    if (r < live || p.x != p.y) {
+#pragma unroll
+      for (int k = 0; k < kEach; k += kRun) {
+        const int at = place(k);
+        if (at >= nv) continue;
+        if (kFour && (r >= live || !(listed >> k & 15))) {
+          *reinterpret_cast<float4 *>(to + at) = *reinterpret_cast<const float4 *>(now.x + k);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kRun; ++i)
+            if (r >= live || !(listed >> (k + i) & 1)) to[at + i] = now.x[k + i];
+        }
+      }
+    }
+    from += p.ld, to += p.out_ld;
+    if (allowed) allowed += p.words;
+    if (mask) ++mask;
+  };
+  for (int r = r0; r < r1; r += 2) {  // (no copy: the row ahead has the time of a whole row to come)
+    work(r, now, ahead);
+    if (r + 1 < r1) work(r + 1, ahead, now);
   }
 }
 
@@ -224,7 +267,7 @@ extern "C" epq_status epq_logits_adjust(const float *logits, int64_t vocab, int 
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int chunks = (p.vocab + kChunk - 1) / kChunk;
   // rows share the pass over the history; but all SMs have CTAs
-  const int64_t want = std::max<int64_t>(1, 5ll * dev.sm_count / chunks);  // CTAs of a chunk
+  const int64_t want = std::max<int64_t>(1, 12ll * dev.sm_count / chunks);  // CTAs of a chunk
   const int groups = static_cast<int>(std::min<int64_t>(ntok, std::max<int64_t>(1, want / n_seq)));
   p.rows_per_cta = (ntok + groups - 1) / groups;
   p.row_groups = (ntok + p.rows_per_cta - 1) / p.rows_per_cta;
