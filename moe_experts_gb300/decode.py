@@ -19,7 +19,10 @@ TreeDecoder verifies a tree of drafted tokens in one dense step over a paged
 Q8_0 cache: the drafted tokens are the GEMVs' columns, every layer appends
 their keys and values and attends over the cache and the tree, and the walk
 over the logits and the commit of the accepted rows end the step -- all of it
-queued (or captured in one graph) without a host synchronisation.
+queued (or captured in one graph) without a host synchronisation.  Its prompt
+method brings any number of tokens into the cache first; with a RopeTable the
+queries and keys of both are turned by their positions (a drafted token's is its
+depth in the tree), and a step can be given penalties, biases and a grammar.
 
 `timers` (optional) brackets each call of the first layer with a pair of
 CUDA events, so that per-kernel durations can be read after a graph replay.
@@ -236,13 +239,15 @@ class TreeDecoder:
     """A dense decoder that verifies ntok (1..8) drafted tokens per step.
 
     layers, head: packed weights as in DenseDecoder; cache: a PagedKVCache of
-    all layers (one sequence).  Token 0 of a step is the last committed token,
-    the others its drafted continuations; parent names their tree."""
+    all layers (one sequence); rope: None or a RopeTable.  Token 0 of a step is
+    the last committed token, the others its drafted continuations; parent names
+    their tree."""
 
-    def __init__(self, cfg, fmt, layers, head, cache, ntok, device):
+    def __init__(self, cfg, fmt, layers, head, cache, ntok, device, rope=None):
         if not 1 <= ntok <= 8 or cache.n_seq != 1:
             raise ValueError("1..8 drafted tokens of one sequence")
         self.cfg, self.fmt, self.layers, self.head, self.cache, self.ntok = cfg, fmt, layers, head, cache, ntok
+        self.rope = rope
         f32 = dict(dtype=torch.float32, device=device)
         i32 = dict(dtype=torch.int32, device=device)
         self.qkv = torch.empty((1, ntok, cfg.q_rows + 2 * cfg.kv_rows), **f32)
@@ -259,6 +264,49 @@ class TreeDecoder:
         self.attn_ws = L.epq_attention_tree_workspace(cache, cfg.heads, ntok)
         self.verify_ws = L.epq_verify_tree_workspace(self.logits)
 
+    def _reserve(self, extra, n_tok, stream):
+        """Room for extra rows; n_tok: as many, or 0 where there is none (status is nonzero then)."""
+        L.epq_pages_reserve(self.cache, extra, self.status, stream=stream)
+        with torch.cuda.stream(None if stream is None else L._stream_object(stream)):
+            torch.mul(extra, self.status == 0, out=n_tok)
+
+    def prompt(self, x, stream=None):
+        """x [n, H], any n >= 1 (the tokens' embeddings): their rows are appended
+        and committed -> logits [1, vocab] behind the last one.  The weights are
+        read once for every 8 tokens.  status is nonzero when the cache had no
+        room: it stays as it is then, and the logits mean nothing."""
+        c, f, H, nq, nkv, cache = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows, self.cache
+        n, new = x.shape[0], L._allocator(stream)
+        f32, i32 = dict(dtype=torch.float32, device=x.device), dict(dtype=torch.int32, device=x.device)
+        qkv, attn = new((1, n, nq + 2 * nkv), **f32), new((1, n, nq), **f32)
+        h, m, logits = new((n, H), **f32), new((n, c.inter), **f32), new((1, c.vocab), **f32)
+        extra, n_tok = new(1, **i32), new(1, **i32)
+        ws = L.epq_attention_prompt_workspace(cache, c.heads, n, stream)
+        with torch.cuda.stream(None if stream is None else L._stream_object(stream)):
+            extra.fill_(n)
+        self._reserve(extra, n_tok, stream)
+        q, k, v = qkv[..., :nq], qkv[..., nq:nq + nkv], qkv[..., nq + nkv:]
+        eight = [slice(i, min(i + 8, n)) for i in range(0, n, 8)]
+        for li, (wqkv, wo, wgu, wd) in enumerate(self.layers):
+            src = x if li == 0 else h
+            for r in eight:
+                L.epq_gemv_ex(f, wqkv, src[r], nq + 2 * nkv, H, y=qkv[0, r], rms_prenorm=True, rms_eps=c.rms_eps,
+                              weights_ready=True, stream=stream)
+            if self.rope is not None:
+                L.epq_rope(q, self.rope, c.heads, start=cache.length, n_tok=n_tok, out=q, stream=stream)
+            L.epq_pages_append(k, v, cache, li, rope=self.rope, n_tok=n_tok, stream=stream)
+            L.epq_attention_prompt(q, cache, li, c.heads, 1.0 / math.sqrt(c.head_dim), n_tok=n_tok, out=attn,
+                                   workspace=ws, stream=stream)
+            for r in eight:
+                L.epq_gemv_ex(f, wo, attn[0, r], H, nq, y=h[r], residual=src[r], weights_ready=True, stream=stream)
+                L.epq_gemv_ex(f, wgu, h[r], 2 * c.inter, H, y=m[r], rms_prenorm=True, rms_eps=c.rms_eps, swiglu=True,
+                              weights_ready=True, stream=stream)
+                L.epq_gemv_ex(f, wd, m[r], H, c.inter, y=h[r], residual=h[r], weights_ready=True, stream=stream)
+        L.epq_gemv_ex(f, self.head, h[n - 1:], c.vocab, H, y=logits, rms_prenorm=True, rms_eps=c.rms_eps,
+                      weights_ready=True, stream=stream)
+        L.epq_pages_advance(cache, n_tok, stream=stream)
+        return logits
+
     def forward(self, x, parent, stream=None):
         """x [ntok, H] (the tokens' embeddings), parent int32 [1, ntok] ->
         logits [1, ntok, vocab]; the tokens' rows lie behind the committed
@@ -266,15 +314,17 @@ class TreeDecoder:
         stored then, and the logits mean nothing."""
         c, f, H, nq, nkv = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows
         h, qkv, attn = self.h, self.qkv, self.attn
-        L.epq_pages_reserve(self.cache, self.extra, self.status, stream=stream)
-        with torch.cuda.stream(None if stream is None else L._stream_object(stream)):
-            torch.mul(self.extra, self.status == 0, out=self.n_tok)
+        self._reserve(self.extra, self.n_tok, stream)
         L.epq_tree_mask(parent, self.mask, stream=stream)
         q, k, v = qkv[..., :nq], qkv[..., nq:nq + nkv], qkv[..., nq + nkv:]
         for li, (wqkv, wo, wgu, wd) in enumerate(self.layers):
             src = x if li == 0 else h
             L.epq_gemv_ex(f, wqkv, src, nq + 2 * nkv, H, y=qkv[0], rms_prenorm=True, rms_eps=c.rms_eps,
                           weights_ready=True, stream=stream)
+            if self.rope is not None:  # query and key heads lie side by side
+                qk = qkv[..., :nq + nkv]
+                L.epq_rope(qk, self.rope, c.heads + c.kv_heads, start=self.cache.length, mask=self.mask,
+                           n_tok=self.n_tok, out=qk, stream=stream)
             L.epq_attention_tree(q, k, v, self.cache, li, c.heads, 1.0 / math.sqrt(c.head_dim), mask=self.mask,
                                  n_tok=self.n_tok, out=attn, workspace=self.attn_ws, stream=stream)
             L.epq_gemv_ex(f, wo, attn[0], H, nq, y=h, residual=src, weights_ready=True, stream=stream)
@@ -285,13 +335,18 @@ class TreeDecoder:
                       weights_ready=True, stream=stream)
         return self.logits
 
-    def step(self, x, tokens, parent, u, draft=None, temperature=1.0, stream=None):
+    def step(self, x, tokens, parent, u, draft=None, temperature=1.0, constraints=None, stream=None):
         """One verification step: forward, the walk, the commit.  tokens,
         parent int32 and u float32 [1, ntok], draft None or float32 [1, ntok,
         vocab] -> (path, n_accept, next_token); the cache then holds the
-        accepted tokens, and next_token is the root of the next step.  A cache
-        without room stays as it is: n_accept 0, next_token -1, status nonzero."""
+        accepted tokens, and next_token is the root of the next step.
+        constraints: None or arguments of epq_logits_adjust (penalties, history
+        and its lengths, biases, allowed), applied to the logits first; tokens,
+        mask and n_tok are the step's.  A cache without room stays as it is: n_accept 0, next_token -1, status nonzero."""
         self.forward(x, parent, stream=stream)
+        if constraints:
+            L.epq_logits_adjust(self.logits, tokens=tokens, mask=self.mask, n_tok=self.n_tok, out=self.logits,
+                                stream=stream, **constraints)
         L.epq_verify_tree(self.logits, tokens, parent, u, draft=draft, n_tok=self.n_tok, temperature=temperature,
                           path=self.path, n_accept=self.n_accept, next_token=self.next_token, lse=self.lse, workspace=self.verify_ws,
                           stream=stream)
