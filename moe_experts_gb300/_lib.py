@@ -823,6 +823,8 @@ def epq_attention_prompt(q: torch.Tensor, cache: PagedKVCache, layer: int, n_hea
     tokens' own rows have been stored by epq_pages_append."""
     if q.dim() != 3:
         raise ValueError("q must be [n_seq, ntok, n_heads * head_dim]")
+    if window >> 31 > 0:
+        raise ValueError("window must be below 2^31")
     ntok, at = q.shape[1], cache._at
     shape = (cache.n_seq, ntok, n_heads * cache.head_dim)
     q_seq, q_tok = _token_strides(q, "q", shape, at)

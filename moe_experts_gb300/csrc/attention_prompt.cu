@@ -157,7 +157,8 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *e
   return true;
 }
 
-// All lanes of the warp wait; the same answer for all.
+// All lanes of the warp wait; the same answer for all, so that they leave
+// together and meet in the warp-wide instructions that follow.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, unsigned *err, unsigned code, unsigned where) {
   return __all_sync(0xffffffffu, wait(bar, parity, err, code, where));
 }
@@ -237,25 +238,37 @@ __device__ __forceinline__ void find_work(const PromptParams &p, Control &c) {
   const auto units = [&](int pair, int s) {
     return span_of<kD>(p, c.seq[s].x, c.seq[s].y, pair - c.pair0[s]).tiles + kExtra;
   };
-  long long mine = 0, total;
-  for (int k = tid; k < pairs; k += kThreads) mine += units(k, find(k));
-  scan_sum(mine, c.sums, &total);
+  // the tiles of all row tiles, and those before the thread's own (of the first kThreads)
+  long long mine = 0, first = 0, total;
+  for (int k = tid; k < pairs; k += kThreads) {
+    const int each = units(k, find(k));
+    if (k == tid) first = each;
+    mine += each;
+  }
+  long long upto = scan_sum(mine, c.sums, &total);
+  const bool once = pairs <= kThreads;  // then that is the sum which the second look needs
   total *= heads;
   const long long ctas = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x < ctas) {
-    const long long share = total / ctas, rest = total % ctas, b = blockIdx.x;
+    // 32 bits, where they are enough, divide in a fraction of the time
+    const long long share = total >> 32 ? total / ctas : static_cast<unsigned>(total) / static_cast<unsigned>(ctas);
+    const long long rest = total - share * ctas, b = blockIdx.x;
     const long long begin = b * share + (b < rest ? b : rest), end = begin + share + (b < rest);
     long long run = 0;
     for (int k0 = 0; run <= begin; k0 += kThreads) {
       const int k = k0 + tid, s = k < pairs ? find(k) : 0;
-      const long long each = k < pairs ? units(k, s) : 0;
-      long long all;
-      const long long upto = run + heads * scan_sum(each, c.sums, &all), from = upto - heads * each;
-      run += heads * all;
-      if (from <= begin && begin < upto) {
+      long long each = first, all = 0;
+      if (!once) {
+        each = k < pairs ? units(k, s) : 0;
+        upto = scan_sum(each, c.sums, &all);
+      }
+      const long long to = run + heads * upto, from = to - heads * each;
+      run = once ? total : run + heads * all;
+      if (from <= begin && begin < to) {
+        const long long at = begin - from;
         c.s = s, c.rt = k - c.pair0[s];
-        c.y = static_cast<int>((begin - from) / each);
-        c.tile = static_cast<int>((begin - from) % each);
+        c.y = static_cast<int>(at >> 32 ? at / each : static_cast<unsigned>(at) / static_cast<unsigned>(each));
+        c.tile = static_cast<int>(at - c.y * each);
         c.begin = begin, c.end = end;
       }
     }
@@ -305,8 +318,11 @@ struct Walk {
 
 // Item n of the walk, once it is known.  A role that has what it needs of it
 // gives the place back (one arrival a warp).
+template <bool kWarp = true>
 __device__ __forceinline__ bool item_at(const PromptParams &p, Control &c, int n, Item &x) {
-  if (!wait(&c.item_full[n % kItems], (n / kItems) & 1, p.err, DEVERR_FULL_WAIT, n)) return false;
+  uint64_t *bar = &c.item_full[n % kItems];
+  const int phase = (n / kItems) & 1;
+  if (!(kWarp ? wait_warp(bar, phase, p.err, DEVERR_FULL_WAIT, n) : wait(bar, phase, p.err, DEVERR_FULL_WAIT, n))) return false;
   x = c.item[n % kItems];
   return x.tiles > 0;
 }
@@ -463,7 +479,10 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
         }
         any |= p0 + t + 64 * m < it.end && (!read[m] || bad[m]);
       }
-      if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) return;
+      if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) {
+        asm volatile("bar.arrive 1, 64;" ::: "memory");  // the other warp may have gone on to the barrier below
+        return;
+      }
       // the largest of both warps: of the keys, and of the values by block
       uint32_t most[5];
       most[4] = max(kmax & 0xffffu, kmax >> 16);
@@ -560,10 +579,10 @@ __device__ void operands_role(const PromptParams &p, Control &c, uint8_t *smem) 
       for (int x = 0; x < 2; ++x) {  // keys of tile g, then values of the tile before
         const int t = x ? last : g;
         if (x ? last < 0 : !more) continue;
-        if (!x && !wait(&c.scan_full[t % kAhead], (t / kAhead) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
-        if (!wait(&c.raw_full[x][t % kRaw], (t / kRaw) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
+        if (!x && !wait_warp(&c.scan_full[t % kAhead], (t / kAhead) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
+        if (!wait_warp(&c.raw_full[x][t % kRaw], (t / kRaw) & 1, p.err, DEVERR_FULL_WAIT, t)) return;
         // the tile before t has its scores (its products with the values are done): its place is free
-        if (t > 0 && !wait(x ? &c.t_full : &c.s_full[(t - 1) & 1], (x ? t - 1 : (t - 1) >> 1) & 1, p.err, DEVERR_EMPTY_WAIT, t))
+        if (t > 0 && !wait_warp(x ? &c.t_full : &c.s_full[(t - 1) & 1], (x ? t - 1 : (t - 1) >> 1) & 1, p.err, DEVERR_EMPTY_WAIT, t))
           return;
         const Piece &m = piece[x];
         const Entry &e = c.entry[t % kAhead];
@@ -605,7 +624,7 @@ __device__ bool products(const PromptParams &p, Control &c, uint32_t smem) {
   constexpr uint32_t kScores = mma_f16_shape<kPos, false>(), kValues = mma_f16_shape<kCols, true>();
   const uint32_t tm = c.tmem;
   Item it;
-  for (int m = 0; item_at(p, c, m, it); ++m) {
+  for (int m = 0; item_at<false>(p, c, m, it); ++m) {
     mbar_arrive(&c.item_free[m % kItems]);
     const int n = it.tiles;
     if (!wait(&c.q_full, m & 1, p.err, DEVERR_FULL_WAIT, m)) return false;
@@ -764,13 +783,13 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
     for (int k = 0; k < it.tiles; ++k) {
       const int g = it.before + k, p0 = it.p0 + k * kPos;
       const uint32_t s = tm + S::kS + (g & 1) * kPos;
-      if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait_warp(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const Entry &e = c.entry[g % kAhead];
       float mul = row_mul * e.kmul;
       // some position of the tile is not for all rows
       const bool masked =
           p0 + kPos - 1 > it.len + it.t0 || (p.window && p0 <= it.len + it.t1 - p.window) || e.any;
-      if (!wait(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait_warp(&c.s_full[g & 1], (g >> 1) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       tmem_fence_after();
       float up_to = -INFINITY;
       if (masked) {
@@ -831,7 +850,7 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
       mbar_arrive(&c.c_full[g % kAhead]);
       mbar_arrive(&c.p_full[g & 1]);
     }
-    if (n > 0 && !wait(&c.fin_empty, (n - 1) & 1, p.err, DEVERR_EMPTY_WAIT, n)) return;
+    if (n > 0 && !wait_warp(&c.fin_empty, (n - 1) & 1, p.err, DEVERR_EMPTY_WAIT, n)) return;
     c.off[row] = top == -INFINITY ? -INFINITY : off;
     c.den[row] = den;
     mbar_arrive(&c.fin_full);
@@ -845,7 +864,7 @@ __device__ void output_role(const PromptParams &p, Control &c) {
   const int row = threadIdx.x & 127;
   const uint32_t tm = c.tmem + (static_cast<uint32_t>(row & ~31) << 16) + S::kT;
   for (int n = 0;; ++n) {
-    if (!wait(&c.item_full[n % kItems], (n / kItems) & 1, p.err, DEVERR_FULL_WAIT, n)) return;
+    if (!wait_warp(&c.item_full[n % kItems], (n / kItems) & 1, p.err, DEVERR_FULL_WAIT, n)) return;
     const Item &it = c.item[n % kItems];  // kept until the end
     const int tiles = it.tiles, begin = it.before;
     if (tiles == 0) return;
@@ -854,14 +873,13 @@ __device__ void output_role(const PromptParams &p, Control &c) {
     for (int i = 0; i < kCols / 2; ++i) o[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
     for (int g = begin; g < begin + tiles; ++g) {
-      if (!wait(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
-      if (!wait(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait_warp(&c.c_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const float keep = c.corr[g % kAhead][row];
       const Entry &e = c.entry[g % kAhead];
       float mul[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) mul[b] = e.vmul[b];
-      if (!wait(&c.t_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
+      if (!wait_warp(&c.t_full, g & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       tmem_fence_after();
       if (!__all_sync(0xffffffffu, keep == 1.0f)) {
         const float2 keep2 = make_float2(keep, keep), none = make_float2(0.0f, 0.0f);
@@ -881,7 +899,7 @@ __device__ void output_role(const PromptParams &p, Control &c) {
       mbar_arrive(&c.t_free);
       mbar_arrive(&c.entry_free[g % kAhead]);
     }
-    if (!wait(&c.fin_full, n & 1, p.err, DEVERR_FULL_WAIT, n)) return;
+    if (!wait_warp(&c.fin_full, n & 1, p.err, DEVERR_FULL_WAIT, n)) return;
     const float off = c.off[row], den = c.den[row];
     mbar_arrive(&c.fin_empty);
     const int r = it.rt * kRows + row;

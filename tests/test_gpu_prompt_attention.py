@@ -131,6 +131,8 @@ SHAPES = [
     ([8193], [3], 8, 2, 128, 64, 0),
     ([20000, 0, 17], [1, 1, 1], 32, 8, 128, 64, 0),
     ([9000], [20], 16, 4, 256, 128, 5000),
+    ([i % 7 * 3 for i in range(256)], [20 + i % 3 for i in range(256)], 16, 1, 128, 16, 0),  # 768 row tiles: more than a CTA has threads
+    ([0, 5], [10500, 10400], 4, 1, 128, 128, 200),  # the same of two sequences
 ]
 
 
