@@ -26,38 +26,57 @@ struct AppendParams {
   unsigned *err;
 };
 
-// The rotation of elements e .. e + 3 of a head's row `x` (`a` holds them).
-// kFour: pairs, cosines and sines lie in 16-byte words.
-template <bool kFour>
-__device__ __forceinline__ void rotate4(const RotationView &r, const float *x, int e, const float *angles, float4 &a) {
+// What turns elements e .. e + 3 of a head: y = x c + partner s, each product
+// and the sum rounded (the sign of the formula's difference is in s).  kFour:
+// pairs, cosines and sines lie in 16-byte words, and are the same for all heads.
+struct Turn {
+  float c[4], s[4];
+  int partner;  // of the first element, relative to it; 1: the partners are among the four; 0: nothing is turned
+};
+
+__device__ __forceinline__ Turn turn_of(const RotationView &r, int e, const float *angles) {
+  Turn t;
   const int at = e - r.first, half = r.rot / 2;
-  if constexpr (kFour) {
-    if (at < 0 || at >= r.rot) return;
-    if (r.interleaved) {
-      const float4 t = *reinterpret_cast<const float4 *>(angles + at);
-      a = make_float4(turned(a.x, a.y, t.x, t.y, false), turned(a.y, a.x, t.x, t.y, true),
-                      turned(a.z, a.w, t.z, t.w, false), turned(a.w, a.z, t.z, t.w, true));
-    } else {
-      const bool up = at >= half;
-      const float4 b = *reinterpret_cast<const float4 *>(x + (up ? e - half : e + half));
-      const float *cs = angles + 2 * (up ? at - half : at);
-      const float4 t = *reinterpret_cast<const float4 *>(cs), w = *reinterpret_cast<const float4 *>(cs + 4);
-      a = make_float4(turned(a.x, b.x, t.x, t.y, up), turned(a.y, b.y, t.z, t.w, up), turned(a.z, b.z, w.x, w.y, up),
-                      turned(a.w, b.w, w.z, w.w, up));
-    }
+  t.partner = 0;
+  if (!angles || at < 0 || at >= r.rot) return t;
+  if (r.interleaved) {
+    const float4 a = *reinterpret_cast<const float4 *>(angles + at);
+    t.c[0] = t.c[1] = a.x, t.s[0] = -a.y, t.s[1] = a.y, t.c[2] = t.c[3] = a.z, t.s[2] = -a.w, t.s[3] = a.w;
+    t.partner = 1;
   } else {
-    float y[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const int i = at + n;
-      if (i < 0 || i >= r.rot) continue;
-      const bool up = r.interleaved ? i & 1 : i >= half;
-      const int j = r.interleaved ? i >> 1 : up ? i - half : i;
-      const int gap = r.interleaved ? 1 : half;
-      y[n] = turned(y[n], x[up ? e + n - gap : e + n + gap], angles[2 * j], angles[2 * j + 1], up);
-    }
-    a = make_float4(y[0], y[1], y[2], y[3]);
+    const bool up = at >= half;
+    const float *cs = angles + 2 * (up ? at - half : at);
+    const float4 a = *reinterpret_cast<const float4 *>(cs), b = *reinterpret_cast<const float4 *>(cs + 4);
+    t.c[0] = a.x, t.c[1] = a.z, t.c[2] = b.x, t.c[3] = b.z;
+    t.s[0] = up ? a.y : -a.y, t.s[1] = up ? a.w : -a.w, t.s[2] = up ? b.y : -b.y, t.s[3] = up ? b.w : -b.w;
+    t.partner = up ? -half : half;
   }
+  return t;
+}
+
+// x: where the four elements `a` lie.
+__device__ __forceinline__ float4 turned4(const Turn &t, const float *x, float4 a) {
+  if (t.partner == 0) return a;
+  float4 b = make_float4(a.y, a.x, a.w, a.z);
+  if (t.partner != 1) b = *reinterpret_cast<const float4 *>(x + t.partner);
+  const auto f = [&](float u, float v, int i) { return __fadd_rn(__fmul_rn(u, t.c[i]), __fmul_rn(v, t.s[i])); };
+  return make_float4(f(a.x, b.x, 0), f(a.y, b.y, 1), f(a.z, b.z, 2), f(a.w, b.w, 3));
+}
+
+// The same where pairs lie anywhere: x is the head's row, `a` its elements e .. e + 3.
+__device__ __forceinline__ float4 turned_any(const RotationView &r, const float *x, int e, const float *angles, float4 a) {
+  const int half = r.rot / 2;
+  float y[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int i = e - r.first + n;
+    if (i < 0 || i >= r.rot) continue;
+    const bool up = r.interleaved ? i & 1 : i >= half;
+    const int j = r.interleaved ? i >> 1 : up ? i - half : i;
+    const int gap = r.interleaved ? 1 : half;
+    y[n] = turned(y[n], x[up ? e + n - gap : e + n + gap], angles[2 * j], angles[2 * j + 1], up);
+  }
+  return make_float4(y[0], y[1], y[2], y[3]);
 }
 
 // One warp per token and `each` of its key/value heads, one after the other:
@@ -94,6 +113,11 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
   }
   const bool lost = p.r.table && !angles;  // the keys' position has no angle
   uint8_t *row = page_row(p.v, p.layer, page, h0, 0, pos & (p.v.P - 1));
+  Turn turn[N];
+  if constexpr (kFour) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) turn[n] = turn_of(p.r, 128 * n + 4 * lane, angles);
+  }
   for (unsigned h = h0; h < h0 + p.each; ++h, k += kD, v += kD, row += p.v.head_bytes) {
     float4 next[2][N] = {};  // the next head's rows, while these are worked on
     if (h + 1 < h0 + p.each) {
@@ -103,9 +127,10 @@ __global__ void __launch_bounds__(32 * kWarps) append_kernel(const __grid_consta
         next[1][n] = *reinterpret_cast<const float4 *>(v + kD + 128 * n);
       }
     }
-    if (angles) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) rotate4<kFour>(p.r, k - 4 * lane, 128 * n + 4 * lane, angles, x[0][n]);
+    for (int n = 0; n < N; ++n) {
+      if constexpr (kFour) x[0][n] = turned4(turn[n], k + 128 * n, x[0][n]);
+      else if (angles) x[0][n] = turned_any(p.r, k - 4 * lane, 128 * n + 4 * lane, angles, x[0][n]);
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {

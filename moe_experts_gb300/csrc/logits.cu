@@ -50,10 +50,27 @@ struct LogitsParams {
 // whether it is drafted.
 constexpr uint32_t kRead = 0x80000000u, kBiased = 0x40000000u, kDrafted = 0x20000000u, kCount = 0x1fffffffu;
 
-__device__ __forceinline__ float adjusted(float l, uint32_t w, float bias, const float (&pen)[3]) {
+struct Penalties {
+  float repetition, frequency, presence;
+  float inverse;  // of the repetition; 0 where it is out of the range in which quotients are corrected
+};
+
+// l / r, rounded once.  The quotient by the rounded reciprocal is off by at most
+// 1.5 units; one correction by its remainder brings it within one, and from there
+// the second one rounds as the division does (Markstein).  A CTA whose tokens
+// mostly have a note divides eight times a thread and row.
+__device__ __forceinline__ float over(float l, const Penalties &p) {
+  float q = __fmul_rn(l, p.inverse);
+  if (!(q > 0x1p-60f && q < 0x1p60f)) return __fdiv_rn(l, p.repetition);
+  q = fmaf(fmaf(-p.repetition, q, l), p.inverse, q);
+  return fmaf(fmaf(-p.repetition, q, l), p.inverse, q);
+}
+
+__device__ __forceinline__ float adjusted(float l, uint32_t w, float bias, const Penalties &p) {
   if (w & kBiased) l = __fadd_rn(l, bias);
-  if (w & (kRead | kCount)) l = l > 0.0f ? __fdiv_rn(l, pen[0]) : __fmul_rn(l, pen[0]);
-  if (w & kCount) l = __fsub_rn(l, __fadd_rn(__fmul_rn(pen[1], static_cast<float>(w & kCount)), pen[2]));
+  if (w & (kRead | kCount)) l = l > 0.0f ? over(l, p) : __fmul_rn(l, p.repetition);
+  if (w & kCount)
+    l = __fsub_rn(l, __fadd_rn(__fmul_rn(p.frequency, static_cast<float>(w & kCount)), p.presence));
   return l;
 }
 
@@ -106,11 +123,23 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_kernel(const __grid_consta
     if (mask) row.path = *mask;
   };
   load(now, from, allowed);
-  const int live = p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
-  float pen[3] = {1.0f, 0.0f, 0.0f};
-  if (p.penalties) {
+  // all that the CTA has to know is asked for at once; a first look at the history
+  // does not wait for its length
+  constexpr int kLook = 16;
+  const int32_t *h = p.history + static_cast<int64_t>(s) * p.max_history;
+  unsigned look[kLook];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) pen[k] = p.penalties[3 * s + k];
+  for (int k = 0; k < kLook; ++k) look[k] = p.history && tid + k * kThreads < p.max_history ? static_cast<unsigned>(h[tid + k * kThreads]) : ~0u;
+  const int32_t *ids = p.bias_ids + static_cast<int64_t>(s) * p.n_bias;
+  const unsigned id0 = tid < p.n_bias ? static_cast<unsigned>(ids[tid]) : ~0u;
+  const unsigned token = p.tokens && tid < p.ntok ? static_cast<unsigned>(p.tokens[static_cast<int64_t>(s) * p.ntok + tid]) : ~0u;
+  const int length = p.history_len ? min(max(p.history_len[s], 0), p.max_history) : p.max_history;
+  const int given = p.prompt_len ? min(max(p.prompt_len[s], 0), length) : 0;
+  const int live = p.n_tok ? min(max(p.n_tok[s], 0), p.ntok) : p.ntok;
+  Penalties pen = {1.0f, 0.0f, 0.0f, 1.0f};
+  if (p.penalties) {
+    pen = {p.penalties[3 * s], p.penalties[3 * s + 1], p.penalties[3 * s + 2], 0.0f};
+    if (pen.repetition > 0x1p-30f && pen.repetition < 0x1p30f) pen.inverse = __frcp_rn(pen.repetition);
   }
   unsigned noted = 0, listed = 0;  // of the thread's tokens, those with a note, and those that the list has
   uint64_t mine = 0;  // the drafted tokens that are the thread's first listed one
@@ -124,29 +153,27 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_kernel(const __grid_consta
     }
     if (tid < 2) many[tid] = 0;
     if (tid < kMaxTokens) {
-      unsigned at = 0xffffffffu;
-      if (p.tokens && tid < live) at = static_cast<unsigned>(p.tokens[static_cast<int64_t>(s) * p.ntok + tid]) - v0;
+      const unsigned at = tid < live ? token - v0 : ~0u;
       drafted[tid] = at < static_cast<unsigned>(nv) ? static_cast<int>(at) : -1;
     }
     __syncthreads();
     if (p.history) {
-      const int n = p.history_len ? min(max(p.history_len[s], 0), p.max_history) : p.max_history;
-      const int given = p.prompt_len ? min(max(p.prompt_len[s], 0), n) : 0;
-      const int32_t *h = p.history + static_cast<int64_t>(s) * p.max_history;
-      for (int i0 = tid; i0 < n; i0 += 8 * kThreads) {
-        unsigned at[8];  // eight at a time on their way
+      for (int i0 = tid; i0 < length; i0 += kLook * kThreads) {
+        if (i0 != tid) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) at[k] = i0 + k * kThreads < n ? static_cast<unsigned>(h[i0 + k * kThreads]) - v0 : ~0u;
+          for (int k = 0; k < kLook; ++k) look[k] = i0 + k * kThreads < length ? static_cast<unsigned>(h[i0 + k * kThreads]) : ~0u;
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (at[k] >= static_cast<unsigned>(nv)) continue;
-          if (i0 + k * kThreads < given) atomicOr(&note[at[k]], kRead);
-          else atomicAdd(&note[at[k]], 1u);
+        for (int k = 0; k < kLook; ++k) {
+          const unsigned at = look[k] - v0;
+          if (i0 + k * kThreads >= length || at >= static_cast<unsigned>(nv)) continue;
+          if (i0 + k * kThreads < given) atomicOr(&note[at], kRead);
+          else atomicAdd(&note[at], 1u);
         }
       }
     }
     for (int i = tid; i < p.n_bias; i += kThreads) {
-      const unsigned at = static_cast<unsigned>(p.bias_ids[static_cast<int64_t>(s) * p.n_bias + i]) - v0;
+      const unsigned at = (i == tid ? id0 : static_cast<unsigned>(ids[i])) - v0;
       if (at >= static_cast<unsigned>(nv)) continue;
       atomicOr(&note[at], kBiased);
       atomicMax(&entry[at], i + 1);
@@ -267,7 +294,7 @@ extern "C" epq_status epq_logits_adjust(const float *logits, int64_t vocab, int 
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int chunks = (p.vocab + kChunk - 1) / kChunk;
   // rows share the pass over the history; but all SMs have CTAs
-  const int64_t want = std::max<int64_t>(1, 12ll * dev.sm_count / chunks);  // CTAs of a chunk
+  const int64_t want = std::max<int64_t>(1, 8ll * dev.sm_count / chunks);  // CTAs of a chunk
   const int groups = static_cast<int>(std::min<int64_t>(ntok, std::max<int64_t>(1, want / n_seq)));
   p.rows_per_cta = (ntok + groups - 1) / groups;
   p.row_groups = (ntok + p.rows_per_cta - 1) / p.rows_per_cta;

@@ -103,40 +103,48 @@ __device__ __forceinline__ uint8_t *page_row(const PagesView &v, int layer, int 
          static_cast<int64_t>(c * v.P + slot) * v.row;
 }
 
+// a / 127 rounded once: the product with the rounded reciprocal, corrected by its
+// own remainder (Markstein's division; exact for the a whose quotient is not 0 as
+// a half).
+__device__ __forceinline__ float over_127(float a) {
+  constexpr float kInverse = 1.0f / 127.0f;
+  const float q = __fmul_rn(a, kInverse);
+  return a < INFINITY ? fmaf(fmaf(-127.0f, q, a), kInverse, q) : a;
+}
+
 // Q8_0 with the packer's arithmetic (factor fp16(max|x| / 127), codes rint(x /
 // factor) in +-127, 0 for a zero factor) of 4 elements a lane, 8 lanes a block.
-// x times the factor's reciprocal is off by 2^-23 of it, 2^-16 at a code of
-// 127.5, and the rounded quotient by half of that: where the product is not
-// within 2^-15 of the middle between two codes, it has the quotient's code.
-// The others (and NaN) are divided.
+// x times the factor's approximate reciprocal is off by 2^-23 + 2^-24 of it, and
+// the rounded quotient by 2^-24: 2^-15 in all at a code of 127.  Where the
+// product is further than 2^-14 from the middle between two codes, it has the
+// quotient's code, which adding 1.5 2^23 leaves in the low byte.  The others,
+// codes past 127 and NaN are divided.
 __device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
   const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
   float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
 #pragma unroll
   for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
-  const __half dh = __float2half_rn(__fdiv_rn(a, 127.0f));
+  const __half dh = __float2half_rn(over_127(a));
   const float d = __half2float(dh);
-  const float inverse = __frcp_rn(d);
-  float y[4];
-  bool sure = true;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float t = __fmul_rn(e[j], inverse);
-    y[j] = rintf(t);
-    sure = sure && fabsf(t - y[j]) < 0.5f - 0x1p-15f;
-  }
-  if (!sure && d != 0.0f) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = rintf(__fdiv_rn(e[j], d));
-  }
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float z = d != 0.0f ? fminf(fmaxf(y[j], -127.0f), 127.0f) : 0.0f;
-    word |= (static_cast<uint32_t>(static_cast<int>(z)) & 0xffu) << (8 * j);
-  }
   *factor = dh;
-  return word;
+  float inverse;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(d));
+  uint32_t code[4];
+  bool sure = d != 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float t = __fmul_rn(e[j], inverse), r = __fadd_rn(t, 12582912.0f);
+    code[j] = __float_as_uint(r);
+    sure = sure && fabsf(__fsub_rn(t, __fsub_rn(r, 12582912.0f))) < 0.5f - 0x1p-14f && fabsf(t) < 127.25f;
+  }
+  if (!sure) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float y = d != 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(e[j], d)), -127.0f), 127.0f) : 0.0f;
+      code[j] = static_cast<uint32_t>(static_cast<int>(y));
+    }
+  }
+  return __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
 }
 #endif
 

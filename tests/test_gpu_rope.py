@@ -283,3 +283,21 @@ def test_advance_bounds(epq_lib):
     c = _cache(epq_lib, 1, 1, 128, 16, [0, 40, 3], 8, 11)
     epq_lib.epq_pages_advance(c, _i32([2**31 - 1, -5, 4], "cuda"))
     assert c.length.tolist() == [c.max_pages * 16, 40, 7]
+
+
+def test_append_near_ties(epq_lib):
+    """Elements at and next to the middle between two codes, over all mantissas of a factor and its exponents, subnormal
+    halves too: the packer's bytes."""
+    g = torch.Generator().manual_seed(3)
+    n = 4096
+    d = ((1024 + torch.randint(0, 1024, (n * 4,), generator=g)) * 2.0 ** torch.randint(-24, 5, (n * 4,), generator=g)).half()
+    d[:256] = (torch.arange(1, 257) * 2.0 ** -24).half()
+    x = (torch.randint(-127, 127, (n * 4, 32), generator=g) + 0.5).float() * d.float()[:, None]
+    x = (x.view(torch.int32) + torch.randint(-3, 4, x.shape, generator=g, dtype=torch.int32)).view(torch.float32)
+    x[:, 0] = 127.0 * d.float()
+    x[1::7, 0] *= 1.0 + 2.0 ** -12  # a factor that is rounded down: codes past 127
+    x = x.view(1, n, 128)
+    c = _cache(epq_lib, 1, 1, 128, 128, [0], n, 13)
+    epq_lib.epq_pages_append(x.cuda(), x.flip(1).contiguous().cuda(), c, 0)
+    rows = c.pool[0, c.table[0, : n // 128].long(), 0].transpose(0, 1).reshape(2, n, 136).cpu().numpy()
+    assert np.array_equal(rows[0], _rows(x[0].numpy())) and np.array_equal(rows[1], _rows(x[0].flip(0).numpy()))
