@@ -8,7 +8,9 @@
  * (router softmax + top-K, gate/up with SwiGLU, down, weighted combine plus
  * residual); attention over a Q8_0 key/value cache for one token, and for a
  * tree of drafted tokens over pages that sequences share, with the acceptance
- * of the drafted tokens and the pages' upkeep.
+ * of the drafted tokens and the pages' upkeep; rotary positions, a prompt's
+ * rows appended to the pages and their attention; biases, penalties and grammar
+ * masks on logits.
  *
  * Sources, cited by page title and section:
  *   [H]  "端侧推理：llama.cpp 与 GGUF、MLX、ExecuTorch" (edge-inference handbook),
@@ -723,7 +725,13 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  * Requirements: n_seq * ntok < 2^24, n_heads a multiple of n_kv_heads, at most
  * 16 heads per key/value head, scale > 0 and finite, finite q.  A key or value
  * row with a factor that is not finite makes the outputs of the tokens that
- * attend to it NaN, in the heads that read it, and changes no other output. */
+ * attend to it NaN, in the heads that read it, and changes no other output.
+ * Operands are two fp16 parts each, sums float32: a score is off by some 2^-20
+ * of scale * sum |q||k|, an output by some 2^-19 of sum w|v| (w the weights)
+ * beside what its scores make of that; and there are floors: a weight is off by
+ * up to 2^-39 of its row's largest, and a value whose factor is below 2^-21 of
+ * the largest that its 32 columns have among the 128 positions around it (64
+ * for heads of 256) by up to 2^-32 of that.  Two launches. */
 epq_status epq_attention_prompt(const epq_pages *pages, int layer, const float *q, int n_heads, int ntok, float scale,
                                 const epq_attention_prompt_opts *opts, float *out, void *ws, size_t ws_bytes,
                                 epq_stream_t stream);

