@@ -501,6 +501,13 @@ def _queue(stream, at):
     return _raw_stream(at) if stream is None and type(at) is int and _raw_stream is not None else _stream(stream)
 
 
+def _launch_on(stream, at):
+    """_queue, where host tensors are refused on a machine whose GPU would be given their addresses."""
+    if type(at) is not int and torch.cuda.is_available():
+        raise ValueError(f"the tensors are on {at}, not on a GPU")
+    return _queue(stream, at)
+
+
 def _scratch(t, at):
     """A workspace: its address and bytes."""
     if t.get_device() != at or not t.is_contiguous():
@@ -723,7 +730,7 @@ class RopeTable:
         freq = freq.to(device)
         table = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
         _check("epq_rope_table", load().epq_rope_table(freq.data_ptr(), rot_dim, magnitude, n_pos, table.data_ptr(),
-                                                       _queue(None, _place(table))))
+                                                       _launch_on(None, _place(table))))
         self._bind(table, first, interleaved)
 
     @classmethod
@@ -768,7 +775,7 @@ def epq_rope(x: torch.Tensor, rope: RopeTable, n_heads: int, position: torch.Ten
                  None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
                  None if n_tok is None else _need(n_tok, "n_tok", i32, (nseq,), at), x_tok, x_seq, y_tok, y_seq)
     st = _lib.epq_rope(rope._ref, x.data_ptr(), out.data_ptr(), nseq, ntok, n_heads, width // n_heads,
-                       ctypes.byref(o), _queue(stream, at))
+                       ctypes.byref(o), _launch_on(stream, at))
     if st:
         raise EpqError("epq_rope", st)
     return out
@@ -794,7 +801,7 @@ def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, laye
                    None if mask is None else _need(mask, "mask", torch.int64, (nseq, ntok), at),
                    None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at), kv_tok, kv_seq)
     st = _lib.epq_pages_append(cache._ref, layer, k.data_ptr(), v.data_ptr(), ntok, ctypes.byref(o),
-                               _queue(stream, at))
+                               _launch_on(stream, at))
     if st:
         raise EpqError("epq_pages_append", st)
 
@@ -802,7 +809,7 @@ def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, laye
 def epq_pages_advance(cache: PagedKVCache, n: torch.Tensor, stream=None) -> None:
     """Commit n (int32 [n_seq]) appended positions of every sequence."""
     at = cache._at
-    st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _queue(stream, at))
+    st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _launch_on(stream, at))
     if st:
         raise EpqError("epq_pages_advance", st)
 
@@ -834,7 +841,7 @@ def epq_attention_prompt(q: torch.Tensor, cache: PagedKVCache, layer: int, n_hea
     o = PromptOpts(None if n_tok is None else _need(n_tok, "n_tok", torch.int32, cache._per_seq, at), window, q_tok,
                    q_seq)
     st = _lib.epq_attention_prompt(cache._ref, layer, q.data_ptr(), n_heads, ntok, scale, ctypes.byref(o), out_at,
-                                   *_scratch(workspace, at), _queue(stream, at))
+                                   *_scratch(workspace, at), _launch_on(stream, at))
     if st:
         raise EpqError("epq_attention_prompt", st)
     return out
@@ -876,7 +883,7 @@ def epq_logits_adjust(logits: torch.Tensor, penalties: torch.Tensor | None = Non
                    None if bias is None else _need(bias, "bias", f32, (nseq, nb), at), nb,
                    None if allowed is None else _need(allowed, "allowed", i32, (nseq, ntok, (vocab + 31) // 32), at),
                    0, 0)
-    st = load().epq_logits_adjust(src, vocab, nseq, ntok, ctypes.byref(o), dst, _queue(stream, at))
+    st = load().epq_logits_adjust(src, vocab, nseq, ntok, ctypes.byref(o), dst, _launch_on(stream, at))
     if st:
         raise EpqError("epq_logits_adjust", st)
     return out

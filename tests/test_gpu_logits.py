@@ -206,3 +206,51 @@ def test_graph_and_verify(epq_lib):
             toks = [int(a["tokens"][s, i]) for i in rows[1:]] + [int(nxt[s])]
             for row, t in zip(rows, toks):
                 assert bits[s, row, t // 32] >> (t % 32) & 1
+
+
+def test_many_sequences_and_empty_lists(epq_lib):
+    """More sequences than a tree has tokens; histories and biases of no entries."""
+    a = _inputs(300, 2, 70, 9, 3, seed=13)
+    _same(_run(epq_lib, **a), _reference(**a))
+    x = torch.randn(2, 3, 500, device="cuda")
+    none = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    got = epq_lib.epq_logits_adjust(x, torch.full((2, 3), 2.0, device="cuda"), none, bias_ids=none, bias=none.float())
+    assert torch.equal(got, x)
+
+
+@pytest.mark.parametrize("r", [1e-12, 1e12, 3.0000002, 1e-3])
+def test_quotients(epq_lib, r):
+    """Logits from the smallest to the largest numbers over penalties of any size: the division's quotients."""
+    rng = np.random.default_rng(5)
+    n = 60000
+    x = (2.0 ** rng.uniform(-140, 127, n) * rng.choice([-1.0, 1.0], n)).astype(F).reshape(1, 1, n)
+    pen = np.array([[r, 0.0, 0.0]], dtype=F)
+    hist = np.arange(n, dtype=np.int32).reshape(1, n)
+    with np.errstate(all="ignore"):
+        want = np.where(x > 0, x / F(r), x * F(r)).astype(F) - F(0)
+    assert np.array_equal(_run(epq_lib, x, pen, hist), want)
+
+
+def test_long_lists_in_one_chunk(epq_lib):
+    """Lists longer than a CTA has threads, with drafted tokens among them, and just as long."""
+    rng = np.random.default_rng(6)
+    for m in (255, 256, 257, 600, 2048):
+        hist = np.concatenate([rng.permutation(2048)[:m], np.full(20, 5)]).astype(np.int32).reshape(1, -1)
+        x = rng.standard_normal((1, 8, 4000)).astype(F)
+        tok = rng.integers(0, 2048, (1, 8)).astype(np.int32)
+        tok[0, 3] = tok[0, 1]
+        a = dict(x=x, pen=np.array([[1.7, 0.3, 0.2]], dtype=F), hist=hist, plen=np.array([m // 3], dtype=np.int32), tokens=tok,
+                 ids=rng.integers(0, 4000, (1, 50)).astype(np.int32), bias=rng.standard_normal((1, 50)).astype(F))
+        _same(_run(epq_lib, **a), _reference(**a))
+
+
+def test_two_at_once(epq_lib):
+    a, b = _inputs(4, 16, 9000, 500, 20, seed=15), _inputs(2, 5, 7001, 100, 3, seed=16)
+    args = [[_gpu(c.get(k)) for k in ("x", "pen", "hist", "hlen", "plen", "tokens", "mask", "n_tok", "ids", "bias", "allowed")] for c in (a, b)]
+    want = [epq_lib.epq_logits_adjust(*x) for x in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    got = [[epq_lib.epq_logits_adjust(*x, stream=st) for x, st in zip(args, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(p, w) for p, w in zip(pair, want))

@@ -348,3 +348,36 @@ def test_bad_pages_and_refusals_leave_no_error(epq_lib):
     with pytest.raises(ValueError):
         epq_lib.epq_attention_prompt(c.q.cpu(), c.c, 0, 4, c.scale)
     assert epq_lib.epq_device_error() == 0
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_two_at_once(epq_lib, D):
+    """Two calls on two streams with workspaces of their own, again and again while the other runs."""
+    cs = [Case(epq_lib, [700, 20], [300, 129], 8, 2, D, 64, seed=21), Case(epq_lib, [0, 900], [400, 7], 4, 4, D, 16, window=333, seed=22)]
+    want = [c.check() for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for c, st, o in zip(cs, streams, outs):
+            with torch.cuda.stream(st):
+                o.append(c.run())
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(x, w) for x in o)
+    assert epq_lib.epq_device_error() == 0
+
+
+def test_token_counts_out_of_range(epq_lib):
+    """Counts below 0 and above ntok are held to it; no counts are all tokens."""
+    c = Case(epq_lib, [10, 20, 30], [40, 40, 40], 4, 2, 128, 16, seed=23)
+    want = c.check()
+    run = lambda nt: epq_lib.epq_attention_prompt(c.q, c.c, 0, 4, c.scale, n_tok=nt)  # noqa: E731
+    assert torch.equal(run(None), want)
+    got = run(torch.tensor([2**31 - 1, -3, 41], dtype=torch.int32, device="cuda"))
+    assert torch.equal(got[[0, 2]], want[[0, 2]]) and not got[1].any()
+    assert epq_lib.epq_device_error() == 0
+
+
+def test_head_of_256_with_16_queries(epq_lib):
+    Case(epq_lib, [40, 333], [30, 77], 16, 1, 256, 32).check()

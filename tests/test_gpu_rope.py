@@ -301,3 +301,34 @@ def test_append_near_ties(epq_lib):
     epq_lib.epq_pages_append(x.cuda(), x.flip(1).contiguous().cuda(), c, 0)
     rows = c.pool[0, c.table[0, : n // 128].long(), 0].transpose(0, 1).reshape(2, n, 136).cpu().numpy()
     assert np.array_equal(rows[0], _rows(x[0].numpy())) and np.array_equal(rows[1], _rows(x[0].flip(0).numpy()))
+
+
+def test_host_tensors_are_refused(epq_lib):
+    """Where there is a GPU, a call whose tensors are all on the host does not reach it."""
+    with pytest.raises(ValueError):
+        epq_lib.RopeTable(64, 10, device="cpu")
+    t = epq_lib.RopeTable.over(torch.zeros(10, 32, 2))
+    c = epq_lib.PagedKVCache(1, 4, 2, 128, 1, 2, 16, "cpu")
+    k, n = torch.zeros(1, 3, 256), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: epq_lib.epq_rope(k, t, 2), lambda: epq_lib.epq_pages_append(k, k, c, 0), lambda: epq_lib.epq_pages_advance(c, n),
+                 lambda: epq_lib.epq_attention_prompt(k, c, 0, 2, 0.1), lambda: epq_lib.epq_logits_adjust(k)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_append_two_at_once_and_none(epq_lib):
+    """Two caches at the same time on two streams; a call in which no sequence has a row."""
+    x = torch.randn(2, 600, 512, device="cuda")
+    cs = [_cache(epq_lib, 1, 2, 128, 16, [5, 40], 600, 17) for _ in range(3)]
+    tab = epq_lib.RopeTable(128, 1000)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for c, st in zip(cs, streams):
+        epq_lib.epq_pages_append(x[..., :256], x[..., 256:], c, 0, rope=tab, stream=st)
+    torch.cuda.synchronize()
+    before = cs[2].pool.clone()
+    epq_lib.epq_pages_append(x[..., :256], x[..., 256:], cs[2], 0, rope=tab, n_tok=_i32([0, -4], "cuda"))
+    assert torch.equal(cs[2].pool, before)
+    epq_lib.epq_pages_append(x[..., :256], x[..., 256:], cs[2], 0, rope=tab, n_tok=_i32([600, 10000], "cuda"))
+    assert torch.equal(cs[0].pool, cs[1].pool) and torch.equal(cs[0].pool, cs[2].pool)
+    assert epq_lib.epq_device_error() == 0
