@@ -729,9 +729,10 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  * Operands are two fp16 parts each, sums float32: a score is off by some 2^-20
  * of scale * sum |q||k|, an output by some 2^-19 of sum w|v| (w the weights)
  * beside what its scores make of that; and there are floors: a weight is off by
- * up to 2^-39 of its row's largest, and a value whose factor is below 2^-21 of
- * the largest that its 32 columns have among the 128 positions around it (64
- * for heads of 256) by up to 2^-32 of that.  Two launches. */
+ * up to 2^-39 of its row's largest, and a value (a key) whose factor is below
+ * 2^-21 of the largest that its 32 columns (all columns) have among the 128
+ * positions around it, 64 for heads of 256, by up to 2^-32 of the element that
+ * would belong to that one.  Two launches. */
 epq_status epq_attention_prompt(const epq_pages *pages, int layer, const float *q, int n_heads, int ntok, float scale,
                                 const epq_attention_prompt_opts *opts, float *out, void *ws, size_t ws_bytes,
                                 epq_stream_t stream);

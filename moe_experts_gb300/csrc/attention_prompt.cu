@@ -45,8 +45,9 @@
 // Measured with 32 query and 8 key/value heads of 128 (both launches, from a
 // graph): 65 tokens over themselves 18.3 us, 4096 over themselves 346 us, 2048
 // behind 32768 positions 2.26 ms: 500 TFLOP/s of the formula's products, three
-// fp16 products for each, 0.79 of the measured bf16 rate.  Heads of 256 compute their scores once for each half of the columns
-// (registers and tensor memory hold 128 columns of sums): 250 TFLOP/s.
+// fp16 products for each, 0.79 of the measured bf16 rate.  Heads of 256 compute
+// their scores once for each half of the columns (registers and tensor memory
+// hold 128 columns of sums): 250 TFLOP/s.
 // A tile takes 4300 cycles, of which the tensor core's own 48 products are 70 %;
 // the thread that issues them waits 17 % of the time for operands or weights.
 // Beside them the shared memory is as busy (operands written 128 KB, read by the
@@ -70,15 +71,15 @@ constexpr int kRows = 128;     // rows of an item
 constexpr int kCols = 128;     // output columns of an item
 constexpr int kMaxCtas = 152;  // one per SM of a GB300
 constexpr int kMaxGroupPrompt = 16;
-constexpr int kExtra = 4;
+constexpr int kExtra = 4;      // (4096 tokens: 3 365 us, 4 347, 5 350; unequal prompts: 3 31.2, 4 30.9, 5 33.2)
 constexpr int kAhead = 4;  // tiles that the scan may be ahead of the output
 constexpr int kRaw = 2;    // tiles of keys, and of values, as the cache holds them
 constexpr int kJoinWarps = 8;
 constexpr int kPartLd = kCols + 4;
 
 // Warps: 0-3 weights, 4-7 output, 8-15 operands, 16 products, 17 copies, 18-19
-// scan.  Registers of each group of four warps: the launch has
-// 5 * 128 threads * 96, and 5 * 96 = 104 + 168 + 72 + 72 + 64.
+// scan.  Registers of each group of four warps: the launch has 5 * 128 threads *
+// 96, and 5 * 96 = 104 + 168 + 72 + 72 + 64.
 constexpr int kThreads = 640;
 constexpr int kRegsWeights = 104, kRegsOutput = 168, kRegsOperand = 72, kRegsRest = 64;
 constexpr int kRegsLaunch = 96;
@@ -157,10 +158,9 @@ struct Control {
 
 // The code of all roles together has to fit the SM's instruction cache (unrolled
 // further the warps waited for instructions half of the time, 5.0 ms where 2.3
-// are now): loops
-// are unrolled only as far as registers or latencies ask for, and what a wait
-// does when it gives up is out of line.  (No other call: a role's registers are
-// fewer than the launch's.)
+// are now): loops are unrolled only as far as registers or latencies ask for,
+// and what a wait does when it gives up is out of line.  (No other call: a role's
+// registers are fewer than the launch's.)
 __device__ __noinline__ void gave_up(unsigned *err, unsigned code, unsigned where) { record_error(err, code, where); }
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned *err, unsigned code, unsigned where = 0) {
