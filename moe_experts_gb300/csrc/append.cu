@@ -5,9 +5,10 @@
 //
 // over blocks b of 32 elements, x the value, or the key after its rotation.
 //
-// 8192 tokens of 8 heads of 128 take 21 us, 4.2 TB/s of the 71 MB read and 18 MB
-// written (0.62 of the copy rate): bound by the instructions of the quantization
-// (0.74 issued per cycle of a scheduler, some 125 for a row of 128 elements).
+// 8192 tokens of 8 heads of 128 take 20.6 us, 4.3 TB/s of the 71 MB read and 18 MB
+// written (0.64 of the copy rate): bound by the instructions of the quantization
+// (0.74 issued per cycle of a scheduler when a row of 128 elements took some 125 of
+// them; with the bound on a block's codes asked of each code it was 21.1 us).
 // With an IEEE division for each element it was 36 us, with every head's position,
 // page and angles worked out anew 33 us.  8 rows in a tree: 3.0 us, one chain of
 // length, page, angles, store.

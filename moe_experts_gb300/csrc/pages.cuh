@@ -117,10 +117,10 @@ __device__ __forceinline__ float over_127(float a) {
 // x times the factor's approximate reciprocal is off by 2^-23 + 2^-24 of it, and
 // the rounded quotient by 2^-24: 2^-15 in all at a code of 127.  Where the
 // product is further than 2^-14 from the middle between two codes, it has the
-// quotient's code, which adding 1.5 2^23 leaves in the low byte.  The others,
-// codes past 127 and NaN are divided.
+// quotient's code, which adding 1.5 2^23 leaves in the low byte.  The others, NaN,
+// and blocks whose factor was rounded so far down that codes pass 127, are divided.
 __device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
-  const float e[4] = {__fadd_rn(x.x, 0.0f), __fadd_rn(x.y, 0.0f), __fadd_rn(x.z, 0.0f), __fadd_rn(x.w, 0.0f)};
+  const float e[4] = {x.x, x.y, x.z, x.w};
   float a = fmaxf(fmaxf(fabsf(e[0]), fabsf(e[1])), fmaxf(fabsf(e[2]), fabsf(e[3])));
 #pragma unroll
   for (int w = 1; w < 8; w <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, w));
@@ -130,12 +130,12 @@ __device__ __forceinline__ uint32_t quantize4(float4 x, __half *factor) {
   float inverse;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(d));
   uint32_t code[4];
-  bool sure = d != 0.0f;
+  bool sure = d != 0.0f && __fmul_rn(a, inverse) < 127.25f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float t = __fmul_rn(e[j], inverse), r = __fadd_rn(t, 12582912.0f);
     code[j] = __float_as_uint(r);
-    sure = sure && fabsf(__fsub_rn(t, __fsub_rn(r, 12582912.0f))) < 0.5f - 0x1p-14f && fabsf(t) < 127.25f;
+    sure = sure && fabsf(__fsub_rn(t, __fsub_rn(r, 12582912.0f))) < 0.5f - 0x1p-14f;
   }
   if (!sure) {
 #pragma unroll
