@@ -716,8 +716,9 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  *   length + i - window) of the cache, which holds the tokens' own rows
  *   (epq_pages_append) behind the committed ones; out_i = sum_j softmax(s_i)_j
  *   v_j, 0 for a token that sees no position.  Query head h reads key/value
- *   head h / (n_heads / n_kv_heads).  A position without a page is left out and
- *   recorded (epq_device_error code 5).
+ *   head h / (n_heads / n_kv_heads).  Such a position without a page is left out
+ *   and recorded (epq_device_error code 5); pages below every token's window need
+ *   not be there.
  *   out  float32 [n_seq][ntok][n_heads][head_dim]
  *   ws, ws_bytes  device scratch of epq_attention_prompt_workspace_bytes(),
  *        16-byte aligned, needs no initialisation; calls that share it must be

@@ -132,7 +132,7 @@ struct Item {
   int s, h, col, rt;   // sequence, head, first output column, row tile
   int len, rows;       // the sequence's committed length and rows
   int t0, t1;          // tokens of the row tile
-  int end;             // positions that any of its rows sees
+  int begin, end;      // positions that any of its rows sees
   int p0, tiles;       // first position and tiles of the CTA's part of it; no tiles: there is no further item
   int before;          // tiles of the items before
   int slot;            // where a part of an item goes, -1: the item is whole
@@ -185,7 +185,7 @@ __device__ __forceinline__ int row_tiles(const PromptParams &p, int n) { return 
 
 // Row tile rt of a sequence: its tokens, and the positions that any of them sees.
 struct Span {
-  int t0, t1, end, first, tiles;  // first: the first tile's index; tiles: how many
+  int t0, t1, begin, end, first, tiles;  // first: the first tile's index; tiles: how many
 };
 
 template <int kD>
@@ -195,8 +195,8 @@ __device__ __forceinline__ Span span_of(const PromptParams &p, int len, int n, i
   x.t0 = rt * kRows / p.group;
   x.t1 = (min((rt + 1) * kRows, n * p.group) - 1) / p.group;
   x.end = len + x.t1 + 1;
-  const int begin = p.window ? max(0, len + x.t0 - p.window + 1) : 0;
-  x.first = begin / kPos;
+  x.begin = p.window ? max(0, len + x.t0 - p.window + 1) : 0;
+  x.first = x.begin / kPos;
   x.tiles = (x.end + kPos - 1) / kPos - x.first;
   return x;
 }
@@ -316,8 +316,8 @@ struct Walk {
       const long long take = min(left, static_cast<long long>(span.tiles + kExtra - tile));
       const int a = tile, b = min(tile + static_cast<int>(take), span.tiles);
       if (a < b) {
-        x = {s, y / Shape<kD>::kSplit, y % Shape<kD>::kSplit * kCols, rt, len, n * p.group, span.t0, span.t1, span.end,
-             (span.first + a) * Shape<kD>::kPos, b - a, before, -1};
+        x = {s, y / Shape<kD>::kSplit, y % Shape<kD>::kSplit * kCols, rt, len, n * p.group, span.t0, span.t1, span.begin,
+             span.end, (span.first + a) * Shape<kD>::kPos, b - a, before, -1};
         if (a > 0 || b < span.tiles) {
           x.slot = begins ? 0 : 1;
           if ((threadIdx.x & 31) == 0) p.notes[2 * blockIdx.x + x.slot] = Part{s, rt, y, a, b, span.tiles, {0, 0}};
@@ -380,7 +380,8 @@ __device__ __forceinline__ int half_exponent(int bits) {
 
 // ------------------------------------------------------------------ copies
 // One warp.  A tile's rows lie in runs, each within a page; lane r brings run r
-// of the keys and of the values.
+// of the keys and of the values, where any of its positions is seen (a page that
+// lies below the window of all rows need not be there).
 template <int kD>
 __device__ void copies_role(const PromptParams &p, Control &c, uint8_t *smem) {
   using S = Shape<kD>;
@@ -409,7 +410,7 @@ __device__ void copies_role(const PromptParams &p, Control &c, uint8_t *smem) {
     for (int k = 0; ok && k < x.tiles; ++k) {
       const int g = x.before + k, stage = g % kRaw;
       const int pos = x.p0 + k * S::kPos + lane * run;
-      const bool used = lane * run < S::kPos && pos < x.end;
+      const bool used = lane * run < S::kPos && pos < x.end && pos + run > x.begin;
       const int page = used ? seq_page(p.v, x.s, pos / p.v.P) : -1;
       if (used && page < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(x.s));
       const uint32_t all = __popc(__ballot_sync(0xffffffffu, page >= 0)) * bytes;
@@ -472,7 +473,7 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int pos = p0 + t + 64 * m;
-        const int page = pos < it.end ? seq_page(p.v, it.s, pos / p.v.P) : -1;
+        const int page = pos >= it.begin && pos < it.end ? seq_page(p.v, it.s, pos / p.v.P) : -1;
         read[m] = page >= 0;
         const uint8_t *row = page_row(p.v, p.layer, max(page, 0), it.h, 0, pos % p.v.P);
 #pragma unroll
@@ -495,7 +496,8 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
           kmax = larger2(larger2(kmax, kf[m][x].x), kf[m][x].y);
           if (kWords == 1 || x == split) vmax[0] = larger2(vmax[0], vf[m][x].x), vmax[1] = larger2(vmax[1], vf[m][x].y);
         }
-        any |= p0 + t + 64 * m < it.end && (!read[m] || bad[m]);
+        const int pos = p0 + t + 64 * m;
+        any |= bad[m] || (!read[m] && pos >= it.begin && pos < it.end);
       }
       if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) {
         asm volatile("bar.arrive 1, 64;" ::: "memory");  // the other warp may have gone on to the barrier below
