@@ -132,8 +132,8 @@ struct Item {
   int s, h, col, rt;   // sequence, head, first output column, row tile
   int len, rows;       // the sequence's committed length and rows
   int t0, t1;          // tokens of the row tile
-  int begin, end;      // positions that any of its rows sees
-  int p0, tiles;       // first position and tiles of the CTA's part of it; no tiles: there is no further item
+  int end;             // positions that any of its rows sees
+  int from, tiles;     // first position that any of them sees, and tiles, of the CTA's part of it; no tiles: there is no further item
   int before;          // tiles of the items before
   int slot;            // where a part of an item goes, -1: the item is whole
 };
@@ -316,8 +316,8 @@ struct Walk {
       const long long take = min(left, static_cast<long long>(span.tiles + kExtra - tile));
       const int a = tile, b = min(tile + static_cast<int>(take), span.tiles);
       if (a < b) {
-        x = {s, y / Shape<kD>::kSplit, y % Shape<kD>::kSplit * kCols, rt, len, n * p.group, span.t0, span.t1, span.begin,
-             span.end, (span.first + a) * Shape<kD>::kPos, b - a, before, -1};
+        x = {s, y / Shape<kD>::kSplit, y % Shape<kD>::kSplit * kCols, rt, len, n * p.group, span.t0, span.t1, span.end,
+             max(span.begin, (span.first + a) * Shape<kD>::kPos), b - a, before, -1};
         if (a > 0 || b < span.tiles) {
           x.slot = begins ? 0 : 1;
           if ((threadIdx.x & 31) == 0) p.notes[2 * blockIdx.x + x.slot] = Part{s, rt, y, a, b, span.tiles, {0, 0}};
@@ -409,8 +409,8 @@ __device__ void copies_role(const PromptParams &p, Control &c, uint8_t *smem) {
     tell();
     for (int k = 0; ok && k < x.tiles; ++k) {
       const int g = x.before + k, stage = g % kRaw;
-      const int pos = x.p0 + k * S::kPos + lane * run;
-      const bool used = lane * run < S::kPos && pos < x.end && pos + run > x.begin;
+      const int pos = (x.from & -S::kPos) + k * S::kPos + lane * run;
+      const bool used = lane * run < S::kPos && pos < x.end && pos + run > x.from;
       const int page = used ? seq_page(p.v, x.s, pos / p.v.P) : -1;
       if (used && page < 0) record_error(p.err, DEVERR_NO_PAGE, static_cast<unsigned>(x.s));
       const uint32_t all = __popc(__ballot_sync(0xffffffffu, page >= 0)) * bytes;
@@ -466,14 +466,14 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
     const int split = it.col / kCols;
 #pragma unroll 1
     for (int k = 0; k < it.tiles; ++k) {
-      const int g = it.before + k, p0 = it.p0 + k * kPos;
+      const int g = it.before + k, p0 = (it.from & -kPos) + k * kPos;
       Entry &e = c.entry[g % kAhead];
       uint2 kf[kMine][kWords], vf[kMine][kWords];
       bool read[kMine];
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int pos = p0 + t + 64 * m;
-        const int page = pos >= it.begin && pos < it.end ? seq_page(p.v, it.s, pos / p.v.P) : -1;
+        const int page = pos >= it.from && pos < it.end ? seq_page(p.v, it.s, pos / p.v.P) : -1;
         read[m] = page >= 0;
         const uint8_t *row = page_row(p.v, p.layer, max(page, 0), it.h, 0, pos % p.v.P);
 #pragma unroll
@@ -497,7 +497,7 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
           if (kWords == 1 || x == split) vmax[0] = larger2(vmax[0], vf[m][x].x), vmax[1] = larger2(vmax[1], vf[m][x].y);
         }
         const int pos = p0 + t + 64 * m;
-        any |= bad[m] || (!read[m] && pos >= it.begin && pos < it.end);
+        any |= bad[m] || (!read[m] && pos >= it.from && pos < it.end);
       }
       if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) {
         asm volatile("bar.arrive 1, 64;" ::: "memory");  // the other warp may have gone on to the barrier below
@@ -801,7 +801,7 @@ __device__ void weights_role(const PromptParams &p, Control &c) {
     float top = -INFINITY, off = 0.0f, den = 0.0f;  // weights are exp2(x - off): 2^15 at the maximum
 #pragma unroll 1
     for (int k = 0; k < it.tiles; ++k) {
-      const int g = it.before + k, p0 = it.p0 + k * kPos;
+      const int g = it.before + k, p0 = (it.from & -kPos) + k * kPos;
       const uint32_t s = tm + S::kS + (g & 1) * kPos;
       if (!wait_warp(&c.scan_full[g % kAhead], (g / kAhead) & 1, p.err, DEVERR_FULL_WAIT, g)) return;
       const Entry &e = c.entry[g % kAhead];
