@@ -454,19 +454,25 @@ __device__ __forceinline__ uint32_t larger2(uint32_t a, uint32_t b) {
   return __vmaxu2(a, b);
 }
 
-// Two warps, kPos / 64 positions a lane.
+// Two warps, kPos / 64 positions a lane.  They meet for each tile.  One that gives
+// up says so where its note of the next tile would be, and arrives without
+// waiting: the other one, which meets it there, leaves too, so that neither waits
+// for a warp that has left.
+constexpr uint32_t kGone = 2;
 template <int kD>
 __device__ void scan_role(const PromptParams &p, Control &c) {
   using S = Shape<kD>;
   constexpr int kPos = S::kPos, kWords = kD / 128, kMine = kPos / 64;
   const int t = threadIdx.x - 18 * 32, lane = t & 31;
+  int g = 0;  // the next tile
   Item it;
+  it.tiles = 1;
   for (int n = 0; item_at(p, c, n, it); ++n) {
     item_done(c, n);
     const int split = it.col / kCols;
 #pragma unroll 1
-    for (int k = 0; k < it.tiles; ++k) {
-      const int g = it.before + k, p0 = (it.from & -kPos) + k * kPos;
+    for (int k = 0; k < it.tiles; ++k, ++g) {
+      const int p0 = (it.from & -kPos) + k * kPos;
       Entry &e = c.entry[g % kAhead];
       uint2 kf[kMine][kWords], vf[kMine][kWords];
       bool read[kMine];
@@ -499,10 +505,7 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
         const int pos = p0 + t + 64 * m;
         any |= bad[m] || (!read[m] && pos >= it.from && pos < it.end);
       }
-      if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) {
-        asm volatile("bar.arrive 1, 64;" ::: "memory");  // the other warp may have gone on to the barrier below
-        return;
-      }
+      if (g >= kAhead && !wait_warp(&c.entry_free[g % kAhead], (g / kAhead - 1) & 1, p.err, DEVERR_EMPTY_WAIT, g)) goto gone;
       // the largest of both warps: of the keys, and of the values by block
       uint32_t most[5];
       most[4] = max(kmax & 0xffffu, kmax >> 16);
@@ -519,6 +522,7 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
       }
       named_sync(1, 64);
       const uint32_t *other = c.scan[g & 1][1 - (t >> 5)];
+      if (other[5] == kGone) return;
       float mul[5];
 #pragma unroll
       for (int i = 0; i < 5; ++i) mul[i] = exp2i(7 - half_exponent(max(most[i], other[i])));
@@ -542,6 +546,12 @@ __device__ void scan_role(const PromptParams &p, Control &c) {
       if (lane == 0) mbar_arrive(&c.scan_full[g % kAhead]);
     }
   }
+  if (it.tiles == 0) return;  // no further item, for both; else the item's wait gave up
+gone:
+  if (lane == 0) c.scan[g & 1][t >> 5][5] = kGone;
+  __threadfence_block();
+  __syncwarp();
+  asm volatile("bar.arrive 1, 64;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ operands
