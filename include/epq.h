@@ -683,15 +683,18 @@ typedef struct {
  * quantized to Q8_0 (the packer's arithmetic) and stored in one layer at the
  * positions length + i of their sequence; length itself stays (epq_pages_advance
  * ends the step once every layer has its rows).  The positions must have been
- * reserved; a row without a page is not stored and recorded (epq_device_error
- * code 5).  A key whose position has no angle is stored with factors of NaN:
- * what attends to it is NaN.  ntok >= 1, n_seq * ntok * n_kv_heads < 2^30.  One
- * launch. */
+ * reserved (a sequence that epq_pages_reserve refused has to be left out with
+ * n_tok 0, here and in the step's other calls: its last page may be shared, and
+ * the rows would be the others' too); a row without a page is not stored and
+ * recorded (epq_device_error code 5).  A key whose position has no angle is
+ * stored with factors of NaN: what attends to it is NaN.  ntok >= 1, n_seq *
+ * ntok * n_kv_heads < 2^30.  One launch. */
 epq_status epq_pages_append(const epq_pages *pages, int layer, const float *k, const float *v, int ntok,
                             const epq_append_opts *opts, epq_stream_t stream);
 
 /* epq_pages_advance: commits appended rows, length = min(length + max(n, 0),
- * max_pages * page_size); n int32 [n_seq]. */
+ * max_pages * page_size); n int32 [n_seq], 0 for a sequence whose reservation was
+ * refused (its positions have no pages). */
 epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n, epq_stream_t stream);
 
 /* Options of epq_attention_prompt (all-zero: contiguous q, ntok tokens in every

@@ -786,7 +786,8 @@ def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, laye
                      position: torch.Tensor | None = None, mask: torch.Tensor | None = None,
                      n_tok: torch.Tensor | None = None, stream=None) -> None:
     """k, v float32 [n_seq, ntok, n_kv*D] (views of one wider buffer are read in place): the rows are stored behind
-    the committed positions of one layer, the keys turned by `rope` (positions as in epq_rope, start = the lengths)."""
+    the committed positions of one layer, the keys turned by `rope` (positions as in epq_rope, start = the lengths).
+    n_tok is 0 for a sequence whose reservation was refused: its last page may be shared."""
     if k.dim() != 3:
         raise ValueError("k must be [n_seq, ntok, n_kv * head_dim]")
     ntok, nseq, at = k.shape[1], cache.n_seq, cache._at
@@ -807,7 +808,7 @@ def epq_pages_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache, laye
 
 
 def epq_pages_advance(cache: PagedKVCache, n: torch.Tensor, stream=None) -> None:
-    """Commit n (int32 [n_seq]) appended positions of every sequence."""
+    """Commit n (int32 [n_seq]; 0 where the reservation was refused) appended positions of every sequence."""
     at = cache._at
     st = _lib.epq_pages_advance(cache._ref, _need(n, "n", torch.int32, cache._per_seq, at), _launch_on(stream, at))
     if st:
