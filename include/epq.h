@@ -731,8 +731,9 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  * row with a factor that is not finite makes the outputs of the tokens that
  * attend to it NaN, in the heads that read it, and changes no other output.
  * Operands are two fp16 parts each, sums float32: a score is off by some 2^-20
- * of scale * sum |q||k|, an output by some 2^-19 of sum w|v| (w the weights)
- * beside what its scores make of that; and there are floors: a weight is off by
+ * of scale * sum |q||k| (at most (32 + head_dim/4) 2^-24), an output by some
+ * 2^-19 of sum w|v| (w the weights; at most (128 + T head_dim/2048) 2^-24 over T
+ * positions) beside what its scores make of that; and there are floors: a weight is off by
  * up to 2^-39 of its row's largest, and a value (a key) whose factor is below
  * 2^-21 of the largest that its 32 columns (all columns) have among the 128
  * positions around it, 64 for heads of 256, by up to 2^-32 of the element that
