@@ -630,7 +630,10 @@ epq_status epq_rope_table(const double *freq, int rot_dim, double magnitude, int
 /* A rotation: elements first .. first + rot_dim - 1 of every head, pairs
  * (first + j, first + rot_dim/2 + j), or (first + 2j, first + 2j + 1) when
  * `interleaved` is nonzero.  A token whose position is outside 0..n_pos-1 is
- * recorded (epq_device_error code 6) and its rotated elements become NaN. */
+ * recorded (epq_device_error code 6) and its rotated elements become NaN.  (Of a
+ * key that is quantized after that, by epq_attention_tree or epq_pages_append,
+ * only the blocks that are rotated as a whole get a factor of NaN: the record is
+ * what tells of the others.) */
 typedef struct {
   const float *table;
   int64_t n_pos;
@@ -687,8 +690,11 @@ typedef struct {
  * n_tok 0, here and in the step's other calls: its last page may be shared, and
  * the rows would be the others' too); a row without a page is not stored and
  * recorded (epq_device_error code 5).  A key whose position has no angle is
- * stored with factors of NaN: what attends to it is NaN.  ntok >= 1, n_seq *
- * ntok * n_kv_heads < 2^30.  One launch. */
+ * stored with factors of NaN: what attends to it is NaN.  Elements that are not
+ * finite are quantized as epq_quantize does: an infinity or a block of nothing
+ * but NaN makes its block's factor infinite or NaN, a NaN among other numbers is
+ * code -127 under the factor of the others.  ntok >= 1, n_seq * ntok * n_kv_heads
+ * < 2^30.  One launch. */
 epq_status epq_pages_append(const epq_pages *pages, int layer, const float *k, const float *v, int ntok,
                             const epq_append_opts *opts, epq_stream_t stream);
 
@@ -733,9 +739,9 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  * Operands are two fp16 parts each, sums float32: a score is off by some 2^-20
  * of scale * sum |q||k| (at most (32 + head_dim/4) 2^-24), an output by some
  * 2^-19 of sum w|v| (w the weights; at most (128 + T head_dim/2048) 2^-24 over T
- * positions) beside what its scores make of that; and there are floors: a weight is off by
- * up to 2^-39 of its row's largest, and a value (a key) whose factor is below
- * 2^-21 of the largest that its 32 columns (all columns) have among the 128
+ * positions) beside what its scores make of that; and there are floors: a weight
+ * is off by up to 2^-39 of its row's largest, and a value (a key) whose factor is
+ * below 2^-21 of the largest that its 32 columns (all columns) have among the 128
  * positions around it, 64 for heads of 256, by up to 2^-32 of the element that
  * would belong to that one.  Two launches. */
 epq_status epq_attention_prompt(const epq_pages *pages, int layer, const float *q, int n_heads, int ntok, float scale,
