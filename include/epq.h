@@ -708,6 +708,8 @@ epq_status epq_pages_advance(const epq_pages *pages, const int32_t *n, epq_strea
  *   n_tok    NULL or int32 [n_seq]: tokens of each sequence (0..ntok; the
  *            others' output is 0)
  *   window   0, or how many positions a token attends to, its own included
+ *            (epq_attention_tree has no window: a model that has one goes on
+ *            behind its prompt with this call, its tokens a chain)
  *   q_ld, q_seq_ld  floats between tokens / sequences of q (0 = contiguous);
  *            multiples of 4 */
 typedef struct {

@@ -272,9 +272,12 @@ class TreeDecoder:
 
     def prompt(self, x, stream=None):
         """x [n, H], any n >= 1 (the tokens' embeddings): their rows are appended
-        and committed -> logits [1, vocab] behind the last one.  The weights are
-        read once for every 8 tokens.  status is nonzero when the cache had no
-        room: it stays as it is then, and the logits mean nothing."""
+        and committed -> logits [1, vocab] behind the last one (logits[None] is
+        what epq_logits_adjust and epq_verify_tree take).  The weights are read
+        once for every 8 tokens, which is most of a prompt's time; its attention
+        has no window, as the steps behind it have none.  status is nonzero when
+        the cache had no room: it stays as it is then, and the logits mean
+        nothing."""
         c, f, H, nq, nkv, cache = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows, self.cache
         n, new = x.shape[0], L._allocator(stream)
         f32, i32 = dict(dtype=torch.float32, device=x.device), dict(dtype=torch.int32, device=x.device)
