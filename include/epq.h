@@ -730,7 +730,8 @@ size_t epq_attention_prompt_workspace_bytes(const epq_pages *pages, int n_heads,
  *   head h / (n_heads / n_kv_heads).  Such a position without a page is left out
  *   and recorded (epq_device_error code 5); pages below every token's window need
  *   not be there.
- *   out  float32 [n_seq][ntok][n_heads][head_dim]
+ *   out  float32 [n_seq][ntok][n_heads][head_dim]; may equal a contiguous q for
+ *        heads of 128, else they do not overlap
  *   ws, ws_bytes  device scratch of epq_attention_prompt_workspace_bytes(),
  *        16-byte aligned, needs no initialisation; calls that share it must be
  *        ordered on one stream.

@@ -1115,6 +1115,10 @@ extern "C" epq_status epq_attention_prompt(const epq_pages *pages, int layer, co
   if (!aligned16(q) || !aligned16(out) || p.q_ld % 4 || p.q_seq_ld % 4 || !aligned_to(4, o.n_tok)) return EPQ_ERR_ALIGN;
   if (!ws || ws_bytes < epq_attention_prompt_workspace_bytes(pages, n_heads, ntok)) return EPQ_ERR_WORKSPACE;
   if (!aligned16(ws)) return EPQ_ERR_ALIGN;
+  // in place: a row's queries are read before its output is written, but both
+  // halves of the output of heads of 256 are items that read the whole row
+  const int64_t width = static_cast<int64_t>(n_heads) * p.v.D;
+  if (q == out && (p.v.D != kCols || p.q_ld != width || p.q_seq_ld != ntok * width)) return EPQ_ERR_ARG;
   p.q = q, p.n_tok = o.n_tok, p.layer = layer, p.n_heads = n_heads, p.group = n_heads / p.v.n_kv, p.ntok = ntok;
   p.window = o.window, p.scale = scale, p.out = out;
   p.notes = static_cast<Part *>(ws);
