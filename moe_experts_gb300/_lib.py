@@ -708,9 +708,14 @@ def epq_verify_tree(logits: torch.Tensor, tokens: torch.Tensor, parent: torch.Te
 
 # ------------------------------------------------------------------ rotary positions
 def epq_rope_frequencies(rot_dim: int, base: float = 10000.0, kind: int = EPQ_ROPE_PLAIN, factor: float = 1.0,
-                         context: float = 1.0, low: float | None = None, high: float | None = None):
+                         context: float | None = None, low: float | None = None, high: float | None = None):
     """(float64 [rot_dim / 2] on the host, magnitude): the angles per position and what the cosines and sines are
-    multiplied by; low, high: turns over `context` (None: the kind's usual ones)."""
+    multiplied by; context: the trained one, which EPQ_ROPE_PARTS and EPQ_ROPE_BANDS ask for; low, high: turns over it
+    (None: the kind's usual ones)."""
+    if context is None:
+        if kind in (EPQ_ROPE_PARTS, EPQ_ROPE_BANDS):
+            raise ValueError("this kind of scaling needs the context that the frequencies were trained for")
+        context = 1.0
     usual = (1.0, 4.0) if kind == EPQ_ROPE_BANDS else (1.0, 32.0)
     sc = RopeScaling(kind, factor, context, usual[0] if low is None else low, usual[1] if high is None else high)
     freq, mag = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64), ctypes.c_double()
