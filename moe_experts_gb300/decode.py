@@ -271,7 +271,7 @@ class TreeDecoder:
             torch.mul(extra, self.status == 0, out=n_tok)
 
     def prompt(self, x, stream=None):
-        """x [n, H], any n >= 1 (the tokens' embeddings): their rows are appended
+        """x float32 [n, H], contiguous, any n >= 1 (the tokens' embeddings): their rows are appended
         and committed -> logits [1, vocab] behind the last one (logits[None] is
         what epq_logits_adjust and epq_verify_tree take).  The weights are read
         once for every 8 tokens, which is most of a prompt's time; its attention
@@ -280,6 +280,9 @@ class TreeDecoder:
         nothing."""
         c, f, H, nq, nkv, cache = self.cfg, self.fmt, self.cfg.hidden, self.cfg.q_rows, self.cfg.kv_rows, self.cache
         n, new = x.shape[0], L._allocator(stream)
+        if n < 1:
+            raise ValueError("a prompt has at least one token")
+        L._need(x, "x", torch.float32, (n, H), cache._at)
         f32, i32 = dict(dtype=torch.float32, device=x.device), dict(dtype=torch.int32, device=x.device)
         qkv, attn = new((1, n, nq + 2 * nkv), **f32), new((1, n, nq), **f32)
         h, m, logits = new((n, H), **f32), new((n, c.inter), **f32), new((1, c.vocab), **f32)
