@@ -43,9 +43,9 @@
 // output), and a second launch joins the parts.
 //
 // Measured with 32 query and 8 key/value heads of 128 (both launches, from a
-// graph): 65 tokens over themselves 18.3 us, 4096 over themselves 346 us, 2048
-// behind 32768 positions 2.26 ms: 500 TFLOP/s of the formula's products, three
-// fp16 products for each, 0.79 of the measured bf16 rate.  Heads of 256 compute
+// graph): 65 tokens over themselves 17.9 us, 4096 over themselves 350 us, 2048
+// behind 32768 positions 2.28 ms: 500 TFLOP/s of the formula's products, three
+// fp16 products for each, 0.77 of the measured bf16 rate.  Heads of 256 compute
 // their scores once for each half of the columns (registers and tensor memory
 // hold 128 columns of sums): 250 TFLOP/s.
 // A tile takes 4300 cycles, of which the tensor core's own 48 products are 70 %;
